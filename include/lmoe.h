@@ -234,6 +234,112 @@ const char *lmoe_status_string(lmoe_status s);
 lmoe_status lmoe_forward_noalloc(const lmoe_config *cfg, const lmoe_weights *w,
                                  const uint16_t *x, int32_t T, uint16_t *y, void *stream);
 
+/* ---- operators around the layer -------------------------------------------
+ * Each is one call on device arrays, without a handle; the conventions at the
+ * top of this file hold (`stream` must belong to the current device; a count
+ * of 0 tokens or rows is a no-op).  Arrays are typed by an lmoe_dtype where
+ * several types are taken, and need their elements' natural alignment only
+ * (16-byte aligned arrays with widths and strides that are multiples of 8 run
+ * on wide loads).  Outputs must not overlap inputs or each other. */
+typedef enum { LMOE_F32 = 0, LMOE_BF16 = 1 } lmoe_dtype;
+
+/* Routing from given logits (page "Nemotron 3 Ultra 架构深度拆解报告", CH5
+ * §5.5 and §5.6 Steps 2-4, with the choices other sparse layers make):
+ *   s = sigmoid(l) or softmax(l);  b = s + bias (when one is given)
+ *   groups (n_group > 1): a group's score is the sum of its group_score (1 or
+ *     2) largest b; the topk_group best groups stay, equal ones: lower index
+ *   the top_k experts of the largest b (without a bias: the largest l, which
+ *     is the same order) that stay, equal ones: lower id
+ *   w = scale s, or scale s / (sum of the selected s + 1e-20) (renormalise)
+ * b and the group scores are compared by their values in 64 bits.  A logit of
+ * -inf or NaN is an expert that is not available: its score is 0, its b is
+ * -inf, and it is selected (with weight 0) only where fewer than top_k
+ * others are; +inf counts as the largest finite float. */
+typedef enum { LMOE_SCORE_SIGMOID = 0, LMOE_SCORE_SOFTMAX = 1 } lmoe_score;
+typedef struct {
+  int32_t n_experts;   /* E: 1..1024, any number */
+  int32_t top_k;       /* K: 1..min(64, topk_group * E / n_group) */
+  int32_t score;       /* lmoe_score */
+  int32_t n_group;     /* divides E; at most 64 */
+  int32_t topk_group;  /* 1..n_group */
+  int32_t group_score; /* 1 or 2 (2 needs groups of >= 2 when n_group > 1) */
+  int32_t renormalise; /* 0 or 1 */
+  float scale;         /* finite */
+} lmoe_router;
+
+/* logits: [T, E] of `logits_type`, rows `logits_stride` (>= E) elements
+ * apart; bias: fp32 [E], finite, or NULL.  Writes topk_idx [T, K] (ascending
+ * ids) and topk_w [T, K]. */
+lmoe_status lmoe_route_logits(const lmoe_router *router, const void *logits, int32_t logits_type,
+                              int64_t logits_stride, const float *bias, int32_t T,
+                              int32_t *topk_idx, float *topk_w, void *stream);
+
+/* The gradient of topk_w in the logits, the selection held fixed: from dw
+ * [T, K] (the gradient of topk_w) and the forward's logits and topk_idx,
+ * writes dlogits [T, E] (dense, of logits_type; 0 where the logit is not
+ * available).  Ids outside [0, E) are ignored, equal ids of a token add up. */
+lmoe_status lmoe_route_logits_backward(const lmoe_router *router, const void *logits,
+                                       int32_t logits_type, int64_t logits_stride,
+                                       const int32_t *topk_idx, const float *dw, int32_t T,
+                                       void *dlogits, void *stream);
+
+/* The norms around a block with its gate and residual scale, per token:
+ *   n     = post * y / sqrt(mean(y^2) + eps)    (n = y without post_weight)
+ *   h_out = res_scale * h + gate * n
+ *   x     = pre * h_out / sqrt(mean(h_out^2) + eps)    (if x is wanted)
+ * h is the residual stream before the block, y the block's output (NULL: 0,
+ * the norm ahead of a first block), x the next block's input.  h_out and x
+ * round once from fp32 values (x is computed from the unrounded h_out).
+ * Values and their squares' means must be finite. */
+typedef enum {
+  LMOE_GATE_NONE = 0,    /* 1 */
+  LMOE_GATE_CHANNEL = 1, /* [D] */
+  LMOE_GATE_TOKEN = 2,   /* [T] */
+  LMOE_GATE_FULL = 3     /* [T, D], dense */
+} lmoe_gate;
+typedef struct {
+  const void *h;           /* [T, D], rows h_stride elements apart */
+  const void *y;           /* [T, D], rows y_stride elements apart, or NULL */
+  int64_t h_stride, y_stride;
+  const void *pre_weight;  /* [D] or NULL (1) */
+  const void *post_weight; /* [D] or NULL (y is not normalised; NULL if y is) */
+  const void *res_scale;   /* [D] or NULL (1) */
+  const void *gate;        /* by gate_kind; NULL if LMOE_GATE_NONE */
+  int32_t gate_kind;       /* lmoe_gate (LMOE_GATE_NONE if y is NULL) */
+  int32_t h_type, y_type;  /* lmoe_dtype: of h, h_out and their gradients; of y, x and theirs */
+  int32_t pre_type, post_type, res_scale_type, gate_type; /* lmoe_dtype */
+  int32_t T, D;            /* D: 1..16384 */
+  float eps;               /* finite, > 0 */
+} lmoe_block_norm_args;
+
+/* h_out [T, D] (h_type), x [T, D] (y_type) or NULL, stats fp32 [T, 2] (the
+ * two reciprocal roots, what the backward needs) or NULL; all dense. */
+lmoe_status lmoe_block_norm(const lmoe_block_norm_args *a, void *h_out, void *x, float *stats,
+                            void *stream);
+
+/* Gradients, dense, each in the type of what it belongs to; NULL: not wanted
+ * (dy, dpost_weight, dres_scale, dgate must be NULL where their input is).
+ * Column sums are added in a fixed order: the same bits every time. */
+typedef struct {
+  void *dh, *dy;
+  void *dpre_weight, *dpost_weight, *dres_scale, *dgate;
+} lmoe_block_norm_grads;
+
+/* Bytes of workspace of lmoe_block_norm_backward (partial column sums of the
+ * [D] gradients; 0 if none is wanted, or for arguments it refuses).  Pure
+ * host function. */
+size_t lmoe_block_norm_workspace_size(const lmoe_block_norm_args *a,
+                                      const lmoe_block_norm_grads *g);
+
+/* From the forward's arguments and stats, dh_out [T, D] (h_type) and dx
+ * [T, D] (y_type), either may be NULL (0), the gradients in g.  workspace:
+ * 16-byte aligned device memory of the size above; calls that may overlap
+ * need one each.  T = 0 writes zeros to the [D] gradients. */
+lmoe_status lmoe_block_norm_backward(const lmoe_block_norm_args *a, const float *stats,
+                                     const void *dh_out, const void *dx,
+                                     const lmoe_block_norm_grads *g, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 /* ---- per-kernel timing (HIP events on the forward's stream) ------------ */
 
 /* Number of timed stages of lmoe_forward and the name of stage i.  Stages

@@ -1,0 +1,171 @@
+"""Float64 oracle of the operators around the layer (test infrastructure).
+
+Written from the formulas in ``include/lmoe.h`` with explicit loops over
+tokens where that is the plainest form; shares no code with the library.
+Inputs are float arrays holding the exact values the kernels read.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+E4M3_MAX = 448.0
+
+
+def _clean(l):
+    l = np.asarray(l, np.float64).copy()
+    l[np.isnan(l)] = -np.inf
+    return np.minimum(l, np.float64(np.finfo(np.float32).max))
+
+
+def route_scores(l, softmax: bool):
+    """Scores [T, E] of cleaned logits; 0 where the logit is -inf."""
+    l = _clean(l)
+    s = np.zeros_like(l)
+    for t in range(l.shape[0]):
+        on = l[t] > -np.inf
+        if not on.any():
+            continue
+        v = l[t][on]
+        with np.errstate(over="ignore"):
+            if softmax:
+                e = np.exp(v - v.max())
+                s[t][on] = e / e.sum()
+            else:
+                s[t][on] = 1.0 / (1.0 + np.exp(-v))
+    return s
+
+
+def route(l, bias, K, softmax=False, n_group=1, topk_group=1, group_score=2, renorm=True,
+          scale=1.0):
+    """(idx [T, K] ascending, w [T, K], gap [T]): gap is the distance, in
+    biased score (or logit, without a bias), at the border that decided the
+    selection; inf where nothing was left out."""
+    s = route_scores(l, softmax)
+    l = _clean(l)
+    T, E = l.shape
+    on = l > -np.inf
+    b = np.where(on, s + (0.0 if bias is None else np.asarray(bias, np.float64)), -np.inf)
+    order = b if bias is not None else l
+    idx = np.zeros((T, K), np.int64)
+    w = np.zeros((T, K))
+    G = E // n_group
+    for t in range(T):
+        allowed = list(range(E))
+        if n_group > 1:
+            gs = [np.sort(b[t, g * G:(g + 1) * G])[::-1][:group_score].sum()
+                  for g in range(n_group)]
+            kept = sorted(range(n_group), key=lambda g: (-gs[g], g))[:topk_group]
+            allowed = [e for g in sorted(kept) for e in range(g * G, (g + 1) * G)]
+        chosen = sorted(sorted(allowed, key=lambda e: (-order[t, e], e))[:K])
+        idx[t] = chosen
+        p = s[t, chosen]
+        w[t] = scale * p / (p.sum() + 1e-20) if renorm else scale * p
+    return idx, w
+
+
+def route_backward(l, idx, dw, softmax=False, renorm=True, scale=1.0):
+    """(dlogits, magnitude): magnitude is the same sum with absolute values
+    of its terms, the scale of the rounding errors of each element."""
+    s = route_scores(l, softmax)
+    T, E = s.shape
+    dl, mag = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        ids = [int(i) for i in idx[t]]
+        ok = [0 <= i < E for i in ids]
+        p = np.array([s[t, i] if o else 0.0 for i, o in zip(ids, ok)])
+        g = np.where(ok, np.asarray(dw[t], np.float64), 0.0) * scale
+        if renorm:
+            S = p.sum() + 1e-20
+            dp = (g - (g * p).sum() / S) / S
+            mp = (np.abs(g) + (np.abs(g) * p).sum() / S) / S
+        else:
+            dp, mp = g, np.abs(g)
+        ds, ms = np.zeros(E), np.zeros(E)
+        for i, o, a, m in zip(ids, ok, dp, mp):
+            if o:
+                ds[i] += a
+                ms[i] += m
+        if softmax:
+            # renormalised, sum ds s = D / S (1 - P / S) with D = sum g p and
+            # P = S - 1e-20: taken as D / S * 1e-20 / S, since the difference of
+            # the two nearly equal sums would leave 1e-17 of rounding here
+            c = (g * p).sum() / S * (1e-20 / S) if renorm else (ds * s[t]).sum()
+            dl[t] = s[t] * (ds - c)
+            mc = (np.abs(g) * p).sum() / S * (1e-20 / S) if renorm else (ms * s[t]).sum()
+            mag[t] = s[t] * (ms + mc)
+        else:
+            lt = _clean(l[t:t + 1])[0]
+            e = np.exp(-np.abs(np.where(lt > -np.inf, lt, 0.0)))
+            slope = np.where(lt > -np.inf, e / (1.0 + e) ** 2, 0.0)
+            dl[t], mag[t] = ds * slope, ms * slope
+    return dl, mag
+
+
+def _f64(v):
+    return None if v is None else np.asarray(v, np.float64)
+
+
+def block_norm(h, y, pre, post, gate, alpha, eps):
+    """(h_out, x or None, ry, rh); gate [D], [T, 1] or [T, D] or None."""
+    h, y, pre, post, gate, alpha = (_f64(v) for v in (h, y, pre, post, gate, alpha))
+    T, D = h.shape
+    y = np.zeros_like(h) if y is None else y
+    ry = np.ones((T, 1))
+    n = y
+    if post is not None:
+        ry = 1.0 / np.sqrt((y * y).mean(1, keepdims=True) + eps)
+        n = post * y * ry
+    h2 = (1.0 if alpha is None else alpha) * h + (1.0 if gate is None else gate) * n
+    if pre is None:
+        return h2, None, ry, np.ones((T, 1))
+    rh = 1.0 / np.sqrt((h2 * h2).mean(1, keepdims=True) + eps)
+    return h2, pre * h2 * rh, ry, rh
+
+
+def block_norm_backward(h, y, dh_out, dx, pre, post, gate, alpha, eps):
+    """{name: (gradient, magnitude)}; magnitude bounds the sum of the absolute
+    values of the terms of each element."""
+    h, y, pre, post, gate, alpha, dh_out, dx = (
+        _f64(v) for v in (h, y, pre, post, gate, alpha, dh_out, dx))
+    T, D = h.shape
+    h2, _, ry, rh = block_norm(h, y, pre, post, gate, alpha, eps)
+    yv = np.zeros_like(h) if y is None else y
+    a1 = 1.0 if alpha is None else alpha
+    g1 = 1.0 if gate is None else gate
+    p1 = 1.0 if post is None else post
+    yn = yv * ry
+    n = p1 * yn
+    mh2 = np.abs(a1 * h) + np.abs(g1 * n)
+    G = np.zeros_like(h) if dh_out is None else dh_out.copy()
+    M = np.abs(G)
+    out = {}
+    if dx is not None:
+        hn, mhn = h2 * rh, mh2 * rh
+        a = pre * dx
+        G = G + rh * (a - hn * (a * hn).mean(1, keepdims=True))
+        M = M + rh * (np.abs(a) + mhn * (np.abs(a) * mhn).mean(1, keepdims=True))
+        out["dpre_weight"] = ((dx * hn).sum(0), (np.abs(dx) * mhn).sum(0))
+    elif pre is not None:
+        out["dpre_weight"] = (np.zeros(D), np.zeros(D))
+    out["dh"] = (a1 * G, np.abs(a1) * M)
+    if alpha is not None:
+        out["dres_scale"] = ((G * h).sum(0), (M * np.abs(h)).sum(0))
+    dn, mdn = g1 * G, np.abs(g1) * M
+    if post is not None:
+        out["dpost_weight"] = ((dn * yn).sum(0), (mdn * np.abs(yn)).sum(0))
+    if y is not None:
+        if post is None:
+            out["dy"] = (dn, mdn)
+        else:
+            b, mb = p1 * dn, np.abs(p1) * mdn
+            out["dy"] = (ry * (b - yn * (b * yn).mean(1, keepdims=True)),
+                         ry * (mb + np.abs(yn) * (mb * np.abs(yn)).mean(1, keepdims=True)))
+    if gate is not None:
+        d, m = G * n, M * np.abs(n)
+        if gate.ndim == 1:
+            d, m = d.sum(0), m.sum(0)
+        elif gate.shape == (T, 1) and D != 1:
+            d, m = d.sum(1, keepdims=True), m.sum(1, keepdims=True)
+        out["dgate"] = (d, m)
+    return out

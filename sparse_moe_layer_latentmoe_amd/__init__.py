@@ -37,6 +37,8 @@ EXPORTED = (
     "lmoe_workspace_size", "lmoe_create", "lmoe_forward", "lmoe_route", "lmoe_destroy",
     "lmoe_status_string", "lmoe_num_stages", "lmoe_stage_name", "lmoe_profile_begin",
     "lmoe_profile_end", "lmoe_quantize_mxfp4", "lmoe_forward_noalloc",
+    "lmoe_route_logits", "lmoe_route_logits_backward", "lmoe_block_norm",
+    "lmoe_block_norm_workspace_size", "lmoe_block_norm_backward",
 )
 
 
@@ -123,6 +125,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.lmoe_forward_noalloc.argtypes = [ctypes.POINTER(LmoeConfig), ctypes.POINTER(LmoeWeights),
                                          P, ctypes.c_int32, P, P]
     lib.lmoe_forward_noalloc.restype = ctypes.c_int
+    _declare_operators(lib)
     _lib = lib
     return lib
 
@@ -380,3 +383,11 @@ class LatentMoE:
         if st != LMOE_OK:
             raise LmoeError(st, "lmoe_profile_end")
         return dict(zip(stage_names(), list(ms))), int(nf.value)
+
+
+# The operators around the layer (their own module; the same binding style).
+from .operators import (  # noqa: E402
+    GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, SCORE_SIGMOID, SCORE_SOFTMAX,
+    BlockNormGrads, LmoeBlockNormArgs, LmoeBlockNormGrads, LmoeRouter, block_norm,
+    block_norm_backward, make_router, route_logits, route_logits_backward)
+from .operators import declare as _declare_operators  # noqa: E402

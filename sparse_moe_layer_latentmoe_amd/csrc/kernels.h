@@ -80,6 +80,21 @@ hipError_t router_select(const float* logits, const float* bias, int T, int E, i
                          int n_group, int topk_group, float rho, int32_t* idx, float* w,
                          hipStream_t s);
 
+// Routing from given logits [T, E] (rows `stride` elements apart, fp32 or
+// bf16) and the gradient of its weights; T >= 1, E <= 1024, K <= 64,
+// n_group <= 64 equal groups, best 1 or 2 (with best 2 and n_group > 1,
+// groups of at least two).
+struct RouteProblem {
+  int T, E, K, n_group, topk_group, best, softmax, renorm;
+  float rho;
+  long stride;
+};
+hipError_t route_logits(const RouteProblem& r, const void* logits, bool bf16, const float* bias,
+                        int32_t* idx, float* w, hipStream_t s);
+hipError_t route_logits_backward(const RouteProblem& r, const void* logits, bool bf16,
+                                 const int32_t* idx, const float* dw, void* dlogits,
+                                 hipStream_t s);
+
 // Grouping by expert: counts[E], offsets[E+1], rows_tok[T*K], inv[T*K] and
 // the tile list (tiles of at most tile_m rows) with its length in *ntiles.
 // blockcnt is scratch of ceil(T/64) * E ints.
@@ -91,6 +106,39 @@ hipError_t dispatch(const int32_t* idx, int T, int K, int E, int32_t* blockcnt, 
 // bf16(gamma * h) [T, D] and rn = 1 / sqrt(mean(h^2) + eps) [T].
 hipError_t prenorm(const uint16_t* h, const uint16_t* gamma, int T, int D, float eps,
                    uint16_t* xt, float* rn, hipStream_t s);
+
+// The norms around a block with its gate and residual scale, and their
+// gradients.  T >= 1, 1 <= D <= block_norm_max_width(); h and y may have row
+// strides, every other [T, D] array is dense.  A null y is 0; null post: y is
+// not normalised; null x / dx: no second norm; null alpha, pre: ones.
+struct NormParam {
+  const void* p;
+  int bf16;
+};
+struct BlockNormProblem {
+  const void* h;
+  const void* y;
+  long h_stride, y_stride;
+  bool h_bf16, y_bf16;
+  NormParam pre, post, alpha, gate;
+  int gate_kind;  // 0 none, 1 [D], 2 [T], 3 [T, D]
+  int T, D;
+  float eps;
+};
+struct BlockNormGrads {
+  const float* stats;  // [T, 2] of the forward
+  const void* dh_out;
+  const void* dx;
+  // wanted gradients, in their inputs' types; null: not computed
+  void *dh, *dy, *dpre, *dpost, *dalpha, *dgate;
+};
+int block_norm_max_width();
+hipError_t block_norm(const BlockNormProblem& b, void* h_out, void* x, float* stats,
+                      hipStream_t s);
+// bytes of the partial column sums of `nsums` column outputs
+size_t block_norm_backward_part(int T, int D, int nsums);
+hipError_t block_norm_backward(const BlockNormProblem& b, const BlockNormGrads& g, float* part,
+                               hipStream_t s);
 
 // r = sum_k w[t][k] O[inv[t][k]] -> r16 (bf16) and, if r32 != NULL, fp32.
 hipError_t combine(const uint16_t* o, const int32_t* inv, const float* w, int T, int K, int R,

@@ -1,0 +1,453 @@
+// Routing from given logits (softmax or sigmoid scores) and its gradient.
+//
+// Per token, over E logits l:
+//   s = sigmoid(l)  or  softmax(l)            scores
+//   b = s + bias                              what orders the experts; without
+//                                             a bias the logits order them
+//                                             (every score grows with its logit)
+//   groups: a group's score is the sum of its 1 or 2 largest b; the
+//           topk_group best groups stay (equal ones: the lower index)
+//   I = the K largest of what stays (equal ones: the lower id), ascending ids
+//   w = rho s_I  or  rho s_I / (sum s_I + 1e-20)
+//
+// Selection is decided on the values of b in 64 bits, so that it does not
+// depend on how a 32-bit exponential rounds: the scores are computed in fp32
+// with a known error bound, and only where the border (the K-th against the
+// (K+1)-th expert, or the kept groups' last against the next) is closer than
+// that bound are the candidates next to it computed again in fp64.
+//
+// One wavefront per token, expert 64 j + lane in slot j of lane `lane`, all
+// in registers; the K-th largest key is found bit by bit with one ballot per
+// slot, ending at the first bit whose count is exactly K.
+#include <cfloat>
+#include <type_traits>
+
+#include "kernels.h"
+#include "lmoe_device.h"
+
+namespace lmoe {
+
+namespace {
+
+constexpr int kRouteWaves = 4;  // tokens per work-group
+
+__device__ __forceinline__ float route_load(const float* p) { return *p; }
+__device__ __forceinline__ float route_load(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ void route_store(float* p, float v) { *p = v; }
+__device__ __forceinline__ void route_store(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+
+// Order-preserving maps onto unsigned integers (-0 equals +0) and back.
+__device__ __forceinline__ uint32_t key32(float b) {
+  if (b == 0.0f) b = 0.0f;
+  const uint32_t u = __float_as_uint(b);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key32_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+__device__ __forceinline__ uint64_t key64(double b) {
+  if (b == 0.0) b = 0.0;
+  const uint64_t u = (uint64_t)__double_as_longlong(b);
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;  // key32(-inf)
+
+template <class U, int NS>
+__device__ __forceinline__ int count_ge(const U (&key)[NS], U v) {
+  int c = 0;
+#pragma unroll
+  for (int j = 0; j < NS; ++j) c += __popcll(__ballot(key[j] >= v));
+  return c;
+}
+
+// A value v that at least n of the wave's keys reach and that is either
+// reached by exactly n of them or equal to the n-th largest key.  Keys of 0
+// are empty; n is at most the number of others.
+template <class U, int NS>
+__device__ __forceinline__ U border(const U (&key)[NS], int n) {
+  U v = 0;
+  for (int bit = (int)sizeof(U) * 8 - 1; bit >= 0; --bit) {
+    const U c = v | ((U)1 << bit);
+    const int cnt = count_ge<U, NS>(key, c);
+    if (cnt >= n) v = c;
+    if (cnt == n) break;
+  }
+  return v;
+}
+
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <class F>
+__device__ __forceinline__ F wave_sum(F v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  return v;
+}
+
+// A logit as the kernels use it: NaN and -inf mean "not available" (-inf),
+// +inf counts as the largest finite value.
+__device__ __forceinline__ float clean_logit(float v) {
+  return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY;
+}
+
+// Sum of the `best` (1 or 2) largest of the G values of group `lane` in the
+// wave's LDS row; the walk starts at a different place in each lane, so that
+// groups of 32 or 64 do not meet in one LDS bank.
+template <class F>
+__device__ __forceinline__ F group_best(const F* row, int lane, int G, int best) {
+  F t1 = -INFINITY, t2 = -INFINITY;
+  int i = lane % G;
+  for (int n = 0; n < G; ++n) {
+    const F b = row[lane * G + i];
+    if (b > t1) {
+      t2 = t1;
+      t1 = b;
+    } else if (b > t2) {
+      t2 = b;
+    }
+    i = i + 1 == G ? 0 : i + 1;
+  }
+  return best == 2 ? t1 + t2 : t1;
+}
+
+// The lanes of the n largest keys (one per lane; equal keys: lower lanes).
+template <class U>
+__device__ __forceinline__ uint64_t best_lanes(U key, int n, uint64_t below) {
+  const U k[1] = {key};
+  const U v = border<U, 1>(k, n);
+  const uint64_t gt = __ballot(key > v), eq = __ballot(key == v);
+  const int room = n - __popcll(gt);
+  return gt | __ballot(key == v && __popcll(eq & below) < room);
+}
+
+}  // namespace
+
+struct RouteParams {
+  int T, E, K, n_group, topk_group, best, softmax, renorm;
+  float rho;
+  long stride;
+};
+
+template <class LT, int NJ>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
+    const LT* __restrict__ logits, const float* __restrict__ bias, RouteParams p,
+    int32_t* __restrict__ idx_out, float* __restrict__ w_out) {
+  __shared__ float ssel[kRouteWaves][64];
+  // the biased scores of the group step: 32-bit, or 64-bit where it is close
+  __shared__ __attribute__((aligned(8))) char rows[kRouteWaves][NJ * 64 * 8];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int t = blockIdx.x * kRouteWaves + wv;
+  if (t >= p.T) return;
+  const int E = p.E, K = p.K;
+  const LT* lp = logits + (size_t)t * p.stride;
+  const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
+
+  float l[NJ], s[NJ], b[NJ];
+  uint32_t key[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    l[j] = j * 64 + lane < E ? clean_logit(route_load(lp + j * 64 + lane)) : -INFINITY;
+  float m = 0.f, inv = 1.f;
+  if (p.softmax) {
+    m = l[0];
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) m = fmaxf(m, l[j]);
+    m = wave_max(m);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      s[j] = l[j] > -INFINITY ? expf(l[j] - m) : 0.f;
+      sum += s[j];
+    }
+    sum = wave_sum(sum);
+    inv = sum > 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) s[j] *= inv;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) s[j] = l[j] > -INFINITY ? 1.0f / (1.0f + expf(-l[j])) : 0.f;
+  }
+  // Error bound of a biased score: a sigmoid is within 4 ulp of its value
+  // (exp 1, add 1/2, divide 1/2 and their propagation) and at most 1; a
+  // softmax score within 2^-19 of the largest one, inv (up to 16 + 6
+  // additions, the rounding of l - m times the exponential's slope, exp and
+  // two products); the bias addition rounds by 2^-24 of its result, which is
+  // added where the border is known.
+  const float serr = p.softmax ? 0x1p-19f * inv : 0x1p-21f;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int e = j * 64 + lane;
+    const bool on = l[j] > -INFINITY;
+    b[j] = on ? (bias ? s[j] + bias[e] : s[j]) : -INFINITY;
+    key[j] = e < E ? (on ? key32(bias ? b[j] : l[j]) : kKeyMinusInf) : 0u;
+  }
+
+  // biased score of slot j in 64 bits (only where the border is close)
+  double m64 = 0.0, inv64 = 1.0;
+  bool have64 = false;
+  auto prepare64 = [&]() {
+    if (have64) return;
+    have64 = true;
+    if (!p.softmax) return;
+    m64 = (double)m;
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (l[j] > -INFINITY) sum += exp((double)l[j] - m64);
+    sum = wave_sum(sum);
+    inv64 = sum > 0.0 ? 1.0 / sum : 0.0;
+  };
+  auto biased64 = [&](int j) -> double {
+    if (!(l[j] > -INFINITY)) return -INFINITY;
+    const double v = p.softmax ? exp((double)l[j] - m64) * inv64
+                               : 1.0 / (1.0 + exp(-(double)l[j]));
+    return bias ? v + (double)bias[j * 64 + lane] : v;
+  };
+
+  if (p.n_group > 1) {
+    const int G = E / p.n_group;
+    float* row = reinterpret_cast<float*>(rows[wv]);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (j * 64 + lane < E) row[j * 64 + lane] = b[j];
+    wave_lds_fence();
+    const bool has = lane < p.n_group;
+    const float gs = has ? group_best(row, lane, G, p.best) : -INFINITY;
+    const uint32_t gk[1] = {has ? key32(gs) : 0u};
+    const uint32_t gv = border<uint32_t, 1>(gk, p.topk_group);
+    const float gt = key32_value(gv);
+    // a group's score is off by at most two scores' bounds and two roundings
+    const float gerr = 4.f * serr + 0x1p-21f * fabsf(gt);
+    const int over = __popcll(__ballot(has && gs >= gt + 2.f * gerr));
+    const int upto = __popcll(__ballot(has && gs > gt - 2.f * gerr));
+    uint64_t kept;
+    if (over < p.topk_group && upto > p.topk_group) {
+      prepare64();
+      double* row64 = reinterpret_cast<double*>(rows[wv]);
+      wave_lds_fence();  // the fp32 row has been read
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (j * 64 + lane < E) row64[j * 64 + lane] = biased64(j);
+      wave_lds_fence();
+      kept = best_lanes<uint64_t>(has ? key64(group_best(row64, lane, G, p.best)) : 0ull,
+                                  p.topk_group, below);
+    } else {
+      kept = best_lanes<uint32_t>(gk[0], p.topk_group, below);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int e = j * 64 + lane;
+      if (e < E && !((kept >> (e / G)) & 1ull)) {
+        key[j] = 0u;
+        b[j] = -INFINITY;
+      }
+    }
+  }
+
+  uint32_t v = border<uint32_t, NJ>(key, K);
+  if (bias && v > kKeyMinusInf) {
+    const float bt = key32_value(v);
+    const float err = 2.f * serr + 0x1p-22f * fabsf(bt);
+    int over = 0, upto = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      over += __popcll(__ballot(b[j] >= bt + 2.f * err));
+      upto += __popcll(__ballot(b[j] > bt - 2.f * err));
+    }
+    if (over < K && upto > K) {
+      // more than K within reach of the border: those next to it are
+      // ordered by their 64-bit values, those above are in
+      prepare64();
+      uint64_t k64[NJ];
+      int sure = 0;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const bool in = b[j] >= bt + 4.f * err;
+        sure += __popcll(__ballot(in));
+        k64[j] = !in && b[j] > bt - 4.f * err ? key64(biased64(j)) : 0ull;
+        key[j] = in ? 0xFFFFFFFFu : 0u;
+      }
+      const uint64_t v64 = border<uint64_t, NJ>(k64, K - sure);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (k64[j]) key[j] = k64[j] > v64 ? 0xFFFFFFFEu : (k64[j] == v64 ? 1u : 0u);
+      v = 1u;
+    }
+  }
+
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) above += __popcll(__ballot(key[j] > v));
+  int room = K - above;  // experts with key == v still to take, lowest ids first
+  int base = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const uint64_t eq = __ballot(key[j] == v);
+    const bool on = key[j] > v || (key[j] == v && __popcll(eq & below) < room);
+    const int took = __popcll(eq);
+    room -= took < room ? took : room;
+    const uint64_t mk = __ballot(on);
+    if (on) {
+      const int pos = base + __popcll(mk & below);
+      idx_out[(size_t)t * K + pos] = j * 64 + lane;
+      ssel[wv][pos] = s[j];
+    }
+    base += __popcll(mk);
+  }
+  wave_lds_fence();
+  const float sk = lane < K ? ssel[wv][lane] : 0.f;
+  float w = sk * p.rho;
+  if (p.renorm) w = (sk / (wave_sum(sk) + 1e-20f)) * p.rho;
+  if (lane < K) w_out[(size_t)t * K + lane] = w;
+}
+
+// Gradient of the weights in the logits, the selection held fixed.  With
+// S = sum of the selected scores + 1e-20 and D = sum dw_k s_k:
+//   renormalised   ds_k = rho / S (dw_k - D / S),   otherwise ds_k = rho dw_k
+//   sigmoid        dl_k = ds_k s_k (1 - s_k), zero for the others
+//   softmax        dl_i = s_i (ds_i - c), c = sum ds_k s_k; renormalised, that
+//                  sum is rho D / S (1 - (S - 1e-20) / S) = rho D / S 1e-20 / S,
+//                  taken in that form so that nothing cancels
+// One wavefront per token; ds goes through an LDS row to the lanes that own
+// the experts.  Equal ids add up, in order; ids outside [0, E) are ignored.
+template <class LT, int NJ>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_logits_backward_kernel(
+    const LT* __restrict__ logits, const int32_t* __restrict__ idx, const float* __restrict__ dw,
+    RouteParams p, LT* __restrict__ dlogits) {
+  __shared__ float row[kRouteWaves][NJ * 64];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int t = blockIdx.x * kRouteWaves + wv;
+  if (t >= p.T) return;
+  const int E = p.E, K = p.K;
+  const LT* lp = logits + (size_t)t * p.stride;
+  const int id = lane < K ? idx[(size_t)t * K + lane] : -1;
+  const bool valid = id >= 0 && id < E;
+  const float g = valid ? dw[(size_t)t * K + lane] : 0.f;
+  const float lk = valid ? clean_logit(route_load(lp + id)) : -INFINITY;
+
+  float s[NJ];
+  float m = 0.f, inv = 1.f;
+  if (p.softmax) {
+    m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      s[j] = j * 64 + lane < E ? clean_logit(route_load(lp + j * 64 + lane)) : -INFINITY;
+      m = fmaxf(m, s[j]);
+    }
+    m = wave_max(m);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      s[j] = s[j] > -INFINITY ? expf(s[j] - m) : 0.f;
+      sum += s[j];
+    }
+    sum = wave_sum(sum);
+    inv = sum > 0.f ? 1.0f / sum : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) row[wv][j * 64 + lane] = 0.f;
+
+  float sk, slope;  // score of slot `lane` of the selection, and (sigmoid) s (1 - s)
+  if (p.softmax) {
+    sk = lk > -INFINITY ? expf(lk - m) * inv : 0.f;
+    slope = sk;
+  } else {
+    const float ex = lk > -INFINITY ? expf(-fabsf(lk)) : 0.f;
+    const float r = 1.0f / (1.0f + ex);
+    sk = lk > -INFINITY ? (lk >= 0.f ? r : ex * r) : 0.f;
+    slope = ex * r * r;
+  }
+  float ds = p.rho * g, c = 0.f;
+  if (p.renorm) {
+    const float S = wave_sum(sk) + 1e-20f;
+    const float D = wave_sum(g * sk);
+    ds = valid ? p.rho / S * (g - D / S) : 0.f;
+    c = p.rho * (D / S) * (1e-20f / S);
+  } else if (p.softmax) {
+    c = wave_sum(ds * sk);
+  }
+  // sigmoid: the finished gradient goes through the row; softmax: ds
+  const float put = p.softmax ? ds : ds * slope;
+  bool dup = false;
+  for (int k = 0; k + 1 < K; ++k) {
+    const int o = __shfl(id, k, 64);
+    dup |= lane > k && valid && o == id;
+  }
+  wave_lds_fence();
+  if (__ballot(dup) == 0ull) {
+    if (valid) row[wv][id] = put;
+  } else {
+    for (int k = 0; k < K; ++k) {
+      if (lane == k && valid) row[wv][id] += put;
+      wave_lds_fence();
+    }
+  }
+  wave_lds_fence();
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int e = j * 64 + lane;
+    if (e < E) {
+      const float r = row[wv][e];
+      route_store(dlogits + (size_t)t * E + e, p.softmax ? s[j] * inv * (r - c) : r);
+    }
+  }
+}
+
+namespace {
+template <class F>
+void with_slots(int E, F f) {
+  const int nj = (E + 63) / 64;
+  if (nj <= 1) f(std::integral_constant<int, 1>{});
+  else if (nj <= 2) f(std::integral_constant<int, 2>{});
+  else if (nj <= 4) f(std::integral_constant<int, 4>{});
+  else if (nj <= 8) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 16>{});
+}
+RouteParams params(const RouteProblem& r) {
+  return {r.T, r.E, r.K, r.n_group, r.topk_group, r.best, r.softmax, r.renorm, r.rho, r.stride};
+}
+}  // namespace
+
+hipError_t route_logits(const RouteProblem& r, const void* logits, bool bf16, const float* bias,
+                        int32_t* idx, float* w, hipStream_t s) {
+  const int grid = (r.T + kRouteWaves - 1) / kRouteWaves;
+  const RouteParams p = params(r);
+  with_slots(r.E, [&](auto nj) {
+    constexpr int NJ = decltype(nj)::value;
+    if (bf16)
+      route_logits_kernel<uint16_t, NJ><<<grid, kRouteWaves * 64, 0, s>>>(
+          static_cast<const uint16_t*>(logits), bias, p, idx, w);
+    else
+      route_logits_kernel<float, NJ><<<grid, kRouteWaves * 64, 0, s>>>(
+          static_cast<const float*>(logits), bias, p, idx, w);
+  });
+  return hipGetLastError();
+}
+
+hipError_t route_logits_backward(const RouteProblem& r, const void* logits, bool bf16,
+                                 const int32_t* idx, const float* dw, void* dlogits,
+                                 hipStream_t s) {
+  const int grid = (r.T + kRouteWaves - 1) / kRouteWaves;
+  const RouteParams p = params(r);
+  with_slots(r.E, [&](auto nj) {
+    constexpr int NJ = decltype(nj)::value;
+    if (bf16)
+      route_logits_backward_kernel<uint16_t, NJ><<<grid, kRouteWaves * 64, 0, s>>>(
+          static_cast<const uint16_t*>(logits), idx, dw, p, static_cast<uint16_t*>(dlogits));
+    else
+      route_logits_backward_kernel<float, NJ><<<grid, kRouteWaves * 64, 0, s>>>(
+          static_cast<const float*>(logits), idx, dw, p, static_cast<float*>(dlogits));
+  });
+  return hipGetLastError();
+}
+
+}  // namespace lmoe
