@@ -340,6 +340,58 @@ lmoe_status lmoe_block_norm_backward(const lmoe_block_norm_args *a, const float 
                                      const lmoe_block_norm_grads *g, void *workspace,
                                      size_t workspace_bytes, void *stream);
 
+/* 8-bit floating point (e4m3, OCP: one sign, four exponent and three mantissa
+ * bits, largest finite value 448) with fp32 scales of blocks of 128 along the
+ * last axis: value = code * scale, scale = max(largest magnitude of the block
+ * / 448, 2^-126), code = value / scale rounded to the nearest e4m3 number,
+ * ties to even (fp32 division, correctly rounded).  Inputs must be finite.
+ *
+ * Activations: x [rows, cols] (of `x_type`, rows x_stride >= cols elements
+ * apart), a scale for each block of a row: codes [rows, cols], scales [rows,
+ * ceil(cols / 128)].  Any cols >= 1. */
+lmoe_status lmoe_quantize_fp8(const void *x, int32_t x_type, int64_t rows, int32_t cols,
+                              int64_t x_stride, uint8_t *codes, float *scales, void *stream);
+
+/* Weights: `matrices` matrices w [rows, cols], dense, a scale for each block
+ * of 128 rows x 128 columns (smaller at the edges): codes like w, scales
+ * [matrices, ceil(rows / 128), ceil(cols / 128)]. */
+lmoe_status lmoe_quantize_fp8_weight(const void *w, int32_t w_type, int64_t matrices, int32_t rows,
+                                     int32_t cols, uint8_t *codes, float *scales, void *stream);
+
+/* The product of such activations and weights, y [M, N] = x w^T with fp32
+ * sums, rounded once to y_type:
+ *   y[m][n] = sum_b xs[r][b] ws[n / 128][b] sum_{k in block b} x[r][k] w[n][k]
+ * with r = rows[m], or m when rows is NULL.  With n_groups >= 1 there are
+ * that many weight matrices and row m takes matrix g of the range offsets[g]
+ * <= m < offsets[g + 1] (a sparse layer's rows sorted by expert; empty groups
+ * are fine); rows of no group are not written.  Offsets are cut to [0, M];
+ * they must ascend.  A row index outside [0, x_rows) gives a row of zeros
+ * (if row 0 of x is finite). */
+typedef struct {
+  const uint8_t *x;       /* [x_rows, K] codes, 16-byte aligned */
+  const float *x_scales;  /* [x_rows, K / 128] */
+  const uint8_t *w;       /* [n_groups or 1, N, K] codes, 16-byte aligned */
+  const float *w_scales;  /* [n_groups or 1, ceil(N / 128), K / 128] */
+  const int32_t *rows;    /* [M] or NULL (then x_rows >= M) */
+  const int32_t *offsets; /* [n_groups + 1], NULL if n_groups is 0 */
+  void *y;                /* [M, N], 16-byte aligned */
+  int32_t y_type;         /* lmoe_dtype */
+  int32_t n_groups;       /* 0 (one matrix, no groups) .. 1024 */
+  int32_t M;              /* 0 .. 2^24 */
+  int32_t x_rows;         /* >= 1 if M > 0; with rows, x_rows * K < 2^31 */
+  int32_t N;              /* a multiple of 16, up to 2^20 */
+  int32_t K;              /* a multiple of 128, up to 65536 */
+} lmoe_fp8_matmul_args;
+
+/* Bytes of workspace of lmoe_fp8_matmul (the row tiles of each group; 0
+ * without groups, or for arguments it refuses).  Pure host function. */
+size_t lmoe_fp8_matmul_workspace_size(const lmoe_fp8_matmul_args *a);
+
+/* workspace: 16-byte aligned device memory of that size; calls that may
+ * overlap need one each. */
+lmoe_status lmoe_fp8_matmul(const lmoe_fp8_matmul_args *a, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* ---- per-kernel timing (HIP events on the forward's stream) ------------ */
 
 /* Number of timed stages of lmoe_forward and the name of stage i.  Stages

@@ -169,3 +169,73 @@ def block_norm_backward(h, y, dh_out, dx, pre, post, gate, alpha, eps):
             d, m = d.sum(1, keepdims=True), m.sum(1, keepdims=True)
         out["dgate"] = (d, m)
     return out
+
+
+# ---- 8-bit floating point ------------------------------------------------------
+
+
+def e4m3_values():
+    """The value of each of the 256 e4m3 codes (NaN for 0x7F and 0xFF)."""
+    c = np.arange(256)
+    sign = np.where(c & 0x80, -1.0, 1.0)
+    e, m = (c >> 3) & 15, c & 7
+    v = np.where(e == 0, m / 8.0 * 2.0 ** -6, (1 + m / 8.0) * 2.0 ** (e - 7.0))
+    v = np.where((c & 0x7F) == 0x7F, np.nan, v)
+    return sign * v
+
+
+def to_e4m3(v):
+    """Codes of the e4m3 numbers nearest to v (|v| < 464), ties to even; the
+    sign of a value that rounds to zero is kept."""
+    v = np.asarray(v, np.float64)
+    mags = e4m3_values()[:0x7F]
+    a = np.abs(v)
+    hi = np.clip(np.searchsorted(mags, a), 1, 0x7E)
+    lo = hi - 1
+    dl, dh = a - mags[lo], mags[hi] - a
+    code = np.where((dh < dl) | ((dh == dl) & (hi % 2 == 0)), hi, lo)
+    return (code | np.where(np.signbit(v), 0x80, 0)).astype(np.uint8)
+
+
+def quantize_fp8(x, block_rows: int = 1):
+    """(codes, scales) of x [R, C] fp32, blocks of block_rows x 128; the
+    scale and the ratio are the correctly rounded fp32 quotients."""
+    x = np.asarray(x, np.float32)
+    R, C = x.shape
+    rb, cb = -(-R // block_rows), -(-C // 128)
+    codes = np.zeros((R, C), np.uint8)
+    scales = np.zeros((rb, cb), np.float32)
+    for i in range(rb):
+        for j in range(cb):
+            s = np.s_[i * block_rows:(i + 1) * block_rows, j * 128:(j + 1) * 128]
+            sc = np.maximum(np.abs(x[s]).max() / np.float32(E4M3_MAX), np.float32(2.0 ** -126))
+            scales[i, j] = sc
+            codes[s] = to_e4m3(x[s] / sc)
+    return codes, scales
+
+
+def dequantize(codes, scales, block_rows: int = 1):
+    v = e4m3_values()[codes]
+    s = np.repeat(np.repeat(np.asarray(scales, np.float64), 128, 1), block_rows, 0)
+    return v * s[:v.shape[0], :v.shape[1]]
+
+
+def fp8_matmul(xc, xs, wc, ws, offsets=None, rows=None):
+    """(y, magnitude, written): rows of no group are not written; a row index
+    outside x gives zeros."""
+    x = dequantize(xc, xs)
+    if rows is not None:
+        ok = (rows >= 0) & (rows < x.shape[0])
+        x = np.where(ok[:, None], x[np.where(ok, rows, 0)], 0.0)
+    M = x.shape[0]
+    if offsets is None:
+        w = dequantize(wc, ws, 128)
+        return x @ w.T, np.abs(x) @ np.abs(w).T, np.ones(M, bool)
+    N = wc.shape[1]
+    y, mag, done = np.zeros((M, N)), np.zeros((M, N)), np.zeros(M, bool)
+    for g in range(wc.shape[0]):
+        a, b = (min(max(int(o), 0), M) for o in offsets[g:g + 2])
+        if b > a:
+            w = dequantize(wc[g], ws[g], 128)
+            y[a:b], mag[a:b], done[a:b] = x[a:b] @ w.T, np.abs(x[a:b]) @ np.abs(w).T, True
+    return y, mag, done

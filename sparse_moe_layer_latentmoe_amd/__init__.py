@@ -38,7 +38,8 @@ EXPORTED = (
     "lmoe_status_string", "lmoe_num_stages", "lmoe_stage_name", "lmoe_profile_begin",
     "lmoe_profile_end", "lmoe_quantize_mxfp4", "lmoe_forward_noalloc",
     "lmoe_route_logits", "lmoe_route_logits_backward", "lmoe_block_norm",
-    "lmoe_block_norm_workspace_size", "lmoe_block_norm_backward",
+    "lmoe_block_norm_workspace_size", "lmoe_block_norm_backward", "lmoe_quantize_fp8",
+    "lmoe_quantize_fp8_weight", "lmoe_fp8_matmul_workspace_size", "lmoe_fp8_matmul",
 )
 
 
@@ -388,6 +389,7 @@ class LatentMoE:
 # The operators around the layer (their own module; the same binding style).
 from .operators import (  # noqa: E402
     GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, SCORE_SIGMOID, SCORE_SOFTMAX,
-    BlockNormGrads, LmoeBlockNormArgs, LmoeBlockNormGrads, LmoeRouter, block_norm,
-    block_norm_backward, make_router, route_logits, route_logits_backward)
+    BlockNormGrads, LmoeBlockNormArgs, LmoeBlockNormGrads, LmoeFp8MatmulArgs, LmoeRouter,
+    block_norm, block_norm_backward, fp8_matmul, make_router, quantize_fp8, quantize_fp8_weight,
+    route_logits, route_logits_backward)
 from .operators import declare as _declare_operators  # noqa: E402

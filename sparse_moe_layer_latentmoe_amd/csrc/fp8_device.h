@@ -1,0 +1,33 @@
+// Device-side pieces of the 8-bit floating-point (e4m3) kernels.
+#pragma once
+#include "lmoe_device.h"
+
+namespace lmoe {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kE4M3Max = 448.f;
+
+__device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// D(16x16, fp32) = A(16x128, e4m3) * B(128x16, e4m3) from a zero accumulator.
+// Lane l supplies row l%16 of A and column l%16 of B, 32 k each (which ones
+// does not matter as long as both agree); result layout as mfma_bf16's.
+__device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
+                                                          0, 0, 0);
+}
+
+// Four values within [-448, 448] (up to rounding) as e4m3 codes, lowest byte
+// first, rounded to nearest, ties to even.
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+  return (uint32_t)v;
+}
+
+}  // namespace lmoe

@@ -140,6 +140,34 @@ size_t block_norm_backward_part(int T, int D, int nsums);
 hipError_t block_norm_backward(const BlockNormProblem& b, const BlockNormGrads& g, float* part,
                                hipStream_t s);
 
+// 8-bit floating point (e4m3) with fp32 scales of blocks of 128 along k.
+// Activations [rows, cols] (rows `stride` apart): a scale for each block of a
+// row, scales [rows, ceil(cols / 128)].  Weights [matrices, rows, cols]: a
+// scale for each 128 x 128 block, scales [matrices, ceil(rows / 128),
+// ceil(cols / 128)].
+hipError_t fp8_quantize(const void* x, bool bf16, long rows, int cols, long stride,
+                        uint8_t* codes, float* scales, hipStream_t s);
+hipError_t fp8_quantize_weight(const void* w, bool bf16, long matrices, int rows, int cols,
+                               uint8_t* codes, float* scales, hipStream_t s);
+// y[m] = x[rows ? rows[m] : m] w^T, K a multiple of 128 (at most kFp8MaxBlocks
+// blocks), N a multiple of 16.  groups = 0: one weight matrix for all M rows;
+// else row m takes the matrix of the group whose range offsets[g] ..
+// offsets[g + 1] - 1 holds it (rows of no group are not written).
+constexpr int kFp8MaxBlocks = 512;
+constexpr int kFp8TileM = 128;
+struct Fp8Gemm {
+  const uint8_t* x;     // [x_rows, K]
+  const float* xs;      // [x_rows, KB]
+  const uint8_t* w;     // [groups or 1, N, K]
+  const float* ws;      // [groups or 1, NB, KB]
+  const int32_t* rows;  // [M] or null
+  void* y;              // [M, N], bf16 or fp32
+  int M, N, K, KB, NB, x_rows, groups;
+};
+size_t fp8_matmul_workspace(int rows, int groups);
+hipError_t fp8_matmul(const Fp8Gemm& p, const int32_t* offsets, bool out_bf16, void* ws,
+                      hipStream_t s);
+
 // r = sum_k w[t][k] O[inv[t][k]] -> r16 (bf16) and, if r32 != NULL, fp32.
 hipError_t combine(const uint16_t* o, const int32_t* inv, const float* w, int T, int K, int R,
                    uint16_t* r16, float* r32, hipStream_t s);

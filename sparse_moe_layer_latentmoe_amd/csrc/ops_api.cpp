@@ -1,5 +1,5 @@
 // C ABI of the operators around the layer (routing from logits, the norms
-// around a block): argument checks and launches.  See include/lmoe.h for the
+// around a block, 8-bit block-scaled matrices): argument checks and launches.  See include/lmoe.h for the
 // contract.  Every check runs on the host before any HIP call.
 #include <hip/hip_runtime.h>
 
@@ -132,6 +132,50 @@ BlockNormProblem norm_problem(const lmoe_block_norm_args& a) {
           a.eps};
 }
 
+lmoe_status check_quantize(const void* x, int32_t type, int64_t rows, int64_t cols, int64_t stride,
+                           int64_t nscales, const uint8_t* codes, const float* scales) {
+  const int64_t el = type_size(type);
+  if (!x || !codes || !scales || !aligned(x, el) || !aligned(scales, 4))
+    return LMOE_ERR_INVALID_ARG;
+  if (!disjoint({{x, strided(rows, stride, cols, el)}},
+                {{codes, rows * cols}, {scales, nscales * 4}}))
+    return LMOE_ERR_INVALID_ARG;
+  return LMOE_OK;
+}
+
+// Largest element count of an array whose work-groups a launch can number.
+constexpr int64_t kMaxElements = int64_t{1} << 40;
+
+// Host-side checks that do not need the workspace.
+lmoe_status check_fp8(const lmoe_fp8_matmul_args* a) {
+  if (!a) return LMOE_ERR_INVALID_ARG;
+  if (a->M < 0 || a->N <= 0 || a->K <= 0 || a->n_groups < 0 || !is_type(a->y_type) ||
+      (a->M > 0 && a->x_rows < 1))
+    return LMOE_ERR_INVALID_ARG;
+  if (a->N % 16 || a->K % 128 || a->N > (1 << 20) || a->K > kFp8MaxBlocks * 128 ||
+      a->n_groups > 1024 || a->M > (1 << 24))
+    return LMOE_ERR_UNSUPPORTED;
+  if (a->M == 0) return LMOE_OK;
+  if (!a->x || !a->x_scales || !a->w || !a->w_scales || !a->y || !aligned(a->x, 16) ||
+      !aligned(a->w, 16) || !aligned(a->y, 16) || !aligned(a->x_scales, 4) ||
+      !aligned(a->w_scales, 4) || !aligned(a->rows, 4) || !aligned(a->offsets, 4))
+    return LMOE_ERR_INVALID_ARG;
+  if ((a->n_groups > 0) != (a->offsets != nullptr)) return LMOE_ERR_INVALID_ARG;
+  if (!a->rows && a->x_rows < a->M) return LMOE_ERR_INVALID_ARG;
+  if (a->rows && static_cast<int64_t>(a->x_rows) * a->K >= (int64_t{1} << 31))
+    return LMOE_ERR_UNSUPPORTED;
+  const int64_t G = a->n_groups ? a->n_groups : 1, kb = a->K / 128, nb = (a->N + 127) / 128;
+  if (!disjoint({{a->x, static_cast<int64_t>(a->x_rows) * a->K},
+                 {a->x_scales, a->x_rows * kb * 4},
+                 {a->w, G * a->N * a->K},
+                 {a->w_scales, G * nb * kb * 4},
+                 {a->rows, static_cast<int64_t>(a->M) * 4},
+                 {a->offsets, (G + 1) * 4}},
+                {{a->y, static_cast<int64_t>(a->M) * a->N * type_size(a->y_type)}}))
+    return LMOE_ERR_INVALID_ARG;
+  return LMOE_OK;
+}
+
 lmoe_status status(hipError_t e) { return e == hipSuccess ? LMOE_OK : LMOE_ERR_HIP; }
 
 }  // namespace
@@ -247,6 +291,65 @@ lmoe_status lmoe_block_norm_backward(const lmoe_block_norm_args* a, const float*
                    g->dres_scale, g->dgate};
   return status(block_norm_backward(norm_problem(*a), q, static_cast<float*>(workspace),
                                     static_cast<hipStream_t>(stream)));
+}
+
+lmoe_status lmoe_quantize_fp8(const void* x, int32_t x_type, int64_t rows, int32_t cols,
+                              int64_t x_stride, uint8_t* codes, float* scales, void* stream) {
+  if (rows < 0 || cols <= 0 || !is_type(x_type) || x_stride < cols) return LMOE_ERR_INVALID_ARG;
+  if (rows > kMaxElements / cols || x_stride > (int64_t{1} << 31)) return LMOE_ERR_UNSUPPORTED;
+  if (rows == 0) return LMOE_OK;
+  const int64_t nb = (static_cast<int64_t>(cols) + 127) / 128;
+  if (rows * nb > (int64_t{1} << 34)) return LMOE_ERR_UNSUPPORTED;
+  const lmoe_status st =
+      check_quantize(x, x_type, rows, cols, x_stride, rows * nb, codes, scales);
+  if (st != LMOE_OK) return st;
+  return status(fp8_quantize(x, x_type == LMOE_BF16, rows, cols, x_stride, codes, scales,
+                             static_cast<hipStream_t>(stream)));
+}
+
+lmoe_status lmoe_quantize_fp8_weight(const void* w, int32_t w_type, int64_t matrices, int32_t rows,
+                                     int32_t cols, uint8_t* codes, float* scales, void* stream) {
+  if (matrices < 0 || rows <= 0 || cols <= 0 || !is_type(w_type)) return LMOE_ERR_INVALID_ARG;
+  const int64_t nb = ((static_cast<int64_t>(rows) + 127) / 128) *
+                     ((static_cast<int64_t>(cols) + 127) / 128);
+  if (matrices > (int64_t{1} << 30) / nb) return LMOE_ERR_UNSUPPORTED;
+  if (matrices == 0) return LMOE_OK;
+  const lmoe_status st =
+      check_quantize(w, w_type, matrices * rows, cols, cols, matrices * nb, codes, scales);
+  if (st != LMOE_OK) return st;
+  return status(fp8_quantize_weight(w, w_type == LMOE_BF16, matrices, rows, cols, codes, scales,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+size_t lmoe_fp8_matmul_workspace_size(const lmoe_fp8_matmul_args* a) {
+  if (check_fp8(a) != LMOE_OK || a->M == 0) return 0;
+  return fp8_matmul_workspace(a->M, a->n_groups);
+}
+
+lmoe_status lmoe_fp8_matmul(const lmoe_fp8_matmul_args* a, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  const lmoe_status st = check_fp8(a);
+  if (st != LMOE_OK) return st;
+  if (a->M == 0) return LMOE_OK;
+  const size_t need = fp8_matmul_workspace(a->M, a->n_groups);
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return LMOE_ERR_WORKSPACE;
+  const int64_t G = a->n_groups ? a->n_groups : 1, kb = a->K / 128, nb = (a->N + 127) / 128;
+  if (!disjoint({{a->x, static_cast<int64_t>(a->x_rows) * a->K},
+                 {a->x_scales, a->x_rows * kb * 4},
+                 {a->w, G * a->N * a->K},
+                 {a->w_scales, G * nb * kb * 4},
+                 {a->rows, static_cast<int64_t>(a->M) * 4},
+                 {a->offsets, (G + 1) * 4},
+                 {a->y, static_cast<int64_t>(a->M) * a->N * type_size(a->y_type)}},
+                {{workspace, static_cast<int64_t>(need)}}))
+    return LMOE_ERR_INVALID_ARG;
+  const Fp8Gemm p{a->x,    a->x_scales, a->w,
+                  a->w_scales, a->rows, a->y,
+                  a->M,    a->N,        a->K,
+                  a->K / 128, (a->N + 127) / 128, a->x_rows, a->n_groups};
+  return status(fp8_matmul(p, a->offsets, a->y_type == LMOE_BF16, workspace,
+                           static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

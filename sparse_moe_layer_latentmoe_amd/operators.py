@@ -1,5 +1,7 @@
 """The operators around the layer: routing from given logits and the norms
-around a block, each with its gradient.
+around a block, each with its gradient, and matrices in 8-bit floating point
+(e4m3) with a scale for each block of 128, with their dense and grouped
+products.
 
 Thin wrappers over the C ABI (``include/lmoe.h``), like the rest of the
 binding: they check tensors, allocate the outputs and marshal pointers; the
@@ -49,16 +51,27 @@ class LmoeBlockNormGrads(ctypes.Structure):
         "dh", "dy", "dpre_weight", "dpost_weight", "dres_scale", "dgate")]
 
 
+class LmoeFp8MatmulArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "x", "x_scales", "w", "w_scales", "rows", "offsets", "y")] + [
+        (n, ctypes.c_int32) for n in ("y_type", "n_groups", "M", "x_rows", "N", "K")]
+
+
 def declare(lib: ctypes.CDLL) -> None:
     """Declare the C signatures of this module's entry points."""
     P, I, L, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-    R, A, G = (ctypes.POINTER(t) for t in (LmoeRouter, LmoeBlockNormArgs, LmoeBlockNormGrads))
+    R, A, G, M = (ctypes.POINTER(t) for t in (LmoeRouter, LmoeBlockNormArgs, LmoeBlockNormGrads,
+                                              LmoeFp8MatmulArgs))
     for name, args, res in (
             ("lmoe_route_logits", [R, P, I, L, P, I, P, P, P], ctypes.c_int),
             ("lmoe_route_logits_backward", [R, P, I, L, P, P, I, P, P], ctypes.c_int),
             ("lmoe_block_norm", [A, P, P, P, P], ctypes.c_int),
             ("lmoe_block_norm_workspace_size", [A, G], Z),
-            ("lmoe_block_norm_backward", [A, P, P, P, G, P, Z, P], ctypes.c_int)):
+            ("lmoe_block_norm_backward", [A, P, P, P, G, P, Z, P], ctypes.c_int),
+            ("lmoe_quantize_fp8", [P, I, L, I, L, P, P, P], ctypes.c_int),
+            ("lmoe_quantize_fp8_weight", [P, I, L, I, I, P, P, P], ctypes.c_int),
+            ("lmoe_fp8_matmul_workspace_size", [M], Z),
+            ("lmoe_fp8_matmul", [M, P, Z, P], ctypes.c_int)):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
 
@@ -283,3 +296,90 @@ def block_norm_backward(h, y, stats, dh_out=None, dx=None, pre_weight=None, post
         _done(lib.lmoe_block_norm_backward(a, _ptr(stats), _ptr(dh_out), _ptr(dx), out, _ptr(ws),
                                            nbytes, s), "lmoe_block_norm_backward")
     return g
+
+
+# ---- 8-bit floating point ----------------------------------------------------
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def quantize_fp8(x, stream=None):
+    """(codes float8_e4m3fn [T, K], scales fp32 [T, ceil(K / 128)]) of
+    activations x [T, K] (fp32 or bf16, rows may be strided): each block of
+    128 values of a row has its own scale."""
+    _check(x, "x", _TYPE, ndim=2, dense=False)
+    T, K = x.shape
+    with _launch(x.device, stream) as s:
+        codes = torch.empty((T, K), dtype=_E4M3, device=x.device)
+        scales = torch.empty((T, (K + 127) // 128), dtype=torch.float32, device=x.device)
+        _done(load_library().lmoe_quantize_fp8(_ptr(x), _TYPE[x.dtype], T, K, _row_stride(x),
+                                               _ptr(codes), _ptr(scales), s),
+              "lmoe_quantize_fp8")
+    return codes, scales
+
+
+def quantize_fp8_weight(w, stream=None):
+    """(codes float8_e4m3fn like w, scales fp32 [..., ceil(N / 128),
+    ceil(K / 128)]) of weights w [..., N, K] (fp32 or bf16): each 128 x 128
+    block of a matrix has its own scale."""
+    _check(w, "w", _TYPE)
+    if w.dim() < 2:
+        raise ValueError(f"w: {w.dim()} dimensions, expected at least 2")
+    N, K = w.shape[-2:]
+    lead = tuple(w.shape[:-2])
+    n = w.numel() // (N * K) if N and K else 0
+    with _launch(w.device, stream) as s:
+        codes = torch.empty(w.shape, dtype=_E4M3, device=w.device)
+        scales = torch.empty((*lead, (N + 127) // 128, (K + 127) // 128), dtype=torch.float32,
+                             device=w.device)
+        _done(load_library().lmoe_quantize_fp8_weight(_ptr(w), _TYPE[w.dtype], n, N, K,
+                                                      _ptr(codes), _ptr(scales), s),
+              "lmoe_quantize_fp8_weight")
+    return codes, scales
+
+
+def fp8_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=torch.bfloat16,
+               out=None, stream=None):
+    """y [M, N] = x w^T of quantised matrices (quantize_fp8, quantize_fp8_weight).
+
+    x [X, K], w [N, K]; K a multiple of 128, N of 16.  ``rows`` (int32 [M]):
+    row m of y reads x's row rows[m] (else row m).  ``offsets`` (int32
+    [G + 1], ascending) with w [G, N, K]: rows offsets[g] .. offsets[g + 1] - 1
+    take matrix g; rows of no group are not written (pass ``out`` to keep what
+    they hold).  out_dtype: bf16 or fp32."""
+    e4m3, f32 = (_E4M3,), (torch.float32,)
+    _check(x, "x", e4m3, ndim=2)
+    dev = x.device
+    X, K = x.shape
+    _check(w, "w", e4m3, ndim=2 if offsets is None else 3, device=dev)
+    N = w.shape[-2]
+    if w.shape[-1] != K:
+        raise ValueError(f"w: {w.shape[-1]} columns, x has {K}")
+    kb = (K + 127) // 128
+    _check(x_scales, "x_scales", f32, shape=(X, kb), device=dev)
+    _check(w_scales, "w_scales", f32, shape=(*w.shape[:-2], (N + 127) // 128, kb), device=dev)
+    i32 = (torch.int32,)
+    if offsets is not None:
+        if w.shape[0] < 1:
+            raise ValueError("w: no groups")
+        _check(offsets, "offsets", i32, shape=(w.shape[0] + 1,), device=dev)
+    M = X
+    if rows is not None:
+        _check(rows, "rows", i32, ndim=1, device=dev)
+        M = rows.shape[0]
+    if out is not None:
+        _check(out, "out", _TYPE, shape=(M, N), device=dev)
+    elif out_dtype not in _TYPE:
+        raise TypeError(f"out_dtype: {out_dtype}, expected torch.bfloat16 or torch.float32")
+    lib = load_library()
+    with _launch(dev, stream) as s:
+        y = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
+        a = LmoeFp8MatmulArgs(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(rows),
+                              _ptr(offsets), _ptr(y), _TYPE[y.dtype],
+                              0 if offsets is None else w.shape[0], M, X, N, K)
+        ws, nbytes = None, 0
+        if offsets is not None:
+            nbytes = int(lib.lmoe_fp8_matmul_workspace_size(a))
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        _done(lib.lmoe_fp8_matmul(a, _ptr(ws), nbytes, s), "lmoe_fp8_matmul")
+    return y
