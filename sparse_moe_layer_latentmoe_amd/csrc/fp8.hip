@@ -388,32 +388,43 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
   }
 }
 
-// Many tokens: the half-step pipeline of the bf16 GEMM (lds_pipe_kernel in
-// gemm_tiled.hip) on rows of 128 bytes = one block of k.  Half-step s = 2 kb
-// + h multiplies block kb of the token rows with half h of the block's weight
-// rows; copy units (a weight half, plus the token rows and their scales when
-// h = 0) are issued three half-steps ahead, so the copy stream never drains.
-// Four half-steps are written out, so that every LDS address is a constant,
-// and all but the last few run without conditions.
-// Eight waves, WM along tokens x 8 / WM along weights.  The weight scales of
-// the whole tile are read into LDS once.
-template <bool GROUPED, int BM, int BN, int WM, class OUT>
+// Many tokens: MFMA tiles of BM token rows x BN weight rows fed through LDS by
+// direct global -> LDS copies.  One step is a block of k (128 bytes of a row)
+// in two halves of the block's weight rows; each wave owns 16 TM token rows
+// and 16 TH weight rows of each half, and holds the fragments it multiplies
+// in registers.  A fragment's registers are read anew from LDS, for the next
+// half, right after their last use, so no LDS read is waited for at the top
+// of a step.  During step kb, LDS holds what is read in it (weight half 1 of
+// kb, half 0 of kb + 1, token rows of kb + 1), and copies run into the places
+// of what step kb - 1 read: token rows of kb + 2 and, with a ring of WD
+// blocks of weights, half 1 of block kb + WD - 1 and half 0 of kb + WD.  One
+// barrier a step; the copy instructions are spread over the MFMAs.  Expert
+// weights come from HBM and take WD = 3 (the copies of the last step may
+// still be in flight at the barrier), dense ones mostly from L2.
+//
+// Scales: the tile's weight scales are read into LDS once.  Token scales come
+// eight blocks of k at a time (32 bytes of a row of scales), an eighth of the
+// rows with each token block: one block at a time, every 4-byte load was a
+// cache line of its own, half as many line requests as the data itself.
+template <bool GROUPED, int BM, int BN, int WM, int WD, class OUT>
 __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tiles,
                                               const int* ntiles) {
   constexpr int BH = BN / 2, WN = 8 / WM, NW = 8;
   constexpr int TM = BM / WM / 16, TH = BH / WN / 16;
   constexpr int RPI = 8, ROWB = 128;
-  constexpr int NIA = BM / RPI / NW, NIH = BH / RPI / NW, NI0 = NIA + 1 + NIH;
-  constexpr int L = 3, NBUF = L + 1;  // copy units in flight, weight-half buffers
+  constexpr int NIA = BM / RPI / NW, NIH = BH / RPI / NW;  // copies a wave and unit
   constexpr int ABUF = BM * ROWB, HBUF = BH * ROWB;
   constexpr int NSB = BN / 128;  // scale blocks of the tile's weight rows
   static_assert(NIA * RPI * NW == BM && NIH * RPI * NW == BH && BM % 64 == 0, "rows per unit");
   // One LDS array: with several, the compiler tells them apart and then waits
   // for all copies in flight before every LDS read.
-  constexpr int XS0 = 2 * ABUF + NBUF * HBUF, WS0 = XS0 + 2 * BM * 4;
-  __shared__ __attribute__((aligned(1024))) char smem[WS0 + NSB * kFp8MaxBlocks * 4];
-  float* const sxs = reinterpret_cast<float*>(smem + XS0);  // [2][BM] token scales
+  constexpr int W00 = 2 * ABUF, XS0 = W00 + 2 * WD * HBUF, WS0 = XS0 + 2 * BM * 32;
+  constexpr int SO0 = WS0 + NSB * kFp8MaxBlocks * 4, LDS = SO0 + BM * 4;
+  static_assert(LDS <= 160 * 1024, "LDS");
+  __shared__ __attribute__((aligned(1024))) char smem[LDS];
+  float* const sxs = reinterpret_cast<float*>(smem + XS0);  // [2][BM][8] token scales
   float* const sws = reinterpret_cast<float*>(smem + WS0);  // [NSB][blocks] weight scales
+  uint32_t* const sso = reinterpret_cast<uint32_t*>(smem + SO0);  // [BM] rows' scale offsets
 
   int tm, nb;
   const int nblocks = (p.N + BN - 1) / BN;
@@ -432,12 +443,12 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
   const int w = uniform(threadIdx.x >> 6);
   const int wm = w / WN, wn = w % WN;
   const int K = p.K, KB = p.KB;
-  const int nsub = 2 * KB;
 
   // Copy sources: instruction j of wave w fills rows RPI (w + NW j) .. + 7 of
   // its buffer, written already swizzled (16-byte chunk c of row r in place
-  // c ^ (r / 2) % 8); token rows past the tile's count read its first row,
-  // weight rows past N the last one.
+  // c ^ (r / 2) % 8).  Token rows past the tile's count read its first row;
+  // weight rows past N read on into the next matrix, or past the last one,
+  // where the buffer's bound makes them 0 (their columns are not stored).
   const int lr = lane >> 3;
   const int sw = ((4 * (w & 1)) + (lr >> 1)) & 7;
   const uint32_t chunk = (uint32_t)(((lane & 7) ^ sw) * 16);
@@ -449,64 +460,100 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
     ok = true;
     return gather ? (uint32_t)fp8_x_row(p, m0 + m, ok) : (uint32_t)m;
   };
-  const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(xbase), rs = buffer_rsrc(xsbase);
-  const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.w + ((size_t)e * p.N + n0) * K);
-  uint32_t ao[NIA], bo[2][NIH];
+  const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(xbase);
+  const __amdgpu_buffer_rsrc_t rs =
+      buffer_rsrc(xsbase, ((size_t)p.x_rows - (gather ? 0 : m0)) * KB * 4);
+  const size_t w0 = ((size_t)e * p.N + n0) * K;
+  const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(
+      p.w + w0, (size_t)(GROUPED ? p.groups : 1) * p.N * K - w0);
+  uint32_t ao[NIA], bo = (uint32_t)lr * (uint32_t)K + chunk;
 #pragma unroll
   for (int j = 0; j < NIA; ++j) {
     bool ok;
     ao[j] = x_row(RPI * (w + NW * j) + lr, ok) * (uint32_t)K + chunk;
+    asm volatile("" : "+v"(ao[j]));  // one register: not half of a 64-bit product
   }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int j = 0; j < NIH; ++j)
-      bo[h][j] = (uint32_t)(min(n0 + h * BH + RPI * (w + NW * j) + lr, p.N - 1) - n0) *
-                     (uint32_t)K + chunk;
-  // token scales: 64 a wave and instruction (waves beyond BM / 64 repeat)
-  const int sg = w % (BM / 64);
-  bool dummy;
-  const uint32_t so = x_row(sg * 64 + lane, dummy) * (uint32_t)KB * 4u;
+  asm volatile("" : "+v"(bo));
+  for (int i = threadIdx.x; i < BM; i += 512) {
+    bool ok;
+    sso[i] = x_row(i, ok) * (uint32_t)KB * 4u;
+  }
 
-  // copy unit u (half H of block u / 2, into weight buffer WB)
-  auto issue = [&](auto h_c, auto wb_c, int u) __attribute__((always_inline)) {
-    constexpr int H = decltype(h_c)::value, WB = decltype(wb_c)::value & 3, AB = WB >> 1;
-    const int kb = u >> 1;
-    if constexpr (H == 0) {
-      char* st = smem + AB * ABUF;
-#pragma unroll
-      for (int j = 0; j < NIA; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (w + NW * j) * RPI * ROWB),
-                                                 16, ao[j], kb * ROWB, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(sxs + AB * BM + sg * 64), 4, so, kb * 4,
-                                               0, 0);
-    }
-    char* st = smem + 2 * ABUF + WB * HBUF;
-#pragma unroll
-    for (int j = 0; j < NIH; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(st + (w + NW * j) * RPI * ROWB), 16,
-                                               bo[H][j], kb * ROWB, 0, 0);
+  // copy instruction j of token block kb, of weight half h of block kb
+  auto copy_x = [&](int kb, int j) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        ra, (lds_void*)(smem + (kb & 1) * ABUF + (w + NW * j) * RPI * ROWB), 16, ao[j], kb * ROWB,
+        0, 0);
   };
-  using C0 = std::integral_constant<int, 0>;
-  using C1 = std::integral_constant<int, 1>;
-  using C2 = std::integral_constant<int, 2>;
-  using C3 = std::integral_constant<int, 3>;
-  issue(C0{}, C0{}, 0);
-  issue(C1{}, C1{}, 1);
-  if (nsub > 2) issue(C0{}, C2{}, 2);
-  // the tile's weight scales, written to LDS before the first barrier
-  for (int i = threadIdx.x; i < NSB * KB; i += 512) {
-    const int b = i / KB, k = i - b * KB;
-    sws[b * kFp8MaxBlocks + k] =
-        p.ws[((size_t)e * p.NB + min(n0 / 128 + b, p.NB - 1)) * KB + k];
+  // (to ring offset r)
+  auto copy_w = [&](int kb, int h, int r, int j) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rb, (lds_void*)(smem + W00 + r + h * HBUF + (w + NW * j) * RPI * ROWB), 16, bo,
+        kb * ROWB + (h * BH + (w + NW * j) * RPI) * K, 0, 0);
+  };
+  // Token scales of blocks 8 g .. 8 g + 7: instruction i fills rows 8 i .. + 7,
+  // lane l row 8 i + l / 8, place l % 8, which holds block (l % 8) ^ 4 (i % 2)
+  // of the eight (so that 16 rows' reads of one block meet no bank twice).
+  // Eighth j of a group is BM / 64 instructions, one a wave (some twice).
+  // Blocks past K read the next row's scales, or 0 past the last one's;
+  // nothing uses them.
+  const int sg = w % (BM / 64);
+  auto xs_row = [&](int j) __attribute__((always_inline)) {
+    return sso[8 * (j * (BM / 64) + sg) + lr];
+  };
+  auto copy_xs = [&](int g, int j, uint32_t row) __attribute__((always_inline)) {
+    const int i = j * (BM / 64) + sg;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs, (lds_void*)(sxs + ((g & 1) * BM + 8 * i) * 8), 4,
+        row + (uint32_t)(((lane & 7) ^ ((i & 1) << 2)) * 4), g * 32, 0, 0);
+  };
+  // weight scales of the tile: wave w takes 64 blocks of one of its 128-row
+  // blocks (places past K hold what follows in memory, or 0 past its end)
+  {
+    static_assert(NSB * (kFp8MaxBlocks / 64) <= NW, "a wave for each 64 scales");
+    const size_t ws0 = ((size_t)e * p.NB + n0 / 128) * KB;
+    const __amdgpu_buffer_rsrc_t rws =
+        buffer_rsrc(p.ws + ws0, ((size_t)(GROUPED ? p.groups : 1) * p.NB * KB - ws0) * 4);
+    const int b = w % NSB, i = w / NSB;
+    if (i < kFp8MaxBlocks / 64)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rws, (lds_void*)(sws + b * kFp8MaxBlocks + i * 64), 4, lane * 4, (b * KB + i * 64) * 4, 0,
+          0);
   }
+  // what the first MFMAs need, then what step 0 reads, then what it need not
+  // wait for
+  constexpr int R = 2 * HBUF;  // a block's place in the ring of weights
+#pragma unroll
+  for (int j = 0; j < NIA; ++j) copy_x(0, j);
+#pragma unroll
+  for (int j = 0; j < NIH; ++j) copy_w(0, 0, 0, j);
   wait_lgkmcnt0();
+  stage_barrier_hard();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) copy_xs(0, j, xs_row(j));
+#pragma unroll
+  for (int j = 0; j < NIH; ++j) copy_w(0, 1, 0, j);
+  if (KB > 1) {
+#pragma unroll
+    for (int j = 0; j < NIH; ++j) copy_w(1, 0, R, j);
+#pragma unroll
+    for (int j = 0; j < NIA; ++j) copy_x(1, j);
+    copy_xs(1, 0, xs_row(0));
+    if constexpr (WD == 3) {
+#pragma unroll
+      for (int j = 0; j < NIH; ++j) copy_w(1, 1, R, j);
+      if (KB > 2) {
+#pragma unroll
+        for (int j = 0; j < NIH; ++j) copy_w(2, 0, 2 * R, j);
+      }
+    }
+  }
 
   const int r16 = lane & 15, kq = lane >> 4;
   const uint32_t l0 = r16 * ROWB + (((0 + kq) ^ (r16 >> 1)) << 4);
   const uint32_t l1 = r16 * ROWB + (((4 + kq) ^ (r16 >> 1)) << 4);
   const uint32_t aw = (uint32_t)(wm * (BM / WM)) * ROWB;
-  const uint32_t bw = (uint32_t)(wn * (BH / WN)) * ROWB;
+  const uint32_t bw = (uint32_t)(W00 + wn * (BH / WN) * ROWB);
   // scale block of this wave's weight rows in each half
   const float* const wsl[2] = {sws + (wn * (BH / WN)) / 128 * kFp8MaxBlocks,
                                sws + (BH + wn * (BH / WN)) / 128 * kFp8MaxBlocks};
@@ -515,8 +562,6 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
   for (int a = 0; a < 2 * TH; ++a)
 #pragma unroll
     for (int b = 0; b < TM; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  i32x8 xf[TM];  // token fragments of the current block of k, and their scales
-  float xs[TM];
   uint32_t live = 0;  // token groups whose row index was in range
 #pragma unroll
   for (int t = 0; t < TM; ++t) {
@@ -525,73 +570,111 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
     live |= (uint32_t)ok << t;
   }
 
-  // half-step s with s % 4 = S4; MORE: units s + 1 .. s + L all exist
-  auto half_step = [&](auto s4_c, auto more_c, int s) __attribute__((always_inline)) {
-    constexpr int S4 = decltype(s4_c)::value, H = S4 & 1, AB = S4 >> 1;
-    constexpr bool MORE = decltype(more_c)::value;
-    // unit s has landed: at most units s + 1 and s + 2 are still in flight
-    if (MORE || s + 2 < nsub) wait_vmcnt<NI0 + NIH>();
-    else if (H == 0 && s + 1 < nsub) wait_vmcnt<NIH>();
-    else wait_vmcnt<0>();
-    stage_barrier_hard();
-    if (MORE || s + L < nsub)
-      issue(std::integral_constant<int, H ^ 1>{}, std::integral_constant<int, (S4 + L) & 3>{},
-            s + L);
-    const int kb = s >> 1;
-    if constexpr (H == 0) {
-      const char* st = smem + AB * ABUF + aw;
-#pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        xf[t] = join(*reinterpret_cast<const i32x4*>(st + l0 + t * 16 * ROWB),
-                     *reinterpret_cast<const i32x4*>(st + l1 + t * 16 * ROWB));
-        const float v = sxs[AB * BM + wm * (BM / WM) + t * 16 + r16];
-        xs[t] = (live >> t) & 1 ? v : 0.f;
-      }
-    }
-    const char* st = smem + 2 * ABUF + S4 * HBUF + bw;
-    i32x8 wf[TH];
-#pragma unroll
-    for (int g = 0; g < TH; ++g)
-      wf[g] = join(*reinterpret_cast<const i32x4*>(st + l0 + g * 16 * ROWB),
-                   *reinterpret_cast<const i32x4*>(st + l1 + g * 16 * ROWB));
-    const float ws = wsl[H][kb];
-    // the products run AHEAD MFMAs ahead of their scaling
-    constexpr int NP = TM * TH, AHEAD = 3;
-    f32x4 q[AHEAD];
-    float f = 0.f;
-#pragma unroll
-    for (int i = 0; i < NP + AHEAD; ++i) {
-      if (i >= AHEAD) {
-        const int t = (i - AHEAD) / TH, g = (i - AHEAD) % TH;
-        if (g == 0) f = xs[t] * ws;
-        acc[H * TH + g][t] += q[i % AHEAD] * f;
-        // keeps the scaling here: it must not sink past the barrier, where
-        // all of the half-step's products would be live at once
-        asm volatile("" : "+v"(acc[H * TH + g][t]));
-      }
-      if (i < NP) q[i % AHEAD] = mfma_fp8(wf[i % TH], xf[i / TH]);
-    }
+  // fragments: token group t of block kb, weight group g at ring offset r
+  auto read_x = [&](int kb, int t) __attribute__((always_inline)) {
+    const char* st = smem + (kb & 1) * ABUF + aw + t * 16 * ROWB;
+    return join(*reinterpret_cast<const i32x4*>(st + l0), *reinterpret_cast<const i32x4*>(st + l1));
   };
-  int s = 0;
-  for (; s + 3 + L < nsub; s += 4) {
-    half_step(C0{}, std::true_type{}, s);
-    half_step(C1{}, std::true_type{}, s + 1);
-    half_step(C2{}, std::true_type{}, s + 2);
-    half_step(C3{}, std::true_type{}, s + 3);
-  }
-  for (; s < nsub; s += 4) {
-    half_step(C0{}, std::false_type{}, s);
-    half_step(C1{}, std::false_type{}, s + 1);
-    if (s + 2 < nsub) {
-      half_step(C2{}, std::false_type{}, s + 2);
-      half_step(C3{}, std::false_type{}, s + 3);
-    }
-  }
+  auto read_w = [&](int r, int g) __attribute__((always_inline)) {
+    const char* st = smem + bw + r + g * 16 * ROWB;
+    return join(*reinterpret_cast<const i32x4*>(st + l0), *reinterpret_cast<const i32x4*>(st + l1));
+  };
+  auto read_xs = [&](int kb, int t) __attribute__((always_inline)) {
+    const int row = wm * (BM / WM) + t * 16 + r16;
+    const float x = sxs[(((kb >> 3) & 1) * BM + row) * 8 + ((kb & 7) ^ ((row >> 1) & 4))];
+    return (live >> t) & 1 ? x : 0.f;
+  };
+  i32x8 xf[TM], wf[TH];  // the current half's fragments
+  float xs[TM];          // and the block's token scales
 
-  const int wr = wm * (BM / WM);
+  int r0 = 0;  // ring offset of block kb
+  // Step kb.  COPY: 2 copies everything (kb + WD < KB), 1 all but the weights
+  // of block kb + WD (the last step with copies), 0 nothing.
+  auto step = [&](auto copy_c, int kb) __attribute__((always_inline)) {
+    constexpr int COPY = decltype(copy_c)::value;
+    const int r1 = r0 + R == WD * R ? 0 : r0 + R;
+    const int r2 = r1 + R == WD * R ? 0 : r1 + R;  // r0 when WD = 2
+    // what this step reads has landed (with WD = 3 the weight copies of the
+    // last step may be in flight), and this wave's LDS reads of the last step
+    // are done; then the same for every wave
+    if (WD == 3 && COPY) wait_vmcnt<2 * NIH>();
+    else wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    stage_barrier_hard();
+    // the scales with token block n = kb + 2 are eighth (n - 1) % 8 of the
+    // group that block n + 7 lies in, whose last eighth so comes with its
+    // first block
+    constexpr bool XC = COPY == 2 || (COPY == 1 && WD == 3);  // block kb + 2 exists
+    constexpr int NX = XC ? NIA + 1 : 0;
+    constexpr int NC = NX + (COPY == 2 ? 2 * NIH : (COPY == 1 ? NIH : 0));
+    uint32_t xrow = 0;
+    if constexpr (XC) xrow = xs_row((kb + 1) & 7);
+    // in the order they are waited for; with WD = 2 that is the same barrier
+    // for all, and weights first, the larger part, measured 3% faster
+    constexpr int X0 = WD == 2 ? NC - NX : 0, W0 = WD == 2 ? 0 : NX;
+    auto copy = [&](int c) __attribute__((always_inline)) {
+      if (c >= X0 && c < X0 + NX - 1) copy_x(kb + 2, c - X0);
+      else if (c >= X0 && c < X0 + NX) copy_xs((kb + 9) >> 3, (kb + 1) & 7, xrow);
+      else if (c < W0 + NIH) copy_w(kb + WD - 1, 1, WD == 2 ? r1 : r2, c - W0);
+      else copy_w(kb + WD, 0, r0, c - W0 - NIH);
+    };
+    float f[2][TM];
+    const float s0 = wsl[0][kb], s1 = wsl[1][kb];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      f[0][t] = xs[t] * s0;
+      f[1][t] = xs[t] * s1;
+    }
+    // the products run LAG MFMAs ahead of their scaling
+    constexpr int NP = TM * TH, LAG = 3;
+    // a copy after every other MFMA, or each where there are few
+    constexpr int EVERY = NC <= NP ? 2 : 1;
+    static_assert(NC <= 2 * NP, "copies");
+    f32x4 q[LAG];
+#pragma unroll
+    for (int i = 0; i < 2 * NP + LAG; ++i) {
+      if (i >= LAG) {
+        const int j = i - LAG, h = j / NP, g = j % NP / TM, t = j % TM;
+        acc[h * TH + g][t] += q[j % LAG] * f[h][t];
+        // keeps the scaling here: it must not sink past the barrier, where
+        // all of the step's products would be live at once
+        asm volatile("" : "+v"(acc[h * TH + g][t]));
+      }
+      if (i < 2 * NP) {
+        const int h = i / NP, g = i % NP / TM, t = i % TM;
+        q[i % LAG] = mfma_fp8(wf[g], xf[t]);
+        if (t == TM - 1) wf[g] = read_w(h == 0 ? r0 + HBUF : r1, g);
+        if (h == 1 && g == TH - 1) xf[t] = read_x(kb + 1, t);
+        if (i % EVERY == 0 && i / EVERY < NC) copy(i / EVERY);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int t = 0; t < TM; ++t) xs[t] = read_xs(kb + 1, t);
+    r0 = r1;
+  };
+  if (KB > 2) wait_vmcnt<(WD == 3 ? 4 : 2) * NIH + NIA + 1>();
+  else wait_vmcnt<0>();
+  stage_barrier_hard();
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+    xf[t] = read_x(0, t);
+    xs[t] = read_xs(0, t);
+  }
+#pragma unroll
+  for (int g = 0; g < TH; ++g) wf[g] = read_w(0, g);
+  int kb = 0;
+  for (; kb + WD < KB; ++kb) step(std::integral_constant<int, 2>{}, kb);
+  if (kb + WD - 1 < KB) step(std::integral_constant<int, 1>{}, kb++);
+  for (; kb < KB; ++kb) step(std::integral_constant<int, 0>{}, kb);
+  // the last step read ahead (values that are not used): let the reads end
+  // before the buffers are written below
+  wait_lgkmcnt0();
+  stage_barrier_hard();
+
+  const int mr = wm * (BM / WM);
   if constexpr (std::is_same<OUT, uint16_t>::value) {
-    // bf16 rows through LDS (staged_store), in the token buffers: their last
-    // readers passed the last half-step's barrier, and every copy has landed
+    // bf16 rows through LDS (staged_store), in the token buffers
     struct Out {
       const Fp8Gemm& p;
       __device__ u16x4 pack4(f32x4 v) const { return pack4_bf16(v); }
@@ -604,24 +687,24 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
     static_assert(NW * REG <= 2 * ABUF, "staging room");
     char* const reg = smem + w * REG;
     const Out out{p};
-    staged_store<TH, 0>(out, reg, lane, acc, m0 + wr, mcount - wr, n0 + wn * (BH / WN));
-    staged_store<TH, TH>(out, reg, lane, acc, m0 + wr, mcount - wr, n0 + BH + wn * (BH / WN));
+    staged_store<TH, 0>(out, reg, lane, acc, m0 + mr, mcount - mr, n0 + wn * (BH / WN));
+    staged_store<TH, TH>(out, reg, lane, acc, m0 + mr, mcount - mr, n0 + BH + wn * (BH / WN));
   } else {
 #pragma unroll
     for (int g = 0; g < 2 * TH; ++g)
 #pragma unroll
       for (int t = 0; t < TM; ++t) {
-        const int i = wr + t * 16 + r16;
+        const int i = mr + t * 16 + r16;
         const int n = n0 + (g / TH) * BH + wn * (BH / WN) + (g % TH) * 16;
         if (i < mcount && n < p.N) fp8_store4<OUT>(p, m0 + i, n + kq * 4, acc[g][t]);
       }
   }
 }
 
-template <bool GROUPED, int BM, int BN, int WM, class OUT>
+template <bool GROUPED, int BM, int BN, int WM, int WD, class OUT>
 __global__ __launch_bounds__(512) void fp8_pipe_kernel(Fp8Gemm p, const Tile* tiles,
                                                        const int* ntiles) {
-  fp8_pipe_body<GROUPED, BM, BN, WM, OUT>(p, tiles, ntiles);
+  fp8_pipe_body<GROUPED, BM, BN, WM, WD, OUT>(p, tiles, ntiles);
 }
 
 // ---- launchers ---------------------------------------------------------------------
@@ -654,7 +737,7 @@ hipError_t launch(const Fp8Gemm& p, const Tile* tiles, const int* ntiles, int ma
     } else {
       constexpr int BN = 256;
       const long grid = kXcds * (((long)max_tiles * ((p.N + BN - 1) / BN) + kXcds - 1) / kXcds);
-      fp8_pipe_kernel<true, kFp8TileM, BN, 2, OUT><<<grid, 512, 0, s>>>(p, tiles, ntiles);
+      fp8_pipe_kernel<true, kFp8TileM, BN, 4, 3, OUT><<<grid, 512, 0, s>>>(p, tiles, ntiles);
     }
     return hipGetLastError();
   }
@@ -674,11 +757,14 @@ hipError_t launch(const Fp8Gemm& p, const Tile* tiles, const int* ntiles, int ma
   constexpr int BM = 256, BN = 256;
   const long tot = (long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
   const long grid = kXcds * ((tot + kXcds - 1) / kXcds);
-  fp8_pipe_kernel<false, BM, BN, 4, OUT><<<grid, 512, 0, s>>>(p, nullptr, nullptr);
+  fp8_pipe_kernel<false, BM, BN, 4, 2, OUT><<<grid, 512, 0, s>>>(p, nullptr, nullptr);
   return hipGetLastError();
 }
 
-bool grouped_stream(int rows, int groups) { return rows <= (long)kStreamGroupRows * groups; }
+bool grouped_stream(int rows, int groups, int KB) {
+  return rows <= (long)kStreamGroupRows * groups || KB > kFp8MaxBlocks;
+}
+bool dense_stream(const Fp8Gemm& p) { return p.M <= kStreamRows || p.KB > kFp8MaxBlocks; }
 
 int grouped_tiles(int rows, int groups, int tile_m) {
   return (rows < groups ? rows : groups) + rows / tile_m + 1;
@@ -712,9 +798,9 @@ hipError_t fp8_quantize_weight(const void* w, bool bf16, long matrices, int rows
   return hipGetLastError();
 }
 
-size_t fp8_matmul_workspace(int rows, int groups) {
+size_t fp8_matmul_workspace(int rows, int groups, int KB) {
   if (groups == 0) return 0;
-  const int tile_m = grouped_stream(rows, groups) ? kStreamTileM : kFp8TileM;
+  const int tile_m = grouped_stream(rows, groups, KB) ? kStreamTileM : kFp8TileM;
   return 256 + (size_t)grouped_tiles(rows, groups, tile_m) * sizeof(Tile);
 }
 
@@ -723,9 +809,9 @@ hipError_t fp8_matmul(const Fp8Gemm& p, const int32_t* offsets, bool out_bf16, v
   Tile* tiles = nullptr;
   int32_t* ntiles = nullptr;
   int max_tiles = 0;
-  bool stream = p.M <= kStreamRows;
+  bool stream = dense_stream(p);
   if (p.groups) {
-    stream = grouped_stream(p.M, p.groups);
+    stream = grouped_stream(p.M, p.groups, p.KB);
     const int tile_m = stream ? kStreamTileM : kFp8TileM;
     max_tiles = grouped_tiles(p.M, p.groups, tile_m);
     ntiles = static_cast<int32_t*>(ws);

@@ -125,6 +125,13 @@ __device__ __forceinline__ void stage_barrier_hard() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// The same over `bytes` from `base` (at most 2 GiB of them).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0,
+                                           (int)(bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0),
+                                           0x00020000);
+}
+
 // work_item with the tile list's fields read into scalar registers.
 template <bool GROUPED>
 __device__ __forceinline__ bool work_item_uniform(int nblocks, int mrows, int bm,

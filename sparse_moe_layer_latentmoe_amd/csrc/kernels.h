@@ -149,12 +149,11 @@ hipError_t fp8_quantize(const void* x, bool bf16, long rows, int cols, long stri
                         uint8_t* codes, float* scales, hipStream_t s);
 hipError_t fp8_quantize_weight(const void* w, bool bf16, long matrices, int rows, int cols,
                                uint8_t* codes, float* scales, hipStream_t s);
-// y[m] = x[rows ? rows[m] : m] w^T, K a multiple of 128 (at most kFp8MaxBlocks
-// blocks), N a multiple of 16.  groups = 0: one weight matrix for all M rows;
+// y[m] = x[rows ? rows[m] : m] w^T, K a multiple of 128, N of 16.  groups = 0: one weight matrix for all M rows;
 // else row m takes the matrix of the group whose range offsets[g] ..
 // offsets[g + 1] - 1 holds it (rows of no group are not written).
-constexpr int kFp8MaxBlocks = 512;
-constexpr int kFp8TileM = 128;
+constexpr int kFp8MaxBlocks = 256;  // blocks of k that the LDS-tiled product takes
+constexpr int kFp8TileM = 192;      // rows of a grouped product's tile there
 struct Fp8Gemm {
   const uint8_t* x;     // [x_rows, K]
   const float* xs;      // [x_rows, KB]
@@ -164,7 +163,7 @@ struct Fp8Gemm {
   void* y;              // [M, N], bf16 or fp32
   int M, N, K, KB, NB, x_rows, groups;
 };
-size_t fp8_matmul_workspace(int rows, int groups);
+size_t fp8_matmul_workspace(int rows, int groups, int KB);
 hipError_t fp8_matmul(const Fp8Gemm& p, const int32_t* offsets, bool out_bf16, void* ws,
                       hipStream_t s);
 
