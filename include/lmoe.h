@@ -91,8 +91,17 @@ typedef enum { LMOE_PATH_AUTO = 0, LMOE_PATH_STREAM = 1, LMOE_PATH_TILED = 2 } l
  * to bf16, streaming them for small batches and, for large ones, copying
  * the FP4 codes into the LDS-tiled GEMM's tiles and decoding them right
  * before the MFMAs (the same lmoe_path choice as bf16 weights; R and F must
- * be multiples of 128).  Everything else stays bf16 / fp32. */
-typedef enum { LMOE_EXPERTS_BF16 = 0, LMOE_EXPERTS_MXFP4 = 1 } lmoe_expert_format;
+ * be multiples of 128).  Everything else stays bf16 / fp32.
+ * FP8: the *_fp8 / *_fp8_scale fields, weights as lmoe_quantize_fp8_weight
+ * writes them; the expert projections run on 8-bit activations too: the
+ * latent (from its fp32 values) and the hidden rows relu(.)^2 (from the fp32
+ * sums) are quantised as by lmoe_quantize_fp8, the sums are fp32.  R and F
+ * must be multiples of 128. */
+typedef enum {
+  LMOE_EXPERTS_BF16 = 0,
+  LMOE_EXPERTS_MXFP4 = 1,
+  LMOE_EXPERTS_FP8 = 2
+} lmoe_expert_format;
 
 /* Block steps fused into the layer (bits of lmoe_config.fuse; CH9 §9.3 of
  * the page "Nemotron 3 Ultra 架构深度拆解报告"): the block's pre-norm RMSNorm
@@ -136,6 +145,12 @@ typedef struct {
   const uint8_t *expert_down_scale; /* [E, R, F/32] block scales */
   /* LMOE_FUSE_PRENORM only (may be NULL otherwise): */
   const uint16_t *norm_weight;      /* bf16 [D] RMSNorm weight gamma */
+  /* FP8 experts (expert_format = LMOE_EXPERTS_FP8; else not read), 16-byte
+   * aligned: */
+  const uint8_t *expert_up_fp8;       /* [E, F, R] e4m3 codes */
+  const float *expert_up_fp8_scale;   /* [E, F/128, R/128] block scales */
+  const uint8_t *expert_down_fp8;     /* [E, R, F] e4m3 codes */
+  const float *expert_down_fp8_scale; /* [E, R/128, F/128] block scales */
 } lmoe_weights;
 
 /* Optional device outputs of intermediate values (tests, monitoring).  Any
@@ -383,8 +398,9 @@ typedef struct {
   int32_t K;              /* a multiple of 128, up to 65536 */
 } lmoe_fp8_matmul_args;
 
-/* Bytes of workspace of lmoe_fp8_matmul (the row tiles of each group; 0
- * without groups, or for arguments it refuses).  Pure host function. */
+/* Bytes of workspace of lmoe_fp8_matmul (the row tiles of each group, or the
+ * partial sums of a product split over k; 0 where it needs none, or for
+ * arguments it refuses).  Pure host function. */
 size_t lmoe_fp8_matmul_workspace_size(const lmoe_fp8_matmul_args *a);
 
 /* workspace: 16-byte aligned device memory of that size; calls that may

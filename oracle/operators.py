@@ -203,15 +203,12 @@ def quantize_fp8(x, block_rows: int = 1):
     x = np.asarray(x, np.float32)
     R, C = x.shape
     rb, cb = -(-R // block_rows), -(-C // 128)
-    codes = np.zeros((R, C), np.uint8)
-    scales = np.zeros((rb, cb), np.float32)
-    for i in range(rb):
-        for j in range(cb):
-            s = np.s_[i * block_rows:(i + 1) * block_rows, j * 128:(j + 1) * 128]
-            sc = np.maximum(np.abs(x[s]).max() / np.float32(E4M3_MAX), np.float32(2.0 ** -126))
-            scales[i, j] = sc
-            codes[s] = to_e4m3(x[s] / sc)
-    return codes, scales
+    p = np.zeros((rb * block_rows, cb * 128), np.float32)
+    p[:R, :C] = x
+    p = p.reshape(rb, block_rows, cb, 128)
+    scales = np.maximum(np.abs(p).max((1, 3)) / np.float32(E4M3_MAX), np.float32(2.0 ** -126))
+    codes = to_e4m3(p / scales[:, None, :, None]).reshape(rb * block_rows, cb * 128)
+    return np.ascontiguousarray(codes[:R, :C]), scales
 
 
 def dequantize(codes, scales, block_rows: int = 1):
@@ -239,3 +236,18 @@ def fp8_matmul(xc, xs, wc, ws, offsets=None, rows=None):
             w = dequantize(wc[g], ws[g], 128)
             y[a:b], mag[a:b], done[a:b] = x[a:b] @ w.T, np.abs(x[a:b]) @ np.abs(w).T, True
     return y, mag, done
+
+
+def experts_fp8(z32, idx, w, up, down):
+    """The routed experts with FP8 weights and activations: z quantised from
+    fp32, the hidden rows relu(.)^2 rounded to fp32 and quantised, fp64 sums.
+    ``up[e]`` / ``down[e]``: (codes, scales) of a quantised weight."""
+    z = dequantize(*quantize_fp8(z32))
+    r = np.zeros_like(z)
+    for e in np.unique(idx):
+        tok, pos = np.nonzero(idx == e)
+        u = z[tok] @ dequantize(*up[int(e)], 128).T
+        h = dequantize(*quantize_fp8((np.maximum(u, 0.0) ** 2).astype(np.float32)))
+        r[tok] += np.asarray(w, np.float64)[tok, pos][:, None] * (
+            h @ dequantize(*down[int(e)], 128).T)
+    return r

@@ -29,7 +29,7 @@ LMOE_ERR_SCRATCH = -6
 NOALLOC_SCRATCH_BYTES = 64 << 20      # LMOE_NOALLOC_SCRATCH_BYTES
 
 PATH_AUTO, PATH_STREAM, PATH_TILED = 0, 1, 2
-EXPERTS_BF16, EXPERTS_MXFP4 = 0, 1
+EXPERTS_BF16, EXPERTS_MXFP4, EXPERTS_FP8 = 0, 1, 2
 FUSE_PRENORM, FUSE_RESIDUAL = 1, 2      # lmoe_fuse bits
 FUSE_BLOCK = FUSE_PRENORM | FUSE_RESIDUAL
 
@@ -66,7 +66,8 @@ class LmoeWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "fc1_latent", "router", "router_bias", "expert_up", "expert_down",
         "fc2_latent", "shared_up", "shared_down", "expert_up_mxfp4", "expert_up_scale",
-        "expert_down_mxfp4", "expert_down_scale", "norm_weight")]
+        "expert_down_mxfp4", "expert_down_scale", "norm_weight", "expert_up_fp8",
+        "expert_up_fp8_scale", "expert_down_fp8", "expert_down_fp8_scale")]
 
 
 class LmoeTaps(ctypes.Structure):
@@ -237,6 +238,10 @@ def weight_specs(shape, expert_format: int = EXPERTS_BF16, fuse: int = 0) -> dic
         spec.update(expert_up_mxfp4=((E, F, R // 2), u8), expert_up_scale=((E, F, R // 32), u8),
                     expert_down_mxfp4=((E, R, F // 2), u8),
                     expert_down_scale=((E, R, F // 32), u8))
+    elif expert_format == EXPERTS_FP8:
+        e4m3, nf, nr = torch.float8_e4m3fn, (F + 127) // 128, (R + 127) // 128
+        spec.update(expert_up_fp8=((E, F, R), e4m3), expert_up_fp8_scale=((E, nf, nr), f32),
+                    expert_down_fp8=((E, R, F), e4m3), expert_down_fp8_scale=((E, nr, nf), f32))
     else:
         spec.update(expert_up=((E, F, R), bf16), expert_down=((E, R, F), bf16))
     if fuse & FUSE_PRENORM:

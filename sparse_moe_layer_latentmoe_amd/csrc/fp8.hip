@@ -216,12 +216,27 @@ __device__ __forceinline__ long fp8_x_row(const Fp8Gemm& p, int m, bool& ok) {
   return ok ? r : 0;
 }
 
+// What a product stores: float or uint16_t (bf16) rows of y, or the
+// activation relu(v)^2 quantised again (codes in y, a scale for each 128
+// columns in ys; N a multiple of 128).
+struct Relu2Fp8 {};
+
+// Four values / s as codes.
+__device__ __forceinline__ uint32_t fp8_codes4(f32x4 v, float s) {
+  if (s >= kFastScale) {
+    const float r = 1.0f / s;
+    return fp8_pack4(fp8_ratio(v[0], s, r), fp8_ratio(v[1], s, r), fp8_ratio(v[2], s, r),
+                     fp8_ratio(v[3], s, r));
+  }
+  return fp8_pack4(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
+}
+
 template <class OUT>
 __device__ __forceinline__ void fp8_store4(const Fp8Gemm& p, int m, int n, f32x4 v) {
   OUT* y = static_cast<OUT*>(p.y) + (size_t)m * p.N + n;
   if constexpr (std::is_same<OUT, float>::value)
     *reinterpret_cast<f32x4*>(y) = v;
-  else
+  else if constexpr (std::is_same<OUT, uint16_t>::value)
     store4_bf16(y, v);
 }
 
@@ -244,34 +259,21 @@ __device__ __forceinline__ i32x4 fp8_permute(const i32x4& a, const i32x4& b, int
 // split over the NW waves of a work-group, whose sums are added in LDS in a
 // fixed order.  A wave instruction loads 8 rows x 128 bytes; ds_bpermute
 // moves the pieces to the MFMA's lanes (the layout that the bf16 streaming
-// GEMM measured fastest).  Work-group: 16 RG weight rows x 16 MT token rows.
-template <bool GROUPED, int NW, int MT, int RG, int U, class OUT>
+// GEMM measured fastest).  Work-group: 16 RG weight rows x 16 token rows.
+template <bool GROUPED, int NW, int RG, int U, class OUT>
 __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Tile* tiles,
                                                              const int* ntiles) {
-  constexpr int J = RG * MT;
-  __shared__ f32x4 red[NW > 1 ? NW : 1][J][64];
+  static_assert(RG <= 8, "one scale block");
+  __shared__ f32x4 red[NW][RG][64];
   const int nblocks = (p.N + 16 * RG - 1) / (16 * RG);
-  int nb, tm;
-  if (GROUPED) {
-    nb = blockIdx.x % nblocks;
-    tm = blockIdx.x / nblocks;
-  } else {
-    // the m tiles that share a weight block run back to back on one XCD
-    const int mtiles = (p.M + 16 * MT - 1) / (16 * MT);
-    const int local = blockIdx.x / kXcds;
-    tm = local % mtiles;
-    nb = (local / mtiles) * kXcds + blockIdx.x % kXcds;
-    if (nb >= nblocks) return;
-  }
-  int e = 0, m0, mcount;
+  const int nb = blockIdx.x % nblocks;
+  const int tm = blockIdx.x / nblocks;
+  int e = 0, m0 = 0, mcount = p.M;
   if (GROUPED) {
     if (tm >= *ntiles) return;
     e = uniform(tiles[tm].expert);
     m0 = uniform(tiles[tm].row0);
     mcount = uniform(tiles[tm].nrows);
-  } else {
-    m0 = tm * (16 * MT);
-    mcount = min(16 * MT, p.M - m0);
   }
   const int n0 = nb * (16 * RG);
   const int lane = threadIdx.x & 63;
@@ -292,29 +294,21 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
   }
   // 16 RG rows lie in one scale block (RG <= 8 divides it)
   const float* wsp = p.ws + ((size_t)e * p.NB + n0 / 128) * KB;
-  const uint8_t* xp[MT];
-  const float* xsp[MT];
-  bool xok[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int i = t * 16 + r16;
-    const long row = fp8_x_row(p, m0 + (i < mcount ? i : 0), xok[t]);
-    xp[t] = p.x + row * K + kq * 16;
-    xsp[t] = p.xs + row * KB;
-  }
+  bool xok;
+  const long row = fp8_x_row(p, m0 + (r16 < mcount ? r16 : 0), xok);
+  const uint8_t* xp = p.x + row * K + kq * 16;
+  const float* xsp = p.xs + row * KB;
   const int src0 = (((r16 & 7) << 3) | kq) * 4;
   const int src1 = (((r16 & 7) << 3) | (4 + kq)) * 4;
   const bool lo = r16 < 8;
 
-  f32x4 acc[RG][MT];
+  f32x4 acc[RG];
 #pragma unroll
-  for (int g = 0; g < RG; ++g)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[g][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int g = 0; g < RG; ++g) acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   struct Stage {
-    i32x4 l[U][RG][2], x[U][MT][2];
-    float xs[U][MT], ws[U];
+    i32x4 l[U][RG][2], x[U][2];
+    float xs[U], ws[U];
   };
   auto load = [&](Stage& S, int kb) __attribute__((always_inline)) {
 #pragma unroll
@@ -326,12 +320,9 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
         S.l[u][g][0] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wa[g] + k));
         S.l[u][g][1] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wb[g] + k));
       }
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        S.x[u][t][0] = *reinterpret_cast<const i32x4*>(xp[t] + k);
-        S.x[u][t][1] = *reinterpret_cast<const i32x4*>(xp[t] + k + 64);
-        S.xs[u][t] = xsp[t][kb + u];
-      }
+      S.x[u][0] = *reinterpret_cast<const i32x4*>(xp + k);
+      S.x[u][1] = *reinterpret_cast<const i32x4*>(xp + k + 64);
+      S.xs[u] = xsp[kb + u];
       S.ws[u] = wsp[kb + u];
     }
   };
@@ -339,16 +330,13 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (U > 1 && kb + u >= kend) break;
+      const i32x8 xf = join(S.x[u][0], S.x[u][1]);
+      const float f = (xok ? S.xs[u] : 0.f) * S.ws[u];
 #pragma unroll
       for (int g = 0; g < RG; ++g) {
         const i32x8 wf = join(fp8_permute(S.l[u][g][0], S.l[u][g][1], src0, lo),
                               fp8_permute(S.l[u][g][0], S.l[u][g][1], src1, lo));
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          const f32x4 q = mfma_fp8(wf, join(S.x[u][t][0], S.x[u][t][1]));
-          const float f = (xok[t] ? S.xs[u][t] : 0.f) * S.ws[u];
-          acc[g][t] += q * f;
-        }
+        acc[g] += mfma_fp8(wf, xf) * f;
       }
     }
   };
@@ -363,28 +351,46 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
     }
   }
 
-  if constexpr (NW > 1) {
 #pragma unroll
-    for (int g = 0; g < RG; ++g)
+  for (int g = 0; g < RG; ++g) red[w][g][lane] = acc[g];
+  __syncthreads();
+  if constexpr (std::is_same<OUT, Relu2Fp8>::value) {
+    // the work-group holds a whole block of 128 columns of each row
+    static_assert(RG == 8 && RG % NW == 0, "one scale block");
+    __shared__ float top[NW][16];
+    f32x4 v[RG / NW];
+    float m = 0.f;
 #pragma unroll
-      for (int t = 0; t < MT; ++t) red[w][g * MT + t][lane] = acc[g][t];
-    __syncthreads();
-    for (int j = w; j < J; j += NW) {
-      f32x4 sm = red[0][j][lane];
+    for (int i = 0; i < RG / NW; ++i) {
+      const int g = w + i * NW;
+      v[i] = red[0][g][lane];
 #pragma unroll
-      for (int v = 1; v < NW; ++v) sm += red[v][j][lane];
-      const int g = j / MT, t = j % MT;
-      const int i = t * 16 + r16, n = n0 + g * 16;
-      if (i < mcount && n < p.N) fp8_store4<OUT>(p, m0 + i, n + kq * 4, sm);
+      for (int u = 1; u < NW; ++u) v[i] += red[u][g][lane];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = fmaxf(m, v[i][j] = relu_sq(v[i][j]));
     }
-  } else {
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    if (kq == 0) top[w][r16] = m;
+    __syncthreads();
 #pragma unroll
-    for (int g = 0; g < RG; ++g)
+    for (int u = 0; u < NW; ++u) m = fmaxf(m, top[u][r16]);
+    const float sc = fp8_scale(m);
+    if (r16 < mcount) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int i = t * 16 + r16, n = n0 + g * 16;
-        if (i < mcount && n < p.N) fp8_store4<OUT>(p, m0 + i, n + kq * 4, acc[g][t]);
-      }
+      for (int i = 0; i < RG / NW; ++i)
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + (size_t)(m0 + r16) * p.N + n0 +
+                                     (w + i * NW) * 16 + kq * 4) = fp8_codes4(v[i], sc);
+      if (w == 0 && kq == 0) p.ys[(size_t)(m0 + r16) * p.NB + n0 / 128] = sc;
+    }
+    return;
+  }
+  for (int g = w; g < RG; g += NW) {
+    f32x4 sm = red[0][g][lane];
+#pragma unroll
+    for (int v = 1; v < NW; ++v) sm += red[v][g][lane];
+    const int n = n0 + g * 16;
+    if (r16 < mcount && n < p.N) fp8_store4<OUT>(p, m0 + r16, n + kq * 4, sm);
   }
 }
 
@@ -406,9 +412,11 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
 // eight blocks of k at a time (32 bytes of a row of scales), an eighth of the
 // rows with each token block: one block at a time, every 4-byte load was a
 // cache line of its own, half as many line requests as the data itself.
+//
+// Split over k (dense, few tiles): work-group (x, y) computes tile x over the
+// y-th part of the blocks and writes fp32 partial sums to part y of `y`.
 template <bool GROUPED, int BM, int BN, int WM, int WD, class OUT>
-__device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tiles,
-                                              const int* ntiles) {
+__device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, const int* ntiles) {
   constexpr int BH = BN / 2, WN = 8 / WM, NW = 8;
   constexpr int TM = BM / WM / 16, TH = BH / WN / 16;
   constexpr int RPI = 8, ROWB = 128;
@@ -442,7 +450,13 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
   const int lane = threadIdx.x & 63;
   const int w = uniform(threadIdx.x >> 6);
   const int wm = w / WN, wn = w % WN;
-  const int K = p.K, KB = p.KB;
+  const int K = p.K, KBT = p.KB;  // blocks of a whole row
+  int kb0 = 0, KB = KBT;          // this work-group's: kb0 .. kb0 + KB - 1
+  if (!GROUPED && p.splits > 1) {
+    kb0 = blockIdx.y * KBT / p.splits;
+    KB = (blockIdx.y + 1) * KBT / p.splits - kb0;
+    p.y = static_cast<float*>(p.y) + (size_t)blockIdx.y * p.M * p.N;
+  }
 
   // Copy sources: instruction j of wave w fills rows RPI (w + NW j) .. + 7 of
   // its buffer, written already swizzled (16-byte chunk c of row r in place
@@ -453,8 +467,8 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
   const int sw = ((4 * (w & 1)) + (lr >> 1)) & 7;
   const uint32_t chunk = (uint32_t)(((lane & 7) ^ sw) * 16);
   const bool gather = p.rows != nullptr;
-  const uint8_t* xbase = gather ? p.x : p.x + (size_t)m0 * K;
-  const float* xsbase = gather ? p.xs : p.xs + (size_t)m0 * KB;
+  const uint8_t* xbase = (gather ? p.x : p.x + (size_t)m0 * K) + kb0 * ROWB;
+  const float* xsbase = (gather ? p.xs : p.xs + (size_t)m0 * KBT) + kb0;
   auto x_row = [&](int i, bool& ok) -> uint32_t {
     const int m = i < mcount ? i : 0;
     ok = true;
@@ -462,8 +476,8 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
   };
   const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(xbase);
   const __amdgpu_buffer_rsrc_t rs =
-      buffer_rsrc(xsbase, ((size_t)p.x_rows - (gather ? 0 : m0)) * KB * 4);
-  const size_t w0 = ((size_t)e * p.N + n0) * K;
+      buffer_rsrc(xsbase, (((size_t)p.x_rows - (gather ? 0 : m0)) * KBT - kb0) * 4);
+  const size_t w0 = ((size_t)e * p.N + n0) * K + kb0 * ROWB;
   const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(
       p.w + w0, (size_t)(GROUPED ? p.groups : 1) * p.N * K - w0);
   uint32_t ao[NIA], bo = (uint32_t)lr * (uint32_t)K + chunk;
@@ -476,7 +490,7 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
   asm volatile("" : "+v"(bo));
   for (int i = threadIdx.x; i < BM; i += 512) {
     bool ok;
-    sso[i] = x_row(i, ok) * (uint32_t)KB * 4u;
+    sso[i] = x_row(i, ok) * (uint32_t)KBT * 4u;
   }
 
   // copy instruction j of token block kb, of weight half h of block kb
@@ -511,13 +525,13 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
   // blocks (places past K hold what follows in memory, or 0 past its end)
   {
     static_assert(NSB * (kFp8MaxBlocks / 64) <= NW, "a wave for each 64 scales");
-    const size_t ws0 = ((size_t)e * p.NB + n0 / 128) * KB;
+    const size_t ws0 = ((size_t)e * p.NB + n0 / 128) * KBT + kb0;
     const __amdgpu_buffer_rsrc_t rws =
-        buffer_rsrc(p.ws + ws0, ((size_t)(GROUPED ? p.groups : 1) * p.NB * KB - ws0) * 4);
+        buffer_rsrc(p.ws + ws0, ((size_t)(GROUPED ? p.groups : 1) * p.NB * KBT - ws0) * 4);
     const int b = w % NSB, i = w / NSB;
     if (i < kFp8MaxBlocks / 64)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rws, (lds_void*)(sws + b * kFp8MaxBlocks + i * 64), 4, lane * 4, (b * KB + i * 64) * 4, 0,
+          rws, (lds_void*)(sws + b * kFp8MaxBlocks + i * 64), 4, lane * 4, (b * KBT + i * 64) * 4, 0,
           0);
   }
   // what the first MFMAs need, then what step 0 reads, then what it need not
@@ -673,7 +687,59 @@ __device__ __forceinline__ void fp8_pipe_body(const Fp8Gemm& p, const Tile* tile
   stage_barrier_hard();
 
   const int mr = wm * (BM / WM);
-  if constexpr (std::is_same<OUT, uint16_t>::value) {
+  if constexpr (std::is_same<OUT, Relu2Fp8>::value) {
+    // Each half is one block of 128 columns, held by WN waves: they exchange
+    // their rows' largest values through the weight ring, then put the codes
+    // into the token buffers as rows of 256 bytes (16-byte chunk c of row r
+    // in place c ^ r % 16), which leave as whole cache lines.
+    static_assert(BN == 256, "two scale blocks");
+    float* const top = reinterpret_cast<float*>(smem + W00);  // [2][WN][BM]
+#pragma unroll
+    for (int g = 0; g < 2 * TH; ++g)
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[g][t][j] = relu_sq(acc[g][t][j]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        float m = 0.f;
+#pragma unroll
+        for (int g = 0; g < TH; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) m = fmaxf(m, acc[h * TH + g][t][j]);
+        m = fmaxf(m, __shfl_xor(m, 16, 64));
+        m = fmaxf(m, __shfl_xor(m, 32, 64));
+        if (kq == 0) top[(h * WN + wn) * BM + mr + t * 16 + r16] = m;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        const int row = mr + t * 16 + r16;
+        float m = 0.f;
+#pragma unroll
+        for (int u = 0; u < WN; ++u) m = fmaxf(m, top[(h * WN + u) * BM + row]);
+        const float sc = fp8_scale(m);
+        if (wn == 0 && kq == 0 && row < mcount && n0 + h * 128 < p.N)
+          p.ys[(size_t)(m0 + row) * p.NB + n0 / 128 + h] = sc;
+#pragma unroll
+        for (int g = 0; g < TH; ++g) {
+          const int c = h * 8 + wn * TH + g;
+          *reinterpret_cast<uint32_t*>(smem + row * 256 + ((c ^ r16) << 4) + kq * 4) =
+              fp8_codes4(acc[h * TH + g][t], sc);
+        }
+      }
+    __syncthreads();
+    const int c = threadIdx.x & 15;
+    for (int row = threadIdx.x >> 4; row < mcount; row += 32)
+      if (n0 + c * 16 < p.N)
+        *reinterpret_cast<i32x4*>(static_cast<uint8_t*>(p.y) + (size_t)(m0 + row) * p.N + n0 +
+                                  c * 16) =
+            *reinterpret_cast<const i32x4*>(smem + row * 256 + ((c ^ (row & 15)) << 4));
+  } else if constexpr (std::is_same<OUT, uint16_t>::value) {
     // bf16 rows through LDS (staged_store), in the token buffers
     struct Out {
       const Fp8Gemm& p;
@@ -707,6 +773,19 @@ __global__ __launch_bounds__(512) void fp8_pipe_kernel(Fp8Gemm p, const Tile* ti
   fp8_pipe_body<GROUPED, BM, BN, WM, WD, OUT>(p, tiles, ntiles);
 }
 
+// y = the sum of the parts, in order, four values a thread.
+__device__ __forceinline__ void put4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void put4(uint16_t* p, f32x4 v) { store4_bf16(p, v); }
+template <class OUT>
+__global__ __launch_bounds__(256) void fp8_add_kernel(const float* __restrict__ part, int splits,
+                                                      long n4, OUT* __restrict__ y) {
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  f32x4 v = reinterpret_cast<const f32x4*>(part)[i];
+  for (int s = 1; s < splits; ++s) v += reinterpret_cast<const f32x4*>(part)[s * n4 + i];
+  put4(y + i * 4, v);
+}
+
 // ---- launchers ---------------------------------------------------------------------
 
 namespace {
@@ -721,53 +800,126 @@ void with_input(bool bf16, bool vec, F f) {
 
 bool wide(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// Rows per group (average) up to which a grouped product streams weights,
-// and rows up to which a dense one does.
-constexpr int kStreamGroupRows = 32;
-constexpr int kStreamRows = 64;
+// How a product runs.  Times below: 8192 tokens' and smaller problems of the
+// layer's shapes (K = 8192, 2048 or 5120), one MI355X.
+using Plan = Fp8Plan;
 
-template <class OUT>
-hipError_t launch(const Fp8Gemm& p, const Tile* tiles, const int* ntiles, int max_tiles,
-                  bool stream, hipStream_t s) {
-  if (p.groups) {
-    if (stream) {
-      constexpr int RG = 2, NW = 8;
-      const long grid = (long)max_tiles * ((p.N + 16 * RG - 1) / (16 * RG));
-      fp8_stream_kernel<true, NW, 1, RG, 1, OUT><<<grid, NW * 64, 0, s>>>(p, tiles, ntiles);
-    } else {
-      constexpr int BN = 256;
-      const long grid = kXcds * (((long)max_tiles * ((p.N + BN - 1) / BN) + kXcds - 1) / kXcds);
-      fp8_pipe_kernel<true, kFp8TileM, BN, 4, 3, OUT><<<grid, 512, 0, s>>>(p, tiles, ntiles);
+// Grouped: rows per group on average decide.  Up to 4, weights are streamed
+// past 16-row tiles (decode, 1.4 rows: 609 us; at 8.3 rows 1009 us against
+// 915 for 64-row tiles).  Above that, the tile height with the least work:
+// a group of r rows takes about r / BM + 0.4 tiles (at least one), whose cost
+// for 64, 128 and 192 rows is 1.0, 1.25 and 1.675 us a block of k on the full
+// chip (44 rows a group: 1086 / 1123 / 1261 us; 88: 1472 / 1197 / 1289; 176:
+// 2088 / 1856 / 1468; 352: - / 2403 / 2145).
+Plan tiled_plan(double r) {
+  const int bm[3] = {64, 128, 192};
+  const double cost[3] = {1.0, 1.25, 1.675};
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 3; ++i) {
+    const double n = r / bm[i] + 0.4;
+    const double c = (n > 1 ? n : 1.0) * cost[i];
+    if (i == 0 || c < least) best = i, least = c;
+  }
+  return {false, bm[best], 1};
+}
+Plan grouped_plan(int rows, int groups, int KB) {
+  if (rows <= 4L * groups || KB > kFp8MaxBlocks) return {true, kStreamTileM, 1};
+  return tiled_plan((double)rows / groups);
+}
+
+// Dense: up to 16 rows stream the weights (16 rows x 10240 x 8192: 18 us
+// against 21 for tiles).  Above that the tile shape and the split of k with
+// the least estimated time: rounds of tiles over the 256 CUs, each so many
+// blocks of k long (256 x 256 tiles: 1.65 us a block, 128 x 256: 0.96; 64 x
+// 128 tiles, two of which fit a CU: 0.45, or 0.34 for each 256 of them), plus
+// what a tile takes to start and end and, for a split, the second launch and
+// the partial sums' traffic.  187 x 2048 x 8192: 24 us unsplit, 14.6 split;
+// 32 x 10240 x 8192: 31 and 21.
+struct DenseTile {
+  int bm, bn;
+};
+constexpr DenseTile kDenseTiles[3] = {{256, 256}, {128, 256}, {64, 128}};
+double tile_us(const DenseTile& t, long n) {
+  if (t.bm == 64) return n * (0.34 / 256) > 0.45 ? n * (0.34 / 256) : 0.45;
+  return (double)((n + 255) / 256) * (t.bm == 256 ? 1.65 : 0.96);
+}
+Plan dense_plan(int M, int N, int KB) {
+  if (M <= 16) return {true, kStreamTileM, 1};
+  Plan best{};
+  double least = 0;
+  for (const DenseTile& t : kDenseTiles)
+    for (int s = 1; s <= 8; s *= 2) {
+      // a part is at least 8 blocks, and at most what the kernel takes
+      const int kb = (KB + s - 1) / s;
+      if ((s > 1 && KB / s < 8) || kb > kFp8MaxBlocks) continue;
+      const long n = (long)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn) * s;
+      double us = tile_us(t, n) * kb + 3.4;
+      if (s > 1) us += 4.0 + (double)s * M * N * 8 / 4e6;
+      if (best.bm == 0 || us < least) best = {false, t.bm, s}, least = us;
     }
-    return hipGetLastError();
-  }
-  if (stream) {
-    auto go = [&](auto mt) {
-      constexpr int MT = decltype(mt)::value, RG = 1, NW = 8;
-      const long nblocks = (p.N + 16 * RG - 1) / (16 * RG);
-      const long mtiles = (p.M + 16 * MT - 1) / (16 * MT);
-      const long grid = kXcds * mtiles * ((nblocks + kXcds - 1) / kXcds);
-      fp8_stream_kernel<false, NW, MT, RG, 2, OUT><<<grid, NW * 64, 0, s>>>(p, nullptr, nullptr);
-    };
-    if (p.M <= 16) go(std::integral_constant<int, 1>{});
-    else if (p.M <= 32) go(std::integral_constant<int, 2>{});
-    else go(std::integral_constant<int, 4>{});
-    return hipGetLastError();
-  }
-  constexpr int BM = 256, BN = 256;
-  const long tot = (long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-  const long grid = kXcds * ((tot + kXcds - 1) / kXcds);
-  fp8_pipe_kernel<false, BM, BN, 4, 2, OUT><<<grid, 512, 0, s>>>(p, nullptr, nullptr);
-  return hipGetLastError();
+  return best;
 }
 
-bool grouped_stream(int rows, int groups, int KB) {
-  return rows <= (long)kStreamGroupRows * groups || KB > kFp8MaxBlocks;
+Plan make_plan(int M, int N, int KB, int groups) {
+  return groups ? grouped_plan(M, groups, KB) : dense_plan(M, N, KB);
 }
-bool dense_stream(const Fp8Gemm& p) { return p.M <= kStreamRows || p.KB > kFp8MaxBlocks; }
 
 int grouped_tiles(int rows, int groups, int tile_m) {
   return (rows < groups ? rows : groups) + rows / tile_m + 1;
+}
+
+long xcd_grid(long work) { return kXcds * ((work + kXcds - 1) / kXcds); }
+
+// Four waves x 4 row groups: 589 and 559 us for the decode batch's up and down
+// projection, against 644 and 557 for 8 x 2, 615 and 563 for 4 x 2, 928 and
+// 601 for 8 x 1; 595 and 565 for 4 x 8, which quantises its output.
+template <class OUT>
+hipError_t launch_grouped(const Fp8Gemm& p, const Plan& plan, const Tile* tiles, const int* ntiles,
+                          int max_tiles, hipStream_t s) {
+  using std::integral_constant;
+  if (plan.stream) {
+    constexpr int RG = std::is_same<OUT, Relu2Fp8>::value ? 8 : 4, NW = 4;
+    const long grid = (long)max_tiles * ((p.N + 16 * RG - 1) / (16 * RG));
+    fp8_stream_kernel<true, NW, RG, 1, OUT><<<grid, NW * 64, 0, s>>>(p, tiles, ntiles);
+  } else {
+    auto go = [&](auto bm, auto wm) {
+      constexpr int BN = 256;
+      const long grid = xcd_grid((long)max_tiles * ((p.N + BN - 1) / BN));
+      fp8_pipe_kernel<true, decltype(bm)::value, BN, decltype(wm)::value, 3, OUT>
+          <<<grid, 512, 0, s>>>(p, tiles, ntiles);
+    };
+    if (plan.bm == 64) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (plan.bm == 128) go(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+    else go(integral_constant<int, 192>{}, integral_constant<int, 4>{});
+  }
+  return hipGetLastError();
+}
+
+template <class OUT>
+hipError_t launch_dense(const Fp8Gemm& p, const Plan& plan, hipStream_t s) {
+  using std::integral_constant;
+  if (plan.stream) {
+    constexpr int RG = 1, NW = 8;
+    const long grid = (p.N + 16 * RG - 1) / (16 * RG);
+    fp8_stream_kernel<false, NW, RG, 2, OUT><<<grid, NW * 64, 0, s>>>(p, nullptr, nullptr);
+  } else {
+    auto go = [&](auto bm, auto bn, auto wm, auto wd) {
+      constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
+      const long tot = (long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+      fp8_pipe_kernel<false, BM, BN, decltype(wm)::value, decltype(wd)::value, OUT>
+          <<<dim3(xcd_grid(tot), p.splits), 512, 0, s>>>(p, nullptr, nullptr);
+    };
+    using I2 = integral_constant<int, 2>;
+    using I3 = integral_constant<int, 3>;
+    using I4 = integral_constant<int, 4>;
+    using I128 = integral_constant<int, 128>;
+    using I256 = integral_constant<int, 256>;
+    if (plan.bm == 256) go(I256{}, I256{}, I4{}, I2{});
+    else if (plan.bm == 128) go(I128{}, I256{}, I2{}, I3{});
+    else go(integral_constant<int, 64>{}, I128{}, I2{}, I3{});
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -798,30 +950,55 @@ hipError_t fp8_quantize_weight(const void* w, bool bf16, long matrices, int rows
   return hipGetLastError();
 }
 
-size_t fp8_matmul_workspace(int rows, int groups, int KB) {
-  if (groups == 0) return 0;
-  const int tile_m = grouped_stream(rows, groups, KB) ? kStreamTileM : kFp8TileM;
-  return 256 + (size_t)grouped_tiles(rows, groups, tile_m) * sizeof(Tile);
+size_t fp8_matmul_workspace(int M, int N, int KB, int groups) {
+  const Plan plan = make_plan(M, N, KB, groups);
+  if (groups) return 256 + (size_t)grouped_tiles(M, groups, plan.bm) * sizeof(Tile);
+  return plan.splits > 1 ? (size_t)plan.splits * M * N * sizeof(float) : 0;
 }
 
-hipError_t fp8_matmul(const Fp8Gemm& p, const int32_t* offsets, bool out_bf16, void* ws,
-                      hipStream_t s) {
-  Tile* tiles = nullptr;
-  int32_t* ntiles = nullptr;
-  int max_tiles = 0;
-  bool stream = dense_stream(p);
+hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws, hipStream_t s) {
+  const Plan plan = make_plan(p.M, p.N, p.KB, p.groups);
+  p.splits = plan.splits;
   if (p.groups) {
-    stream = grouped_stream(p.M, p.groups, p.KB);
-    const int tile_m = stream ? kStreamTileM : kFp8TileM;
-    max_tiles = grouped_tiles(p.M, p.groups, tile_m);
-    ntiles = static_cast<int32_t*>(ws);
-    tiles = reinterpret_cast<Tile*>(static_cast<char*>(ws) + 256);
-    fp8_tiles_kernel<<<1, 1024, 0, s>>>(offsets, p.groups, p.M, tile_m, max_tiles, tiles, ntiles);
+    const int max_tiles = grouped_tiles(p.M, p.groups, plan.bm);
+    int32_t* ntiles = static_cast<int32_t*>(ws);
+    Tile* tiles = reinterpret_cast<Tile*>(static_cast<char*>(ws) + 256);
+    fp8_tiles_kernel<<<1, 1024, 0, s>>>(offsets, p.groups, p.M, plan.bm, max_tiles, tiles, ntiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    return out_bf16 ? launch_grouped<uint16_t>(p, plan, tiles, ntiles, max_tiles, s)
+                    : launch_grouped<float>(p, plan, tiles, ntiles, max_tiles, s);
   }
-  return out_bf16 ? launch<uint16_t>(p, tiles, ntiles, max_tiles, stream, s)
-                  : launch<float>(p, tiles, ntiles, max_tiles, stream, s);
+  if (p.splits > 1) {
+    void* y = p.y;
+    p.y = ws;
+    const hipError_t e = launch_dense<float>(p, plan, s);
+    if (e != hipSuccess) return e;
+    const long n4 = (long)p.M * p.N / 4;
+    const long grid = (n4 + 255) / 256;
+    const float* part = static_cast<const float*>(ws);
+    if (out_bf16)
+      fp8_add_kernel<<<grid, 256, 0, s>>>(part, p.splits, n4, static_cast<uint16_t*>(y));
+    else
+      fp8_add_kernel<<<grid, 256, 0, s>>>(part, p.splits, n4, static_cast<float*>(y));
+    return hipGetLastError();
+  }
+  return out_bf16 ? launch_dense<uint16_t>(p, plan, s) : launch_dense<float>(p, plan, s);
+}
+
+Fp8Plan fp8_expert_plan(int rows, int experts, int KB, int path) {
+  if (KB > kFp8MaxBlocks || path == 1) return {true, kStreamTileM, 1};
+  return path == 2 ? tiled_plan((double)rows / experts) : grouped_plan(rows, experts, KB);
+}
+
+hipError_t fp8_exp_up(const Fp8Gemm& p, const Fp8Plan& plan, const Tile* tiles, const int* ntiles,
+                      int max_tiles, hipStream_t s) {
+  return launch_grouped<Relu2Fp8>(p, plan, tiles, ntiles, max_tiles, s);
+}
+
+hipError_t fp8_exp_down(const Fp8Gemm& p, const Fp8Plan& plan, const Tile* tiles,
+                        const int* ntiles, int max_tiles, hipStream_t s) {
+  return launch_grouped<uint16_t>(p, plan, tiles, ntiles, max_tiles, s);
 }
 
 }  // namespace lmoe

@@ -153,7 +153,6 @@ hipError_t fp8_quantize_weight(const void* w, bool bf16, long matrices, int rows
 // else row m takes the matrix of the group whose range offsets[g] ..
 // offsets[g + 1] - 1 holds it (rows of no group are not written).
 constexpr int kFp8MaxBlocks = 256;  // blocks of k that the LDS-tiled product takes
-constexpr int kFp8TileM = 192;      // rows of a grouped product's tile there
 struct Fp8Gemm {
   const uint8_t* x;     // [x_rows, K]
   const float* xs;      // [x_rows, KB]
@@ -162,10 +161,29 @@ struct Fp8Gemm {
   const int32_t* rows;  // [M] or null
   void* y;              // [M, N], bf16 or fp32
   int M, N, K, KB, NB, x_rows, groups;
+  int splits = 1;       // of k: set by fp8_matmul
+  float* ys = nullptr;  // [M, NB]: the scales of a quantised output
 };
-size_t fp8_matmul_workspace(int rows, int groups, int KB);
-hipError_t fp8_matmul(const Fp8Gemm& p, const int32_t* offsets, bool out_bf16, void* ws,
+// bytes of `ws`: the groups' row tiles, or the partial sums of a split of k
+size_t fp8_matmul_workspace(int M, int N, int KB, int groups);
+hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws,
                       hipStream_t s);
+
+// The layer's expert projections in that format, on the dispatch's tile list
+// (tiles of plan.bm rows; groups = experts, N and K multiples of 128):
+//   up    y = e4m3 codes and ys = scales of relu(z[rows] Wup[e]^T)^2
+//   down  y = H Wdn[e]^T in bf16
+// path: lmoe_path; KB: blocks of the longer of the two k ranges.
+struct Fp8Plan {
+  bool stream;  // weight streaming, else LDS-tiled
+  int bm;       // token rows of a tile
+  int splits;   // of k (dense tiles)
+};
+Fp8Plan fp8_expert_plan(int rows, int experts, int KB, int path);
+hipError_t fp8_exp_up(const Fp8Gemm& p, const Fp8Plan& plan, const Tile* tiles, const int* ntiles,
+                      int max_tiles, hipStream_t s);
+hipError_t fp8_exp_down(const Fp8Gemm& p, const Fp8Plan& plan, const Tile* tiles,
+                        const int* ntiles, int max_tiles, hipStream_t s);
 
 // r = sum_k w[t][k] O[inv[t][k]] -> r16 (bf16) and, if r32 != NULL, fp32.
 hipError_t combine(const uint16_t* o, const int32_t* inv, const float* w, int T, int K, int R,

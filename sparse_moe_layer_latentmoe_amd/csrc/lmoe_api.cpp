@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -69,7 +70,8 @@ lmoe_status check_config(const lmoe_config* c) {
       !std::isfinite(c->routed_scaling_factor))
     return LMOE_ERR_INVALID_ARG;
   if (c->path < LMOE_PATH_AUTO || c->path > LMOE_PATH_TILED) return LMOE_ERR_INVALID_ARG;
-  if (c->expert_format != LMOE_EXPERTS_BF16 && c->expert_format != LMOE_EXPERTS_MXFP4)
+  if (c->expert_format != LMOE_EXPERTS_BF16 && c->expert_format != LMOE_EXPERTS_MXFP4 &&
+      c->expert_format != LMOE_EXPERTS_FP8)
     return LMOE_ERR_INVALID_ARG;
   if (c->hidden_size % 64 || c->moe_latent_size % 64 || c->moe_intermediate_size % 64 ||
       c->moe_shared_expert_intermediate_size % 64)
@@ -91,6 +93,10 @@ lmoe_status check_config(const lmoe_config* c) {
   if (c->expert_format == LMOE_EXPERTS_MXFP4 &&
       (c->moe_latent_size % 128 || c->moe_intermediate_size % 128))
     return LMOE_ERR_UNSUPPORTED;
+  // FP8 experts: whole scale blocks
+  if (c->expert_format == LMOE_EXPERTS_FP8 &&
+      (c->moe_latent_size % 128 || c->moe_intermediate_size % 128))
+    return LMOE_ERR_UNSUPPORTED;
   // block steps: known bits; the pre-norm's epsilon finite and >= 0
   if (c->fuse & ~(LMOE_FUSE_PRENORM | LMOE_FUSE_RESIDUAL)) return LMOE_ERR_INVALID_ARG;
   if ((c->fuse & LMOE_FUSE_PRENORM) && !(std::isfinite(c->norm_eps) && c->norm_eps >= 0.f))
@@ -108,7 +114,7 @@ long max_tiles(const lmoe_config& c, long T, int tile_m) {
 
 struct Layout {
   size_t xt, rn, z32, z16, hs, ys, part, logits, idx, tw, counts, offsets, blockcnt, rows_tok,
-      inv, tiles, ntiles, h, o, r16, total;
+      inv, tiles, ntiles, h, hscale, o, r16, z8, zscale, total;
 };
 
 Layout make_layout(const lmoe_config& c) {
@@ -151,9 +157,14 @@ Layout make_layout(const lmoe_config& c) {
   L.inv = take(slots * 4);
   L.tiles = take(ntile * sizeof(Tile));
   L.ntiles = take(16);
-  L.h = take(slots * F * 2);
+  // FP8 experts: hidden rows and the latent as codes with their scales
+  const bool fp8 = c.expert_format == LMOE_EXPERTS_FP8;
+  L.h = take(slots * F * (fp8 ? 1 : 2));
+  L.hscale = take(fp8 ? slots * (F / 128) * 4 : 0);
   L.o = take(slots * R * 2);
   L.r16 = take(T * R * 2);
+  L.z8 = take(fp8 ? T * R : 0);
+  L.zscale = take(fp8 ? T * (R / 128) * 4 : 0);
   L.total = off;
   return L;
 }
@@ -170,6 +181,12 @@ lmoe_status check_weights(const lmoe_config& c, const lmoe_weights* w) {
     if (!w->expert_up_mxfp4 || !w->expert_up_scale || !w->expert_down_mxfp4 ||
         !w->expert_down_scale || !aligned16(w->expert_up_mxfp4) ||
         !aligned16(w->expert_down_mxfp4))
+      return LMOE_ERR_INVALID_ARG;
+  } else if (c.expert_format == LMOE_EXPERTS_FP8) {
+    if (!w->expert_up_fp8 || !w->expert_up_fp8_scale || !w->expert_down_fp8 ||
+        !w->expert_down_fp8_scale || !aligned16(w->expert_up_fp8) ||
+        !aligned16(w->expert_down_fp8) || !aligned16(w->expert_up_fp8_scale) ||
+        !aligned16(w->expert_down_fp8_scale))
       return LMOE_ERR_INVALID_ARG;
   } else if (!w->expert_up || !w->expert_down || !aligned16(w->expert_up) ||
              !aligned16(w->expert_down)) {
@@ -242,7 +259,10 @@ lmoe_status run_forward(const lmoe_config& c, const lmoe_weights& w, const Layou
   const bool expert_tiled =
       tiled_ok && (c.path == LMOE_PATH_TILED ||
                    (c.path == LMOE_PATH_AUTO && static_cast<long>(T) * K > 32L * E));
-  const int tile_m = expert_tiled ? tiled_block_m() : kStreamTileM;
+  const bool fp8 = c.expert_format == LMOE_EXPERTS_FP8;
+  const Fp8Plan plan8 =
+      fp8 ? fp8_expert_plan(T * K, E, std::max(R, F) / 128, c.path) : Fp8Plan{};
+  const int tile_m = fp8 ? plan8.bm : (expert_tiled ? tiled_block_m() : kStreamTileM);
   const int ntile_max = static_cast<int>(max_tiles(c, T, tile_m));
 
   // Block pre-norm: the projections read bf16(gamma h) and scale by 1/rms.
@@ -354,7 +374,18 @@ lmoe_status run_forward(const lmoe_config& c, const lmoe_weights& w, const Layou
       !done("dispatch"))
     return LMOE_ERR_HIP;
   if (!mark()) return LMOE_ERR_HIP;
-  if (mxfp4) {
+  if (fp8) {
+    // the latent is quantised from its fp32 values, the hidden rows from the
+    // up projection's fp32 sums
+    uint8_t* z8 = reinterpret_cast<uint8_t*>(ws + L.z8);
+    float* zscale = reinterpret_cast<float*>(ws + L.zscale);
+    if (!ok(fp8_quantize(z32, false, T, R, R, z8, zscale, s))) return LMOE_ERR_HIP;
+    Fp8Gemm pup{z8,      zscale, w.expert_up_fp8, w.expert_up_fp8_scale, rows_tok, ws + L.h,
+                T * K,   F,      R,               R / 128,               F / 128,  T,
+                E};
+    pup.ys = reinterpret_cast<float*>(ws + L.hscale);
+    if (!ok(fp8_exp_up(pup, plan8, tiles, ntiles, ntile_max, s))) return LMOE_ERR_HIP;
+  } else if (mxfp4) {
     ExpUpMx pup{z16, rows_tok, w.expert_up_mxfp4, w.expert_up_scale, H, R, F};
     if (!ok(expert_tiled ? tiled_mx_exp_up(pup, tiles, ntiles, ntile_max, T, s)
                          : stream_mx_exp_up(pup, tiles, ntiles, ntile_max, T,
@@ -367,7 +398,22 @@ lmoe_status run_forward(const lmoe_config& c, const lmoe_weights& w, const Layou
       return LMOE_ERR_HIP;
   }
   if (!done("expert_up") || !mark()) return LMOE_ERR_HIP;
-  if (mxfp4) {
+  if (fp8) {
+    const Fp8Gemm pdn{reinterpret_cast<uint8_t*>(ws + L.h),
+                      reinterpret_cast<float*>(ws + L.hscale),
+                      w.expert_down_fp8,
+                      w.expert_down_fp8_scale,
+                      nullptr,
+                      O,
+                      T * K,
+                      R,
+                      F,
+                      F / 128,
+                      R / 128,
+                      T * K,
+                      E};
+    if (!ok(fp8_exp_down(pdn, plan8, tiles, ntiles, ntile_max, s))) return LMOE_ERR_HIP;
+  } else if (mxfp4) {
     ExpDownMx pdn{H, w.expert_down_mxfp4, w.expert_down_scale, O, R, F};
     if (!ok(expert_tiled ? tiled_mx_exp_down(pdn, tiles, ntiles, ntile_max, s)
                          : stream_mx_exp_down(pdn, tiles, ntiles, ntile_max, s)))
@@ -459,7 +505,10 @@ lmoe_status lmoe_create(const lmoe_config* cfg, const lmoe_weights* w, void* wor
   lmoe_handle* h = new (std::nothrow) lmoe_handle();
   if (!h) return LMOE_ERR_INVALID_ARG;
   h->cfg = *cfg;
-  h->w = *w;
+  // the FP8 fields are read only with that format
+  h->w = lmoe_weights{};
+  std::memcpy(&h->w, w, cfg->expert_format == LMOE_EXPERTS_FP8 ? sizeof(lmoe_weights)
+                                                               : offsetof(lmoe_weights, expert_up_fp8));
   h->ws = static_cast<char*>(workspace);
   h->L = L;
   const char* dbg = std::getenv("LMOE_DEBUG");

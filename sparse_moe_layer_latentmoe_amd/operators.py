@@ -377,9 +377,7 @@ def fp8_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=torc
         a = LmoeFp8MatmulArgs(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(rows),
                               _ptr(offsets), _ptr(y), _TYPE[y.dtype],
                               0 if offsets is None else w.shape[0], M, X, N, K)
-        ws, nbytes = None, 0
-        if offsets is not None:
-            nbytes = int(lib.lmoe_fp8_matmul_workspace_size(a))
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        nbytes = int(lib.lmoe_fp8_matmul_workspace_size(a))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         _done(lib.lmoe_fp8_matmul(a, _ptr(ws), nbytes, s), "lmoe_fp8_matmul")
     return y
