@@ -159,7 +159,7 @@ def workspace_size(cfg: LmoeConfig) -> int:
 
 
 def _ptr(t) -> int | None:
-    return None if t is None else int(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream_handle(stream) -> int | None:

@@ -77,8 +77,8 @@ def declare(lib: ctypes.CDLL) -> None:
 
 
 def _check(t, what: str, dtypes, ndim=None, shape=None, device=None, dense: bool = True) -> None:
-    """Raise unless ``t`` is a GPU tensor of one of ``dtypes`` and this shape;
-    dense, or (not dense) with its last axis contiguous."""
+    """Raise unless ``t`` is a GPU tensor of one of ``dtypes`` and this shape,
+    on GPU number ``device``; dense, or (not dense) with contiguous rows."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
@@ -87,29 +87,33 @@ def _check(t, what: str, dtypes, ndim=None, shape=None, device=None, dense: bool
         raise ValueError(f"{what}: {t.dim()} dimensions, expected {ndim}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dense:
-        if not t.is_contiguous():
+    if not t.is_contiguous():
+        if dense:
             raise ValueError(f"{what}: must be contiguous")
-    elif t.shape[-1] > 1 and t.stride(-1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{what}: rows must be contiguous and not overlap")
-    if t.device.type != "cuda":
+        if t.shape[-1] > 1 and t.stride(-1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError(f"{what}: rows must be contiguous and not overlap")
+    if not t.is_cuda:
         raise ValueError(f"{what}: must be a GPU tensor, got one on {t.device}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{what}: on {t.device}, expected cuda:{device}")
+
+
+def _type(t) -> int:
+    return F32 if t is None else _TYPE[t.dtype]
 
 
 def _row_stride(t) -> int:
-    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1])
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 @contextlib.contextmanager
-def _switched(device, stream):
+def _switched(device: int, stream):
     with torch.cuda.device(device):
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.current_stream() if stream is None else \
                 torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream) or 0))
-        if stream.device != device:
-            raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
+        if stream.device.index != device:
+            raise ValueError(f"stream: on {stream.device}, the tensors are on cuda:{device}")
         with torch.cuda.stream(stream):
             yield stream.cuda_stream
 
@@ -129,11 +133,11 @@ class _OnCurrent:
         return False
 
 
-def _launch(device, stream):
-    """Context with ``device`` and ``stream`` current (so that allocations
+def _launch(device: int, stream):
+    """Context with GPU ``device`` and ``stream`` current (so that allocations
     belong to that stream); yields the stream's handle."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return _OnCurrent(torch.cuda.current_stream().cuda_stream)
+    if stream is None and device == torch._C._cuda_getDevice():
+        return _OnCurrent(torch._C._cuda_getCurrentRawStream(device))
     return _switched(device, stream)
 
 
@@ -165,9 +169,9 @@ def route_logits(router: LmoeRouter, logits, bias=None, stream=None):
     if E != router.n_experts:
         raise ValueError(f"logits: {E} experts, the router has {router.n_experts}")
     if bias is not None:
-        _check(bias, "bias", (torch.float32,), shape=(E,), device=logits.device)
+        _check(bias, "bias", (torch.float32,), shape=(E,), device=logits.get_device())
     K = max(int(router.top_k), 0)
-    with _launch(logits.device, stream) as s:
+    with _launch(logits.get_device(), stream) as s:
         idx = torch.empty((T, K), dtype=torch.int32, device=logits.device)
         w = torch.empty((T, K), dtype=torch.float32, device=logits.device)
         _done(load_library().lmoe_route_logits(
@@ -184,9 +188,9 @@ def route_logits_backward(router: LmoeRouter, logits, topk_idx, dw, stream=None)
     if E != router.n_experts:
         raise ValueError(f"logits: {E} experts, the router has {router.n_experts}")
     K = int(router.top_k)
-    _check(topk_idx, "topk_idx", (torch.int32,), shape=(T, K), device=logits.device)
-    _check(dw, "dw", (torch.float32,), shape=(T, K), device=logits.device)
-    with _launch(logits.device, stream) as s:
+    _check(topk_idx, "topk_idx", (torch.int32,), shape=(T, K), device=logits.get_device())
+    _check(dw, "dw", (torch.float32,), shape=(T, K), device=logits.get_device())
+    with _launch(logits.get_device(), stream) as s:
         dl = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
         _done(load_library().lmoe_route_logits_backward(
             router, _ptr(logits), _TYPE[logits.dtype], _row_stride(logits), _ptr(topk_idx),
@@ -211,32 +215,30 @@ class BlockNormGrads:
 def _norm_args(h, y, pre_weight, post_weight, gate, res_scale, eps) -> LmoeBlockNormArgs:
     _check(h, "h", _TYPE, ndim=2, dense=False)
     T, D = h.shape
-    dev = h.device
+    dev = h.get_device()
     if y is not None:
         _check(y, "y", _TYPE, shape=(T, D), device=dev, dense=False)
-    a = LmoeBlockNormArgs()
-    for name, t in (("pre", pre_weight), ("post", post_weight), ("res_scale", res_scale)):
+    for name, t in (("pre_weight", pre_weight), ("post_weight", post_weight),
+                    ("res_scale", res_scale)):
         if t is not None:
-            _check(t, name if name == "res_scale" else name + "_weight", _TYPE, shape=(D,),
-                   device=dev)
-            setattr(a, name if name == "res_scale" else name + "_weight", t.data_ptr())
-            setattr(a, name + "_type", _TYPE[t.dtype])
+            _check(t, name, _TYPE, shape=(D,), device=dev)
+    kind = GATE_NONE
     if gate is not None:
-        shape = tuple(gate.shape) if isinstance(gate, torch.Tensor) else None
-        kind = {(D,): GATE_CHANNEL, (T, D): GATE_FULL}.get(shape)
-        if shape == (T, 1) and D != 1:
-            kind = GATE_TOKEN
-        if shape is not None and kind is None:
-            raise ValueError(f"gate: shape {shape}, expected ({D},), ({T}, 1) or ({T}, {D})")
         _check(gate, "gate", _TYPE, device=dev)
-        a.gate, a.gate_kind, a.gate_type = gate.data_ptr(), kind, _TYPE[gate.dtype]
-    a.h, a.h_stride, a.h_type = h.data_ptr(), _row_stride(h), _TYPE[h.dtype]
-    if y is not None:
-        a.y, a.y_stride, a.y_type = y.data_ptr(), _row_stride(y), _TYPE[y.dtype]
-    else:
-        a.y_type = BF16
-    a.T, a.D, a.eps = T, D, eps
-    return a
+        shape = gate.shape
+        if shape == (D,):
+            kind = GATE_CHANNEL
+        elif shape == (T, D):
+            kind = GATE_FULL
+        elif shape == (T, 1):
+            kind = GATE_TOKEN
+        else:
+            raise ValueError(f"gate: shape {tuple(shape)}, expected ({D},), ({T}, 1) or ({T}, {D})")
+    return LmoeBlockNormArgs(
+        h.data_ptr(), _ptr(y), _row_stride(h), 0 if y is None else _row_stride(y),
+        _ptr(pre_weight), _ptr(post_weight), _ptr(res_scale), _ptr(gate), kind, _TYPE[h.dtype],
+        BF16 if y is None else _TYPE[y.dtype], _type(pre_weight), _type(post_weight),
+        _type(res_scale), _type(gate), T, D, eps)
 
 
 def _y_dtype(y):
@@ -255,7 +257,7 @@ def block_norm(h, y=None, pre_weight=None, post_weight=None, gate=None, res_scal
     has y's (bf16 without y).  stats (want_stats) is what the backward needs."""
     a = _norm_args(h, y, pre_weight, post_weight, gate, res_scale, eps)
     T, D = h.shape
-    with _launch(h.device, stream) as s:
+    with _launch(h.get_device(), stream) as s:
         h_out = torch.empty((T, D), dtype=h.dtype, device=h.device)
         x = torch.empty((T, D), dtype=_y_dtype(y), device=h.device) \
             if pre_weight is not None else None
@@ -274,15 +276,16 @@ def block_norm_backward(h, y, stats, dh_out=None, dx=None, pre_weight=None, post
     a = _norm_args(h, y, pre_weight, post_weight, gate, res_scale, eps)
     T, D = h.shape
     dev = h.device
-    _check(stats, "stats", (torch.float32,), shape=(T, 2), device=dev)
+    gpu = h.get_device()
+    _check(stats, "stats", (torch.float32,), shape=(T, 2), device=gpu)
     if dh_out is not None:
-        _check(dh_out, "dh_out", (h.dtype,), shape=(T, D), device=dev)
+        _check(dh_out, "dh_out", (h.dtype,), shape=(T, D), device=gpu)
     if dx is not None:
         if pre_weight is None:
             raise ValueError("dx: the forward had no pre_weight, so no x")
-        _check(dx, "dx", (_y_dtype(y),), shape=(T, D), device=dev)
+        _check(dx, "dx", (_y_dtype(y),), shape=(T, D), device=gpu)
     lib = load_library()
-    with _launch(dev, stream) as s:
+    with _launch(gpu, stream) as s:
         g = BlockNormGrads(dh=torch.empty((T, D), dtype=h.dtype, device=dev))
         if y is not None:
             g.dy = torch.empty((T, D), dtype=y.dtype, device=dev)
@@ -309,7 +312,7 @@ def quantize_fp8(x, stream=None):
     128 values of a row has its own scale."""
     _check(x, "x", _TYPE, ndim=2, dense=False)
     T, K = x.shape
-    with _launch(x.device, stream) as s:
+    with _launch(x.get_device(), stream) as s:
         codes = torch.empty((T, K), dtype=_E4M3, device=x.device)
         scales = torch.empty((T, (K + 127) // 128), dtype=torch.float32, device=x.device)
         _done(load_library().lmoe_quantize_fp8(_ptr(x), _TYPE[x.dtype], T, K, _row_stride(x),
@@ -328,7 +331,7 @@ def quantize_fp8_weight(w, stream=None):
     N, K = w.shape[-2:]
     lead = tuple(w.shape[:-2])
     n = w.numel() // (N * K) if N and K else 0
-    with _launch(w.device, stream) as s:
+    with _launch(w.get_device(), stream) as s:
         codes = torch.empty(w.shape, dtype=_E4M3, device=w.device)
         scales = torch.empty((*lead, (N + 127) // 128, (K + 127) // 128), dtype=torch.float32,
                              device=w.device)
@@ -349,30 +352,30 @@ def fp8_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=torc
     they hold).  out_dtype: bf16 or fp32."""
     e4m3, f32 = (_E4M3,), (torch.float32,)
     _check(x, "x", e4m3, ndim=2)
-    dev = x.device
+    dev, gpu = x.device, x.get_device()
     X, K = x.shape
-    _check(w, "w", e4m3, ndim=2 if offsets is None else 3, device=dev)
+    _check(w, "w", e4m3, ndim=2 if offsets is None else 3, device=gpu)
     N = w.shape[-2]
     if w.shape[-1] != K:
         raise ValueError(f"w: {w.shape[-1]} columns, x has {K}")
     kb = (K + 127) // 128
-    _check(x_scales, "x_scales", f32, shape=(X, kb), device=dev)
-    _check(w_scales, "w_scales", f32, shape=(*w.shape[:-2], (N + 127) // 128, kb), device=dev)
+    _check(x_scales, "x_scales", f32, shape=(X, kb), device=gpu)
+    _check(w_scales, "w_scales", f32, shape=(*w.shape[:-2], (N + 127) // 128, kb), device=gpu)
     i32 = (torch.int32,)
     if offsets is not None:
         if w.shape[0] < 1:
             raise ValueError("w: no groups")
-        _check(offsets, "offsets", i32, shape=(w.shape[0] + 1,), device=dev)
+        _check(offsets, "offsets", i32, shape=(w.shape[0] + 1,), device=gpu)
     M = X
     if rows is not None:
-        _check(rows, "rows", i32, ndim=1, device=dev)
+        _check(rows, "rows", i32, ndim=1, device=gpu)
         M = rows.shape[0]
     if out is not None:
-        _check(out, "out", _TYPE, shape=(M, N), device=dev)
+        _check(out, "out", _TYPE, shape=(M, N), device=gpu)
     elif out_dtype not in _TYPE:
         raise TypeError(f"out_dtype: {out_dtype}, expected torch.bfloat16 or torch.float32")
     lib = load_library()
-    with _launch(dev, stream) as s:
+    with _launch(gpu, stream) as s:
         y = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
         a = LmoeFp8MatmulArgs(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(rows),
                               _ptr(offsets), _ptr(y), _TYPE[y.dtype],
