@@ -21,8 +21,8 @@
 // bits every time).
 #include <type_traits>
 
+#include "gemm_device.h"
 #include "kernels.h"
-#include "lmoe_device.h"
 
 namespace lmoe {
 
@@ -80,10 +80,11 @@ __device__ __forceinline__ void store8v(float* p, int c, int D, const float (&v)
 template <int TPR, bool VEC>
 __device__ __forceinline__ void store8v(uint16_t* p, int c, int D, const float (&v)[8]) {
   if constexpr (VEC) {
-    u16x8 a;
+    // one instruction for two values; rounds as f32_to_bf16
+    f32x8 a;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = f32_to_bf16(v[i]);
-    *reinterpret_cast<u16x8*>(p + c) = a;
+    for (int i = 0; i < 8; ++i) a[i] = v[i];
+    *reinterpret_cast<bf16x8*>(p + c) = __builtin_convertvector(a, bf16x8);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -104,17 +105,16 @@ struct RowSum {
   f32x2* lds;  // [2][TPR / 64]
   int turn = 0;
   __device__ f32x2 operator()(float a, float b) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-      a += __shfl_xor(a, off, 64);
-      b += __shfl_xor(b, off, 64);
-    }
+    a = wave_reduce(a, AddOp{});
+    b = wave_reduce(b, AddOp{});
     if constexpr (TPR > 64) {
       constexpr int NW = TPR / 64;
       f32x2* buf = lds + turn * NW;
       turn ^= 1;
       if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = f32x2{a, b};
-      __syncthreads();
+      // LDS only: loads of the next row stay in flight
+      wait_lgkmcnt0();
+      stage_barrier();
       a = b = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
@@ -392,6 +392,240 @@ __global__ __launch_bounds__(TPR* rows_per_group<TPR>()) void block_norm_backwar
   }
 }
 
+// The training step's usual case (y, dh_out, dx, dh and dy all there, wide
+// loads, rows up to 8192): the next row's loads are issued before the current
+// row is worked on (a row of 8192 is 115 KB a CU, enough to cover HBM's
+// latency), and the [D] parameters lie in LDS (1 where absent).  Registers
+// are what limits it: the sums take 64 of a thread's 256 and each of the two
+// rows up to 72, so a row stays as it was loaded and is converted again in
+// each of its passes.  GATE: 0 a gate of [D], [T] or none, 1 [T, D] in bf16, 2
+// [T, D] in fp32.
+namespace {
+
+// Eight values as they lie in memory.  renew() hides from the compiler that a
+// later conversion gives the same values as an earlier one, so that it
+// converts again instead of keeping them in registers in between.
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const void* p, size_t i) {
+    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+    a = q[0];
+    b = q[1];
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = a[i], o[4 + i] = b[i];
+  }
+  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(a), "+v"(b)); }
+};
+template <>
+struct Raw8<uint16_t> {
+  u16x8 a;
+  __device__ __forceinline__ void load(const void* p, size_t i) {
+    a = *reinterpret_cast<const u16x8*>(static_cast<const uint16_t*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = bf16_to_f32(a[i]);
+  }
+  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(a)); }
+};
+
+}  // namespace
+
+template <class HT, class YT, int TPR, int NC, int GATE>
+__global__ __launch_bounds__(TPR* rows_per_group<TPR>()) void block_norm_backward_ahead_kernel(
+    BlockNormDev p, BlockNormBackDev q) {
+  using GT = typename std::conditional<GATE == 2, float, uint16_t>::type;
+  __shared__ f32x2 lds[2 * TPR / 64];
+  extern __shared__ __attribute__((aligned(16))) float par[];  // [4][D] alpha, post, pre, gate
+  RowSum<TPR> row_sum{lds};
+  const int tid = threadIdx.x % TPR;
+  const int group = blockIdx.x * rows_per_group<TPR>() + threadIdx.x / TPR;
+  const int ngroups = gridDim.x * rows_per_group<TPR>();
+  const int D = p.D;
+  const float invd = 1.0f / D;
+  const bool post = p.post.p != nullptr;
+  auto col = [&](int i) { return (i * TPR + tid) * 8; };
+  for (int c = threadIdx.x; c < D; c += TPR * rows_per_group<TPR>())
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const ParamVec w = i == 0 ? p.alpha : (i == 1 ? p.post : (i == 2 ? p.pre : p.gate));
+      float v = 1.f;
+      if (w.p && (i < 3 || p.gate_kind == 1))
+        v = w.bf16 ? bf16_to_f32(static_cast<const uint16_t*>(w.p)[c])
+                   : static_cast<const float*>(w.p)[c];
+      par[i * D + c] = v;
+    }
+  __syncthreads();
+  auto param = [&](int i, int c, float (&v)[8]) __attribute__((always_inline)) {
+    load8v<TPR, true>(par + i * D, c, D, v);
+  };
+
+  float spost[NC][8], spre[NC][8], salpha[NC][8], sgate[NC][8];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    fill8(spost[i], 0.f);
+    fill8(spre[i], 0.f);
+    fill8(salpha[i], 0.f);
+    fill8(sgate[i], 0.f);
+  }
+  struct Row {
+    Raw8<HT> h[NC], dho[NC];
+    Raw8<YT> y[NC], dx[NC];
+    Raw8<GT> g[GATE ? NC : 1];
+    f32x2 st;
+    float gt;
+  };
+  auto load_row = [&](Row& r, int t) __attribute__((always_inline)) {
+    const size_t at = (size_t)t * D;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      // threads past the row's end read its first columns (used nowhere)
+      const int c = col(i) < D ? col(i) : 0;
+      r.h[i].load(p.h, (size_t)t * p.hs + c);
+      r.y[i].load(p.y, (size_t)t * p.ys + c);
+      r.dho[i].load(q.dh_out, at + c);
+      r.dx[i].load(q.dx, at + c);
+      if constexpr (GATE > 0) r.g[i].load(p.gate.p, at + c);
+    }
+    r.st = *reinterpret_cast<const f32x2*>(q.stats + 2 * (size_t)t);
+    r.gt = 1.f;
+    if (p.gate_kind == 2)
+      r.gt = p.gate.bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p.gate.p)[t])
+                         : static_cast<const float*>(p.gate.p)[t];
+  };
+  Row next;
+  if (group < p.T) load_row(next, group);
+  for (int t = group; t < p.T; t += ngroups) {
+    Row row = next;
+    if (t + ngroups < p.T) load_row(next, t + ngroups);
+    const float ry = row.st[0], rh = row.st[1];
+    // the values that two passes share: alpha h, g and n = post yn; yn = y ry
+    auto gate = [&](int i, int c, float (&g)[8]) __attribute__((always_inline)) {
+      if constexpr (GATE > 0) {
+        row.g[i].get(g);
+      } else {
+        param(3, c, g);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) g[v] *= row.gt;
+      }
+    };
+    auto normed = [&](int i, float (&yn)[8]) __attribute__((always_inline)) {
+      row.y[i].get(yn);
+#pragma unroll
+      for (int v = 0; v < 8; ++v) yn[v] *= ry;
+    };
+    auto renew = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        row.h[i].renew();
+        row.dho[i].renew();
+        row.y[i].renew();
+        row.dx[i].renew();
+        if constexpr (GATE > 0) row.g[i].renew();
+      }
+    };
+    float s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = col(i);
+      if (c < D) {
+        float h[8], yn[8], g[8], d[8], al[8], w[8], pr[8];
+        row.h[i].get(h);
+        row.dx[i].get(d);
+        normed(i, yn);
+        gate(i, c, g);
+        param(0, c, al);
+        param(1, c, w);
+        param(2, c, pr);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const float hn = (al[v] * h[v] + g[v] * (w[v] * yn[v])) * rh;
+          spre[i][v] = fmaf(d[v], hn, spre[i][v]);
+          s1 = fmaf(d[v] * pr[v], hn, s1);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one piece's values at a time
+    }
+    const float m1 = row_sum(s1, 0.f)[0] * invd;
+    renew();
+    // G, dh, the column sums, dg and b = post g G
+    float s2 = 0.f, s3 = 0.f;
+    float b[NC][8];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = col(i);
+      fill8(b[i], 0.f);
+      if (c < D) {
+        float h[8], yn[8], g[8], al[8], w[8], G[8], d[8], pr[8];
+        row.h[i].get(h);
+        normed(i, yn);
+        gate(i, c, g);
+        param(0, c, al);
+        param(1, c, w);
+        row.dho[i].get(G);
+        row.dx[i].get(d);
+        param(2, c, pr);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const float n = w[v] * yn[v];
+          const float hn = (al[v] * h[v] + g[v] * n) * rh;
+          G[v] += rh * (d[v] * pr[v] - hn * m1);
+          salpha[i][v] = fmaf(G[v], h[v], salpha[i][v]);
+          const float dn = G[v] * g[v];
+          const float dg = G[v] * n;
+          spost[i][v] = fmaf(dn, yn[v], spost[i][v]);
+          if constexpr (GATE == 0) {
+            sgate[i][v] += dg;
+            s3 += dg;
+          }
+          g[v] = dg;
+          b[i][v] = w[v] * dn;
+          s2 = fmaf(b[i][v], yn[v], s2);
+          G[v] *= al[v];
+        }
+        store8v<TPR, true>(static_cast<HT*>(q.dh) + (size_t)t * D, c, D, G);
+        if constexpr (GATE > 0)
+          if (q.dgate) store8v<TPR, true>(static_cast<GT*>(q.dgate) + (size_t)t * D, c, D, g);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const f32x2 s = row_sum(s2, s3);
+    const float m2 = post ? s[0] * invd : 0.f;
+    if (p.gate_kind == 2 && q.dgate && tid == 0) {
+      if (q.dgate_bf16)
+        static_cast<uint16_t*>(q.dgate)[t] = f32_to_bf16(s[1]);
+      else
+        static_cast<float*>(q.dgate)[t] = s[1];
+    }
+    renew();
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = col(i);
+      if (c >= D) continue;
+      float yn[8];
+      normed(i, yn);
+#pragma unroll
+      for (int v = 0; v < 8; ++v) b[i][v] = ry * (b[i][v] - yn[v] * m2);
+      store8v<TPR, true>(static_cast<YT*>(q.dy) + (size_t)t * D, c, D, b[i]);
+    }
+  }
+  float* part = q.part + (size_t)group * q.nsums * D;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = col(i);
+    if (c >= D) continue;
+    if (q.s_post >= 0) store8v<TPR, true>(part + (size_t)q.s_post * D, c, D, spost[i]);
+    if (q.s_pre >= 0) store8v<TPR, true>(part + (size_t)q.s_pre * D, c, D, spre[i]);
+    if (q.s_alpha >= 0) store8v<TPR, true>(part + (size_t)q.s_alpha * D, c, D, salpha[i]);
+    if (q.s_gate >= 0) store8v<TPR, true>(part + (size_t)q.s_gate * D, c, D, sgate[i]);
+  }
+}
+
 // Column sums: out[slot][c] = sum over g of part[g][slot][c], g in a fixed
 // order.  A work-group adds 64 columns of one slot, its 16 waves every 16th
 // group each.
@@ -531,6 +765,7 @@ hipError_t block_norm_backward(const BlockNormProblem& b, const BlockNormGrads& 
   const bool vec = inputs_vec(b) && vec_ok(g.dh_out, 0, 1) && vec_ok(g.dx, 0, 1) &&
                    vec_ok(g.dh, 0, 1) && vec_ok(g.dy, 0, 1) &&
                    (b.gate_kind != 3 || vec_ok(g.dgate, 0, 1));
+  const bool ahead = vec && b.y && g.dh_out && g.dx && g.dh && g.dy;
   const int grid = backward_blocks(b.T, b.D);
   // no rows: the column sums below are of nothing and write zeros
   if (b.T > 0) with_types(b.h_bf16, b.y_bf16, [&](auto ht, auto yt) {
@@ -539,6 +774,17 @@ hipError_t block_norm_backward(const BlockNormProblem& b, const BlockNormGrads& 
     auto launch = [&](auto tpr, auto nc) {
       constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
       constexpr int RPG = rows_per_group<TPR>();
+      if constexpr (TPR < 1024)
+        if (ahead) {
+          const size_t lds = (size_t)4 * b.D * sizeof(float);
+          if (b.gate_kind != 3)
+            block_norm_backward_ahead_kernel<HT, YT, TPR, NC, 0><<<grid, TPR * RPG, lds, s>>>(p, q);
+          else if (b.gate.bf16)
+            block_norm_backward_ahead_kernel<HT, YT, TPR, NC, 1><<<grid, TPR * RPG, lds, s>>>(p, q);
+          else
+            block_norm_backward_ahead_kernel<HT, YT, TPR, NC, 2><<<grid, TPR * RPG, lds, s>>>(p, q);
+          return;
+        }
       if (vec)
         block_norm_backward_kernel<HT, YT, TPR, NC, true><<<grid, TPR * RPG, 0, s>>>(p, q);
       else

@@ -113,10 +113,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(const T* __restrict__
   const int c = (int)(b - row * nb) * 128 + (threadIdx.x & 15) * 8;
   float v[8];
   fp8_load8<VEC>(x + row * stride, c, cols, v);
-  float m = max8(v);
-#pragma unroll
-  for (int off = 1; off < 16; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  const float s = fp8_scale(m);
+  const float s = fp8_scale(row16_reduce(max8(v), MaxOp{}));
   fp8_store8<VEC>(codes + row * cols, c, cols, fp8_pack8(v, s));
   if ((threadIdx.x & 15) == 0) scales[b] = s;
 }
@@ -145,8 +142,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_weight_kernel(const T* __res
       m = fmaxf(m, max8(v[i]));
     }
   }
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  m = wave_reduce(m, MaxOp{});
   if ((threadIdx.x & 63) == 0) wm[threadIdx.x >> 6] = m;
   __syncthreads();
   const float s = fp8_scale(fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3])));

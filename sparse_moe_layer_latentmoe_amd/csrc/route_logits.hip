@@ -17,8 +17,14 @@
 // that bound are the candidates next to it computed again in fp64.
 //
 // One wavefront per token, expert 64 j + lane in slot j of lane `lane`, all
-// in registers; the K-th largest key is found bit by bit with one ballot per
-// slot, ending at the first bit whose count is exactly K.
+// in registers.  The K-th largest key of a set is found bit by bit, a ballot
+// and a population count per slot and bit, ending at the first bit whose count
+// is exactly K.  That count is what the kernel spends its time on, so with
+// several slots it runs on one key a lane: first on the lanes' largest keys,
+// whose K-th largest bounds the K-th largest of all from below; then the few
+// keys that reach that bound move to one a lane (through LDS, ids ascending)
+// and are searched again.  Where more than 64 reach it (equal keys), or the
+// border turns out closer than the scores' error, all slots are searched.
 #include <cfloat>
 #include <type_traits>
 
@@ -81,17 +87,20 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-template <class F>
-__device__ __forceinline__ F wave_sum(F v) {
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
   return v;
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
+__device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, AddOp{}); }
+__device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, MaxOp{}); }
+
+// exp and 1 / x in one instruction each (2^x and 1 / x within 1 ulp; the
+// argument's rounding adds 2^-24 |x log2 e| of the result).
+__device__ __forceinline__ float fast_exp(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504f);
 }
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
 // A logit as the kernels use it: NaN and -inf mean "not available" (-inf),
 // +inf counts as the largest finite value.
@@ -99,24 +108,43 @@ __device__ __forceinline__ float clean_logit(float v) {
   return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY;
 }
 
-// Sum of the `best` (1 or 2) largest of the G values of group `lane` in the
-// wave's LDS row; the walk starts at a different place in each lane, so that
-// groups of 32 or 64 do not meet in one LDS bank.
+// Sums of the `best` (1 or 2) largest of each group's G values in the wave's
+// LDS row; lane g returns group g's.  Each group is walked by P lanes (the
+// largest power of two with n_group P <= 64), whose two largest are then
+// merged; the walk starts at a different place in each group, so that groups
+// a multiple of 64 apart do not meet in one LDS bank.
 template <class F>
-__device__ __forceinline__ F group_best(const F* row, int lane, int G, int best) {
+__device__ __forceinline__ F group_best(const F* row, int lane, int n_group, int G, int best) {
+  int sh = 0;
+  while ((n_group << (sh + 1)) <= 64) ++sh;
+  const int P = 1 << sh, g = lane >> sh, i = lane & (P - 1);
+  const int steps = (G + P - 1) >> sh;
   F t1 = -INFINITY, t2 = -INFINITY;
-  int i = lane % G;
-  for (int n = 0; n < G; ++n) {
-    const F b = row[lane * G + i];
-    if (b > t1) {
-      t2 = t1;
-      t1 = b;
-    } else if (b > t2) {
-      t2 = b;
+  if (g < n_group) {
+    const F* at = row + g * G + i;
+    int n = g % steps;
+    // four reads in flight (past the last step: read again, taken as -inf)
+    for (int k = 0; k < steps; k += 4) {
+      F b[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        b[u] = k + u < steps && i + (n << sh) < G ? at[n << sh] : -INFINITY;
+        n = n + 1 == steps ? 0 : n + 1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        t2 = fmax(t2, fmin(t1, b[u]));
+        t1 = fmax(t1, b[u]);
+      }
     }
-    i = i + 1 == G ? 0 : i + 1;
   }
-  return best == 2 ? t1 + t2 : t1;
+  for (int off = 1; off < P; off <<= 1) {
+    const F o1 = __shfl_xor(t1, off, 64), o2 = __shfl_xor(t2, off, 64);
+    t2 = fmax(fmax(t2, o2), fmin(t1, o1));
+    t1 = fmax(t1, o1);
+  }
+  const F r = best == 2 ? t1 + t2 : t1;
+  return __shfl(r, lane < n_group ? lane << sh : 0, 64);
 }
 
 // The lanes of the n largest keys (one per lane; equal keys: lower lanes).
@@ -165,7 +193,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      s[j] = l[j] > -INFINITY ? expf(l[j] - m) : 0.f;
+      s[j] = l[j] > -INFINITY ? fast_exp(l[j] - m) : 0.f;
       sum += s[j];
     }
     sum = wave_sum(sum);
@@ -174,14 +202,15 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
     for (int j = 0; j < NJ; ++j) s[j] *= inv;
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) s[j] = l[j] > -INFINITY ? 1.0f / (1.0f + expf(-l[j])) : 0.f;
+    for (int j = 0; j < NJ; ++j) s[j] = l[j] > -INFINITY ? fast_rcp(1.0f + fast_exp(-l[j])) : 0.f;
   }
-  // Error bound of a biased score: a sigmoid is within 4 ulp of its value
-  // (exp 1, add 1/2, divide 1/2 and their propagation) and at most 1; a
-  // softmax score within 2^-19 of the largest one, inv (up to 16 + 6
-  // additions, the rounding of l - m times the exponential's slope, exp and
-  // two products); the bias addition rounds by 2^-24 of its result, which is
-  // added where the border is known.
+  // Error bound of a biased score.  A sigmoid s: the exponential is off by
+  // (2^-23 + 2^-23.4 |l|) of itself, which s passes on times s (1 - s), at most
+  // 1/4 and with |l| at most 0.23; the addition and the reciprocal by 2^-24
+  // and 2^-23 of s: 2^-21.6 in all.  A softmax score: within 2^-19 of the
+  // largest one, inv (up to 16 + 6 additions, the rounding of l - m and the
+  // exponential's, times its value, and two products).  The bias addition
+  // rounds by 2^-24 of its result, which is added where the border is known.
   const float serr = p.softmax ? 0x1p-19f * inv : 0x1p-21f;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
@@ -221,7 +250,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
       if (j * 64 + lane < E) row[j * 64 + lane] = b[j];
     wave_lds_fence();
     const bool has = lane < p.n_group;
-    const float gs = has ? group_best(row, lane, G, p.best) : -INFINITY;
+    const float gs0 = group_best(row, lane, p.n_group, G, p.best);
+    const float gs = has ? gs0 : -INFINITY;
     const uint32_t gk[1] = {has ? key32(gs) : 0u};
     const uint32_t gv = border<uint32_t, 1>(gk, p.topk_group);
     const float gt = key32_value(gv);
@@ -238,8 +268,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
       for (int j = 0; j < NJ; ++j)
         if (j * 64 + lane < E) row64[j * 64 + lane] = biased64(j);
       wave_lds_fence();
-      kept = best_lanes<uint64_t>(has ? key64(group_best(row64, lane, G, p.best)) : 0ull,
-                                  p.topk_group, below);
+      const double g64 = group_best(row64, lane, p.n_group, G, p.best);
+      kept = best_lanes<uint64_t>(has ? key64(g64) : 0ull, p.topk_group, below);
     } else {
       kept = best_lanes<uint32_t>(gk[0], p.topk_group, below);
     }
@@ -250,6 +280,66 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
         key[j] = 0u;
         b[j] = -INFINITY;
       }
+    }
+  }
+
+  if constexpr (NJ > 1) {
+    // lanes' largest keys -> a lower bound of the K-th largest of all
+    uint32_t top[1] = {key[0]};
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) top[0] = key[j] > top[0] ? key[j] : top[0];
+    const uint32_t low = border<uint32_t, 1>(top, K);
+    uint64_t in[NJ];
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      in[j] = __ballot(key[j] >= low);
+      n += __popcll(in[j]);
+    }
+    if (low > kKeyMinusInf && n <= 64) {
+      // their keys, ids and scores to one a lane
+      uint32_t* const ck = reinterpret_cast<uint32_t*>(rows[wv]);
+      int base = 0;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        if (key[j] >= low) {
+          const int pos = base + __popcll(in[j] & below);
+          ck[pos] = key[j];
+          ck[64 + pos] = j * 64 + lane;
+          ck[128 + pos] = __float_as_uint(s[j]);
+        }
+        base += __popcll(in[j]);
+      }
+      wave_lds_fence();
+      const uint32_t k1[1] = {lane < n ? ck[lane] : 0u};
+      const int id = ck[64 + lane];
+      const float sc = __uint_as_float(ck[128 + lane]);
+      // at least `low`, so that no key left out lies above it
+      uint32_t v = border<uint32_t, 1>(k1, K);
+      v = v > low ? v : low;
+      bool far = true;  // no key within the scores' error of the border
+      if (bias) {
+        const float bt = key32_value(v), kv = key32_value(k1[0]);
+        const float err = 2.f * serr + 0x1p-22f * fabsf(bt);
+        const int over = __popcll(__ballot(lane < n && kv >= bt + 2.f * err));
+        const int upto = __popcll(__ballot(lane < n && kv > bt - 2.f * err));
+        // keys below `low` are not among these: it has to be out of reach too
+        far = (over == K || upto == K) && (over == K || bt - 2.f * err >= key32_value(low));
+      }
+      if (far) {
+        const uint64_t gt = __ballot(k1[0] > v), eq = __ballot(k1[0] == v);
+        const int room = K - __popcll(gt);
+        const bool on = k1[0] > v || (k1[0] == v && __popcll(eq & below) < room);
+        const uint64_t mk = __ballot(on);
+        const float sum = wave_sum(on ? sc : 0.f);
+        if (on) {
+          const size_t at = (size_t)t * K + __popcll(mk & below);
+          idx_out[at] = id;
+          w_out[at] = p.renorm ? sc * (p.rho / (sum + 1e-20f)) : sc * p.rho;
+        }
+        return;
+      }
+      wave_lds_fence();
     }
   }
 
@@ -347,7 +437,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_backward_kernel
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      s[j] = s[j] > -INFINITY ? expf(s[j] - m) : 0.f;
+      s[j] = s[j] > -INFINITY ? fast_exp(s[j] - m) : 0.f;
       sum += s[j];
     }
     sum = wave_sum(sum);
@@ -358,10 +448,10 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_backward_kernel
 
   float sk, slope;  // score of slot `lane` of the selection, and (sigmoid) s (1 - s)
   if (p.softmax) {
-    sk = lk > -INFINITY ? expf(lk - m) * inv : 0.f;
+    sk = lk > -INFINITY ? fast_exp(lk - m) * inv : 0.f;
     slope = sk;
   } else {
-    const float ex = lk > -INFINITY ? expf(-fabsf(lk)) : 0.f;
+    const float ex = lk > -INFINITY ? fast_exp(-fabsf(lk)) : 0.f;
     const float r = 1.0f / (1.0f + ex);
     sk = lk > -INFINITY ? (lk >= 0.f ? r : ex * r) : 0.f;
     slope = ex * r * r;

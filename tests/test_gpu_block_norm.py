@@ -90,6 +90,12 @@ def check(T, D, ht=B, yt=B, pt=B, gate="channel", post=True, pre=True, alpha=Tru
     close(g1.dh, *b1["dh"], 2.0 ** -15, "dh alone")
     if pre:
         assert not g1.dpre_weight.any()
+        g2 = pkg.block_norm_backward(h, yv, stats, dx=dx, eps=eps, **p)
+        b2 = R.block_norm_backward(exact(h), exact(yv), None, exact(dx), e["pre_weight"],
+                                   e["post_weight"], e["gate"], e["res_scale"], eps)
+        for name in ("dh", "dy", "dpre_weight", "dgate"):
+            if name in b2:
+                close(getattr(g2, name), *b2[name], 2.0 ** -15, name + " of x alone")
 
 
 @pytest.mark.parametrize("T", [1, 5, 67])
