@@ -283,8 +283,8 @@ typedef struct {
 } lmoe_router;
 
 /* logits: [T, E] of `logits_type`, rows `logits_stride` (>= E) elements
- * apart; bias: fp32 [E], finite, or NULL.  Writes topk_idx [T, K] (ascending
- * ids) and topk_w [T, K]. */
+ * apart; bias: fp32 [E], finite, or NULL; T up to 2^22.  Writes topk_idx
+ * [T, K] (ascending ids) and topk_w [T, K]. */
 lmoe_status lmoe_route_logits(const lmoe_router *router, const void *logits, int32_t logits_type,
                               int64_t logits_stride, const float *bias, int32_t T,
                               int32_t *topk_idx, float *topk_w, void *stream);
@@ -323,7 +323,7 @@ typedef struct {
   int32_t gate_kind;       /* lmoe_gate (LMOE_GATE_NONE if y is NULL) */
   int32_t h_type, y_type;  /* lmoe_dtype: of h, h_out and their gradients; of y, x and theirs */
   int32_t pre_type, post_type, res_scale_type, gate_type; /* lmoe_dtype */
-  int32_t T, D;            /* D: 1..16384 */
+  int32_t T, D;            /* T: 0..2^22 - 1, D: 1..16384 */
   float eps;               /* finite, > 0 */
 } lmoe_block_norm_args;
 
@@ -363,13 +363,13 @@ lmoe_status lmoe_block_norm_backward(const lmoe_block_norm_args *a, const float 
  *
  * Activations: x [rows, cols] (of `x_type`, rows x_stride >= cols elements
  * apart), a scale for each block of a row: codes [rows, cols], scales [rows,
- * ceil(cols / 128)].  Any cols >= 1. */
+ * ceil(cols / 128)].  Any cols >= 1, fewer than 2^28 blocks. */
 lmoe_status lmoe_quantize_fp8(const void *x, int32_t x_type, int64_t rows, int32_t cols,
                               int64_t x_stride, uint8_t *codes, float *scales, void *stream);
 
 /* Weights: `matrices` matrices w [rows, cols], dense, a scale for each block
  * of 128 rows x 128 columns (smaller at the edges): codes like w, scales
- * [matrices, ceil(rows / 128), ceil(cols / 128)]. */
+ * [matrices, ceil(rows / 128), ceil(cols / 128)], fewer than 2^24 of them. */
 lmoe_status lmoe_quantize_fp8_weight(const void *w, int32_t w_type, int64_t matrices, int32_t rows,
                                      int32_t cols, uint8_t *codes, float *scales, void *stream);
 

@@ -527,8 +527,8 @@ __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, cons
     const int b = w % NSB, i = w / NSB;
     if (i < kFp8MaxBlocks / 64)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rws, (lds_void*)(sws + b * kFp8MaxBlocks + i * 64), 4, lane * 4, (b * KBT + i * 64) * 4, 0,
-          0);
+          rws, (lds_void*)(sws + b * kFp8MaxBlocks + i * 64), 4, lane * 4,
+          (b * KBT + i * 64) * 4, 0, 0);
   }
   // what the first MFMAs need, then what step 0 reads, then what it need not
   // wait for
@@ -867,6 +867,9 @@ int grouped_tiles(int rows, int groups, int tile_m) {
 
 long xcd_grid(long work) { return kXcds * ((work + kXcds - 1) / kXcds); }
 
+// A launch has fewer than 2^32 threads.
+bool too_many(long grid, int threads) { return grid >= (1L << 32) / threads; }
+
 // Four waves x 4 row groups: 589 and 559 us for the decode batch's up and down
 // projection, against 644 and 557 for 8 x 2, 615 and 563 for 4 x 2, 928 and
 // 601 for 8 x 1; 595 and 565 for 4 x 8, which quantises its output.
@@ -877,11 +880,13 @@ hipError_t launch_grouped(const Fp8Gemm& p, const Plan& plan, const Tile* tiles,
   if (plan.stream) {
     constexpr int RG = std::is_same<OUT, Relu2Fp8>::value ? 8 : 4, NW = 4;
     const long grid = (long)max_tiles * ((p.N + 16 * RG - 1) / (16 * RG));
+    if (too_many(grid, NW * 64)) return hipErrorInvalidConfiguration;
     fp8_stream_kernel<true, NW, RG, 1, OUT><<<grid, NW * 64, 0, s>>>(p, tiles, ntiles);
   } else {
+    constexpr int BN = 256;
+    const long grid = xcd_grid((long)max_tiles * ((p.N + BN - 1) / BN));
+    if (too_many(grid, 512)) return hipErrorInvalidConfiguration;
     auto go = [&](auto bm, auto wm) {
-      constexpr int BN = 256;
-      const long grid = xcd_grid((long)max_tiles * ((p.N + BN - 1) / BN));
       fp8_pipe_kernel<true, decltype(bm)::value, BN, decltype(wm)::value, 3, OUT>
           <<<grid, 512, 0, s>>>(p, tiles, ntiles);
     };

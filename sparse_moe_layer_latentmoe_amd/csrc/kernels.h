@@ -149,9 +149,10 @@ hipError_t fp8_quantize(const void* x, bool bf16, long rows, int cols, long stri
                         uint8_t* codes, float* scales, hipStream_t s);
 hipError_t fp8_quantize_weight(const void* w, bool bf16, long matrices, int rows, int cols,
                                uint8_t* codes, float* scales, hipStream_t s);
-// y[m] = x[rows ? rows[m] : m] w^T, K a multiple of 128, N of 16.  groups = 0: one weight matrix for all M rows;
-// else row m takes the matrix of the group whose range offsets[g] ..
-// offsets[g + 1] - 1 holds it (rows of no group are not written).
+// y[m] = x[rows ? rows[m] : m] w^T, K a multiple of 128, N of 16.  groups = 0:
+// one weight matrix for all M rows; else row m takes the matrix of the group
+// whose range offsets[g] .. offsets[g + 1] - 1 holds it (rows of no group are
+// not written).
 constexpr int kFp8MaxBlocks = 256;  // blocks of k that the LDS-tiled product takes
 struct Fp8Gemm {
   const uint8_t* x;     // [x_rows, K]

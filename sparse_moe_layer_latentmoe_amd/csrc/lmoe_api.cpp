@@ -93,9 +93,10 @@ lmoe_status check_config(const lmoe_config* c) {
   if (c->expert_format == LMOE_EXPERTS_MXFP4 &&
       (c->moe_latent_size % 128 || c->moe_intermediate_size % 128))
     return LMOE_ERR_UNSUPPORTED;
-  // FP8 experts: whole scale blocks
+  // FP8 experts: whole scale blocks, latent rows within 32-bit offsets (2 GiB)
   if (c->expert_format == LMOE_EXPERTS_FP8 &&
-      (c->moe_latent_size % 128 || c->moe_intermediate_size % 128))
+      (c->moe_latent_size % 128 || c->moe_intermediate_size % 128 ||
+       static_cast<int64_t>(c->max_tokens) * c->moe_latent_size >= (int64_t{1} << 31)))
     return LMOE_ERR_UNSUPPORTED;
   // block steps: known bits; the pre-norm's epsilon finite and >= 0
   if (c->fuse & ~(LMOE_FUSE_PRENORM | LMOE_FUSE_RESIDUAL)) return LMOE_ERR_INVALID_ARG;
@@ -507,8 +508,9 @@ lmoe_status lmoe_create(const lmoe_config* cfg, const lmoe_weights* w, void* wor
   h->cfg = *cfg;
   // the FP8 fields are read only with that format
   h->w = lmoe_weights{};
-  std::memcpy(&h->w, w, cfg->expert_format == LMOE_EXPERTS_FP8 ? sizeof(lmoe_weights)
-                                                               : offsetof(lmoe_weights, expert_up_fp8));
+  std::memcpy(&h->w, w,
+              cfg->expert_format == LMOE_EXPERTS_FP8 ? sizeof(lmoe_weights)
+                                                     : offsetof(lmoe_weights, expert_up_fp8));
   h->ws = static_cast<char*>(workspace);
   h->L = L;
   const char* dbg = std::getenv("LMOE_DEBUG");

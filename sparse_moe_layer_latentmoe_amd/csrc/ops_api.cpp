@@ -1,6 +1,7 @@
 // C ABI of the operators around the layer (routing from logits, the norms
-// around a block, 8-bit block-scaled matrices): argument checks and launches.  See include/lmoe.h for the
-// contract.  Every check runs on the host before any HIP call.
+// around a block, 8-bit block-scaled matrices): argument checks and launches.
+// See include/lmoe.h for the contract.  Every check runs on the host before
+// any HIP call.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -86,7 +87,8 @@ lmoe_status check_norm(const lmoe_block_norm_args* a) {
   if (a->gate_kind < LMOE_GATE_NONE || a->gate_kind > LMOE_GATE_FULL ||
       (a->gate != nullptr) != (a->gate_kind != LMOE_GATE_NONE && (a->T > 0 || a->gate)))
     return LMOE_ERR_INVALID_ARG;
-  if (a->D > block_norm_max_width() || a->T > kMaxTokens) return LMOE_ERR_UNSUPPORTED;
+  // a launch has fewer than 2^32 threads, up to 1024 of them to a token
+  if (a->D > block_norm_max_width() || a->T >= kMaxTokens) return LMOE_ERR_UNSUPPORTED;
   if (a->T == 0) return LMOE_OK;
   if (!a->h || a->h_stride < a->D) return LMOE_ERR_INVALID_ARG;
   if (a->y ? a->y_stride < a->D : (a->post_weight || a->gate)) return LMOE_ERR_INVALID_ARG;
@@ -258,7 +260,8 @@ lmoe_status lmoe_block_norm_backward(const lmoe_block_norm_args* a, const float*
       (g->dgate && a->gate_kind == LMOE_GATE_NONE) || (g->dpre_weight && !a->pre_weight) ||
       (T > 0 && g->dy && !a->y))
     return LMOE_ERR_INVALID_ARG;
-  if (!aligned(g->dh, he) || !aligned(g->dy, ye) || !aligned(g->dpre_weight, type_size(a->pre_type)) ||
+  if (!aligned(g->dh, he) || !aligned(g->dy, ye) ||
+      !aligned(g->dpre_weight, type_size(a->pre_type)) ||
       !aligned(g->dpost_weight, type_size(a->post_type)) ||
       !aligned(g->dres_scale, type_size(a->res_scale_type)) ||
       !aligned(g->dgate, type_size(a->gate_type)) || !aligned(dh_out, he) || !aligned(dx, ye) ||
@@ -299,7 +302,8 @@ lmoe_status lmoe_quantize_fp8(const void* x, int32_t x_type, int64_t rows, int32
   if (rows > kMaxElements / cols || x_stride > (int64_t{1} << 31)) return LMOE_ERR_UNSUPPORTED;
   if (rows == 0) return LMOE_OK;
   const int64_t nb = (static_cast<int64_t>(cols) + 127) / 128;
-  if (rows * nb > (int64_t{1} << 34)) return LMOE_ERR_UNSUPPORTED;
+  // a launch has fewer than 2^32 threads: 16 to a block
+  if (rows * nb >= (int64_t{1} << 28)) return LMOE_ERR_UNSUPPORTED;
   const lmoe_status st =
       check_quantize(x, x_type, rows, cols, x_stride, rows * nb, codes, scales);
   if (st != LMOE_OK) return st;
@@ -312,7 +316,8 @@ lmoe_status lmoe_quantize_fp8_weight(const void* w, int32_t w_type, int64_t matr
   if (matrices < 0 || rows <= 0 || cols <= 0 || !is_type(w_type)) return LMOE_ERR_INVALID_ARG;
   const int64_t nb = ((static_cast<int64_t>(rows) + 127) / 128) *
                      ((static_cast<int64_t>(cols) + 127) / 128);
-  if (matrices > (int64_t{1} << 30) / nb) return LMOE_ERR_UNSUPPORTED;
+  // a launch has fewer than 2^32 threads: 256 to a block
+  if (matrices > ((int64_t{1} << 24) - 1) / nb) return LMOE_ERR_UNSUPPORTED;
   if (matrices == 0) return LMOE_OK;
   const lmoe_status st =
       check_quantize(w, w_type, matrices * rows, cols, cols, matrices * nb, codes, scales);

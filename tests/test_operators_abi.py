@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+import lmoe_inputs as li
 import sparse_moe_layer_latentmoe_amd as pkg
 from oracle import operators as R
 
@@ -128,6 +129,145 @@ def test_block_norm_outputs_are_checked(lib):
     c = norm_args(y=None, post_weight=None, gate=None, gate_kind=0)
     assert back(c, at(8), None, at(7), G(None, at(10), None, None, None, None), at(15), 1 << 30,
                 None) == INV
+
+
+@pytest.mark.parametrize("T,D", [((1 << 22) - 1, 8192), (1, 16384), (1 << 22, 8)])
+def test_block_norm_sizes_at_their_limits(lib, T, D):
+    a = norm_args(T=T, D=D, h_stride=D, y_stride=D, h=None)   # refused for h, not for its size
+    assert lib.lmoe_block_norm(a, at(6), at(7), None, None) == (UNS if T >> 22 else INV)
+
+
+def test_quantiser_arguments_are_checked(lib):
+    q = lib.lmoe_quantize_fp8
+    base = dict(x=at(0), t=1, rows=4, cols=200, stride=200, codes=at(1), scales=at(2))
+
+    def call(**kw):
+        v = {**base, **kw}
+        return q(v["x"], v["t"], v["rows"], v["cols"], v["stride"], v["codes"], v["scales"], None)
+
+    assert call(rows=0, x=None, codes=None, scales=None) == pkg.LMOE_OK
+    for kw in (dict(x=None), dict(codes=None), dict(scales=None), dict(t=2), dict(t=-1),
+               dict(rows=-1), dict(cols=0), dict(stride=199), dict(x=at(0) + 1),
+               dict(scales=at(2) + 2), dict(codes=at(0) + 1599), dict(scales=at(1) + 796),
+               dict(t=0, x=at(0) + 2), dict(codes=at(2) + 28)):
+        assert call(**kw) == INV, kw
+    assert call(rows=1 << 27) == UNS                   # 2^28 blocks
+    assert call(rows=1 << 40, cols=1, stride=1) == UNS
+    assert call(stride=(1 << 31) + 1) == UNS
+    qw = lib.lmoe_quantize_fp8_weight
+    assert qw(None, 1, 0, 64, 64, None, None, None) == pkg.LMOE_OK
+    for args in ((None, 1, 2, 64, 64, at(1), at(2)), (at(0), 1, 2, 64, 64, None, at(2)),
+                 (at(0), 1, 2, 64, 64, at(1), None), (at(0), 3, 2, 64, 64, at(1), at(2)),
+                 (at(0), 1, -1, 64, 64, at(1), at(2)), (at(0), 1, 2, 0, 64, at(1), at(2)),
+                 (at(0), 1, 2, 64, 0, at(1), at(2)), (at(0) + 1, 1, 2, 64, 64, at(1), at(2)),
+                 (at(0), 1, 2, 64, 64, at(0) + 16383, at(2)),
+                 (at(0), 1, 2, 64, 64, at(1), at(1) + 8188)):
+        assert qw(*args, None) == INV, args
+    assert qw(at(0), 1, 1 << 22, 129, 129, at(1), at(2), None) == UNS   # 2^24 blocks
+
+
+def mm_args(**kw):
+    a = pkg.LmoeFp8MatmulArgs()
+    for k, v in dict(x=at(0), x_scales=at(1), w=at(2), w_scales=at(3), rows=None, offsets=None,
+                     y=at(4), y_type=1, n_groups=0, M=40, x_rows=40, N=256, K=1024).items():
+        setattr(a, k, v)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(n_groups=-1), INV),
+    (dict(x_rows=0), INV), (dict(y_type=2), INV), (dict(x=None), INV), (dict(x_scales=None), INV),
+    (dict(w=None), INV), (dict(w_scales=None), INV), (dict(y=None), INV),
+    (dict(x=at(0) + 8), INV), (dict(w=at(2) + 4), INV), (dict(y=at(4) + 8), INV),
+    (dict(w_scales=at(3) + 2), INV), (dict(rows=at(5) + 2), INV), (dict(x_rows=39), INV),
+    (dict(offsets=at(5)), INV), (dict(n_groups=3), INV), (dict(y=at(0) + 1024), INV),
+    (dict(y=at(2) + (1 << 18) - 16), INV), (dict(y=at(1) - 16), INV),
+    (dict(rows=at(4) + 32), INV), (dict(N=250), UNS), (dict(K=1000), UNS), (dict(K=65664), UNS),
+    (dict(N=(1 << 20) + 16), UNS), (dict(M=(1 << 24) + 1, x_rows=1 << 25), UNS),
+    (dict(n_groups=1025, offsets=at(5)), UNS),
+    (dict(rows=at(5), x_rows=1 << 21), UNS)])
+def test_product_arguments_are_checked(lib, kw, status):
+    a = mm_args(**kw)
+    assert lib.lmoe_fp8_matmul_workspace_size(a) == 0
+    assert lib.lmoe_fp8_matmul(a, at(6), 1 << 30, None) == status
+
+
+def test_product_workspace_is_checked(lib):
+    size, mm = lib.lmoe_fp8_matmul_workspace_size, lib.lmoe_fp8_matmul
+    assert mm(None, None, 0, None) == INV and size(None) == 0
+    assert size(mm_args(M=0)) == 0 and mm(mm_args(M=0, x=None), None, 0, None) == pkg.LMOE_OK
+    assert size(mm_args(M=5)) == 0                     # one pass over the weights
+    split = mm_args(M=150, x_rows=150, N=2048, K=8192)  # few tiles: k is split
+    grouped = mm_args(n_groups=3, offsets=at(5))
+    for a in (split, grouped):
+        need = size(a)
+        assert need > 0
+        assert mm(a, None, need, None) == WS
+        assert mm(a, at(6), need - 1, None) == WS
+        assert mm(a, at(6) + 8, need, None) == WS
+        assert mm(a, at(0), need, None) == INV         # on x
+        assert mm(a, at(4), need, None) == INV         # on y
+    # a part's sums are fp32 [M, N]
+    assert size(split) % (150 * 2048 * 4) == 0
+
+
+def test_fp8_layer_settings_are_checked(lib):
+    sh = li.LayerShape(256, 128, 16, 4, 256, 512, 5.0)
+
+    def create(c, **kw):
+        w = pkg.LmoeWeights()
+        for name in ("fc1_latent", "router", "router_bias", "fc2_latent", "shared_up",
+                     "shared_down", "expert_up_fp8", "expert_up_fp8_scale", "expert_down_fp8",
+                     "expert_down_fp8_scale"):
+            setattr(w, name, kw.get(name, FAKE))
+        h = ctypes.c_void_p()
+        return lib.lmoe_create(c, w, FAKE, 1 << 40, ctypes.byref(h))
+
+    c = pkg.make_config(sh, 64, expert_format=pkg.EXPERTS_FP8)
+    assert 0 < pkg.workspace_size(c) < pkg.workspace_size(pkg.make_config(sh, 64)) + (1 << 16)
+    for name in ("expert_up_fp8", "expert_up_fp8_scale", "expert_down_fp8",
+                 "expert_down_fp8_scale"):
+        assert create(c, **{name: None}) == INV
+        assert create(c, **{name: FAKE + 8}) == INV
+    for bad in (li.LayerShape(256, 192, 16, 4, 256, 512, 5.0),
+                li.LayerShape(256, 128, 16, 4, 320, 512, 5.0)):
+        assert create(pkg.make_config(bad, 64, expert_format=pkg.EXPERTS_FP8)) == UNS
+    # latent rows past 2 GiB
+    long = li.LayerShape(256, 2048, 16, 4, 256, 512, 5.0)
+    assert create(pkg.make_config(long, 1 << 20, expert_format=pkg.EXPERTS_FP8)) == UNS
+
+
+def test_fp8_weight_specs():
+    spec = pkg.weight_specs(li.FULL, pkg.EXPERTS_FP8)
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    assert "expert_up" not in spec and "expert_up_mxfp4" not in spec
+    assert spec["expert_up_fp8"] == ((512, 5120, 2048), e4m3)
+    assert spec["expert_up_fp8_scale"] == ((512, 40, 16), f32)
+    assert spec["expert_down_fp8"] == ((512, 2048, 5120), e4m3)
+    assert spec["expert_down_fp8_scale"] == ((512, 16, 40), f32)
+
+
+def test_binding_refuses_matrices_it_cannot_pass():
+    e4m3 = torch.float8_e4m3fn
+    x, xs = torch.zeros(4, 256).to(e4m3), torch.zeros(4, 2)
+    with pytest.raises(TypeError, match="dtype"):
+        pkg.quantize_fp8(torch.zeros(4, 256, dtype=torch.float16))
+    with pytest.raises(ValueError, match="GPU"):
+        pkg.quantize_fp8(torch.zeros(4, 256))
+    with pytest.raises(ValueError, match="dimensions"):
+        pkg.quantize_fp8(torch.zeros(256))
+    with pytest.raises(ValueError, match="contiguous"):
+        pkg.quantize_fp8_weight(torch.zeros(256, 128).t())
+    with pytest.raises(ValueError, match="GPU"):
+        pkg.quantize_fp8_weight(torch.zeros(128))
+    with pytest.raises(TypeError, match="dtype"):
+        pkg.fp8_matmul(xs, xs, x, xs)
+    with pytest.raises(ValueError, match="contiguous"):
+        pkg.fp8_matmul(torch.zeros(256, 4).to(e4m3).t(), xs, x, xs)
+    with pytest.raises(ValueError, match="GPU"):
+        pkg.fp8_matmul(x, xs, x, xs)
 
 
 def test_binding_refuses_tensors_it_cannot_pass():
