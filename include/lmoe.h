@@ -373,8 +373,10 @@ lmoe_status lmoe_quantize_fp8(const void *x, int32_t x_type, int64_t rows, int32
 lmoe_status lmoe_quantize_fp8_weight(const void *w, int32_t w_type, int64_t matrices, int32_t rows,
                                      int32_t cols, uint8_t *codes, float *scales, void *stream);
 
-/* The product of such activations and weights, y [M, N] = x w^T with fp32
- * sums, rounded once to y_type:
+/* The product of such activations and weights, y [M, N] = x w^T, rounded once
+ * to y_type (fp32 y: fp32 sums throughout; bf16 y: the sum over a block of k is
+ * the 8-bit matrix instruction's, which keeps about 17 bits of it, and the
+ * blocks are scaled and added in fp32):
  *   y[m][n] = sum_b xs[r][b] ws[n / 128][b] sum_{k in block b} x[r][k] w[n][k]
  * with r = rows[m], or m when rows is NULL.  With n_groups >= 1 there are
  * that many weight matrices and row m takes matrix g of the range offsets[g]

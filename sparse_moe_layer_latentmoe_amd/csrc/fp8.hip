@@ -7,7 +7,11 @@
 //
 // Each block's sum of code products is one MFMA 16x16x128 from a zero
 // accumulator; it is scaled in fp32 into the running sum (four fused
-// multiply-adds per MFMA and lane, which run beside the next MFMA).  Weights
+// multiply-adds per MFMA and lane, which run beside the next MFMA).  That
+// instruction keeps about 17 bits of the block's sum, well below what the
+// result keeps where it is rounded to bf16 or e4m3; fp32 results take the
+// bf16 MFMA on converted codes instead (EXACT: four 16x16x32, sums in fp32).
+// Weights
 // are the MFMA's A operand and tokens its B operand, so a lane's four results
 // are consecutive columns of one token and the scale is one factor per lane.
 //
@@ -217,6 +221,15 @@ __device__ __forceinline__ long fp8_x_row(const Fp8Gemm& p, int m, bool& ok) {
 // columns in ys; N a multiple of 128).
 struct Relu2Fp8 {};
 
+// A fragment as the products take it.
+template <bool EXACT>
+using Frag = typename std::conditional<EXACT, Bf16Frag, i32x8>::type;
+template <bool EXACT>
+__device__ __forceinline__ Frag<EXACT> as_frag(i32x8 a) {
+  if constexpr (EXACT) return fp8_to_bf16(a);
+  else return a;
+}
+
 // Four values / s as codes.
 __device__ __forceinline__ uint32_t fp8_codes4(f32x4 v, float s) {
   if (s >= kFastScale) {
@@ -260,6 +273,7 @@ template <bool GROUPED, int NW, int RG, int U, class OUT>
 __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Tile* tiles,
                                                              const int* ntiles) {
   static_assert(RG <= 8, "one scale block");
+  constexpr bool EXACT = std::is_same<OUT, float>::value;
   __shared__ f32x4 red[NW][RG][64];
   const int nblocks = (p.N + 16 * RG - 1) / (16 * RG);
   const int nb = blockIdx.x % nblocks;
@@ -326,13 +340,13 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (U > 1 && kb + u >= kend) break;
-      const i32x8 xf = join(S.x[u][0], S.x[u][1]);
+      const Frag<EXACT> xf = as_frag<EXACT>(join(S.x[u][0], S.x[u][1]));
       const float f = (xok ? S.xs[u] : 0.f) * S.ws[u];
 #pragma unroll
       for (int g = 0; g < RG; ++g) {
         const i32x8 wf = join(fp8_permute(S.l[u][g][0], S.l[u][g][1], src0, lo),
                               fp8_permute(S.l[u][g][0], S.l[u][g][1], src1, lo));
-        acc[g] += mfma_fp8(wf, xf) * f;
+        acc[g] += mfma_fp8(as_frag<EXACT>(wf), xf) * f;
       }
     }
   };
@@ -411,7 +425,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
 //
 // Split over k (dense, few tiles): work-group (x, y) computes tile x over the
 // y-th part of the blocks and writes fp32 partial sums to part y of `y`.
-template <bool GROUPED, int BM, int BN, int WM, int WD, class OUT>
+template <bool GROUPED, int BM, int BN, int WM, int WD, bool EXACT, class OUT>
 __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, const int* ntiles) {
   constexpr int BH = BN / 2, WN = 8 / WM, NW = 8;
   constexpr int TM = BM / WM / 16, TH = BH / WN / 16;
@@ -641,6 +655,9 @@ __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, cons
     constexpr int EVERY = NC <= NP ? 2 : 1;
     static_assert(NC <= 2 * NP, "copies");
     f32x4 q[LAG];
+    Frag<EXACT> xq[TM], wq;
+#pragma unroll
+    for (int t = 0; t < TM; ++t) xq[t] = as_frag<EXACT>(xf[t]);
 #pragma unroll
     for (int i = 0; i < 2 * NP + LAG; ++i) {
       if (i >= LAG) {
@@ -652,7 +669,8 @@ __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, cons
       }
       if (i < 2 * NP) {
         const int h = i / NP, g = i % NP / TM, t = i % TM;
-        q[i % LAG] = mfma_fp8(wf[g], xf[t]);
+        if (t == 0) wq = as_frag<EXACT>(wf[g]);
+        q[i % LAG] = mfma_fp8(wq, xq[t]);
         if (t == TM - 1) wf[g] = read_w(h == 0 ? r0 + HBUF : r1, g);
         if (h == 1 && g == TH - 1) xf[t] = read_x(kb + 1, t);
         if (i % EVERY == 0 && i / EVERY < NC) copy(i / EVERY);
@@ -763,10 +781,10 @@ __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, cons
   }
 }
 
-template <bool GROUPED, int BM, int BN, int WM, int WD, class OUT>
+template <bool GROUPED, int BM, int BN, int WM, int WD, bool EXACT, class OUT>
 __global__ __launch_bounds__(512) void fp8_pipe_kernel(Fp8Gemm p, const Tile* tiles,
                                                        const int* ntiles) {
-  fp8_pipe_body<GROUPED, BM, BN, WM, WD, OUT>(p, tiles, ntiles);
+  fp8_pipe_body<GROUPED, BM, BN, WM, WD, EXACT, OUT>(p, tiles, ntiles);
 }
 
 // y = the sum of the parts, in order, four values a thread.
@@ -801,7 +819,7 @@ bool wide(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % 
 using Plan = Fp8Plan;
 
 // Grouped: rows per group on average decide.  Up to 4, weights are streamed
-// past 16-row tiles (decode, 1.4 rows: 609 us; at 8.3 rows 1009 us against
+// past 16-row tiles (decode, 1.4 rows: 589 us; at 8.3 rows 1009 us against
 // 915 for 64-row tiles).  Above that, the tile height with the least work:
 // a group of r rows takes about r / BM + 0.4 tiles (at least one), whose cost
 // for 64, 128 and 192 rows is 1.0, 1.25 and 1.675 us a block of k on the full
@@ -831,7 +849,11 @@ Plan grouped_plan(int rows, int groups, int KB) {
 // 128 tiles, two of which fit a CU: 0.45, or 0.34 for each 256 of them), plus
 // what a tile takes to start and end and, for a split, the second launch and
 // the partial sums' traffic.  187 x 2048 x 8192: 24 us unsplit, 14.6 split;
-// 32 x 10240 x 8192: 31 and 21.
+// 32 x 10240 x 8192: 31 and 21.  fp32 results (`exact`: twice the MFMA time and
+// the conversions) run on the same estimate without 256 x 256 tiles, whose
+// converted fragments do not fit the registers; the better of the other two
+// is at most 12% faster than what that picks, from 17 rows to 8192 (8192 x
+// 10240 x 8192: 1160 us, 1.19 PFLOP/s, against 540 in bf16).
 struct DenseTile {
   int bm, bn;
 };
@@ -840,11 +862,12 @@ double tile_us(const DenseTile& t, long n) {
   if (t.bm == 64) return n * (0.34 / 256) > 0.45 ? n * (0.34 / 256) : 0.45;
   return (double)((n + 255) / 256) * (t.bm == 256 ? 1.65 : 0.96);
 }
-Plan dense_plan(int M, int N, int KB) {
+Plan dense_plan(int M, int N, int KB, bool exact) {
   if (M <= 16) return {true, kStreamTileM, 1};
   Plan best{};
   double least = 0;
-  for (const DenseTile& t : kDenseTiles)
+  for (const DenseTile& t : kDenseTiles) {
+    if (exact && t.bm == 256) continue;
     for (int s = 1; s <= 8; s *= 2) {
       // a part is at least 8 blocks, and at most what the kernel takes
       const int kb = (KB + s - 1) / s;
@@ -854,11 +877,12 @@ Plan dense_plan(int M, int N, int KB) {
       if (s > 1) us += 4.0 + (double)s * M * N * 8 / 4e6;
       if (best.bm == 0 || us < least) best = {false, t.bm, s}, least = us;
     }
+  }
   return best;
 }
 
-Plan make_plan(int M, int N, int KB, int groups) {
-  return groups ? grouped_plan(M, groups, KB) : dense_plan(M, N, KB);
+Plan make_plan(int M, int N, int KB, int groups, bool exact) {
+  return groups ? grouped_plan(M, groups, KB) : dense_plan(M, N, KB, exact);
 }
 
 int grouped_tiles(int rows, int groups, int tile_m) {
@@ -887,7 +911,8 @@ hipError_t launch_grouped(const Fp8Gemm& p, const Plan& plan, const Tile* tiles,
     const long grid = xcd_grid((long)max_tiles * ((p.N + BN - 1) / BN));
     if (too_many(grid, 512)) return hipErrorInvalidConfiguration;
     auto go = [&](auto bm, auto wm) {
-      fp8_pipe_kernel<true, decltype(bm)::value, BN, decltype(wm)::value, 3, OUT>
+      fp8_pipe_kernel<true, decltype(bm)::value, BN, decltype(wm)::value, 3,
+                      std::is_same<OUT, float>::value, OUT>
           <<<grid, 512, 0, s>>>(p, tiles, ntiles);
     };
     if (plan.bm == 64) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
@@ -897,18 +922,19 @@ hipError_t launch_grouped(const Fp8Gemm& p, const Plan& plan, const Tile* tiles,
   return hipGetLastError();
 }
 
-template <class OUT>
+template <bool EXACT, class OUT>
 hipError_t launch_dense(const Fp8Gemm& p, const Plan& plan, hipStream_t s) {
   using std::integral_constant;
   if (plan.stream) {
     constexpr int RG = 1, NW = 8;
     const long grid = (p.N + 16 * RG - 1) / (16 * RG);
+    // (never split, so EXACT is what OUT says)
     fp8_stream_kernel<false, NW, RG, 2, OUT><<<grid, NW * 64, 0, s>>>(p, nullptr, nullptr);
   } else {
     auto go = [&](auto bm, auto bn, auto wm, auto wd) {
       constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
       const long tot = (long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-      fp8_pipe_kernel<false, BM, BN, decltype(wm)::value, decltype(wd)::value, OUT>
+      fp8_pipe_kernel<false, BM, BN, decltype(wm)::value, decltype(wd)::value, EXACT, OUT>
           <<<dim3(xcd_grid(tot), p.splits), 512, 0, s>>>(p, nullptr, nullptr);
     };
     using I2 = integral_constant<int, 2>;
@@ -916,9 +942,10 @@ hipError_t launch_dense(const Fp8Gemm& p, const Plan& plan, hipStream_t s) {
     using I4 = integral_constant<int, 4>;
     using I128 = integral_constant<int, 128>;
     using I256 = integral_constant<int, 256>;
-    if (plan.bm == 256) go(I256{}, I256{}, I4{}, I2{});
-    else if (plan.bm == 128) go(I128{}, I256{}, I2{}, I3{});
-    else go(integral_constant<int, 64>{}, I128{}, I2{}, I3{});
+    if constexpr (!EXACT)
+      if (plan.bm == 256) go(I256{}, I256{}, I4{}, I2{});
+    if (plan.bm == 128) go(I128{}, I256{}, I2{}, I3{});
+    else if (plan.bm == 64) go(integral_constant<int, 64>{}, I128{}, I2{}, I3{});
   }
   return hipGetLastError();
 }
@@ -951,14 +978,14 @@ hipError_t fp8_quantize_weight(const void* w, bool bf16, long matrices, int rows
   return hipGetLastError();
 }
 
-size_t fp8_matmul_workspace(int M, int N, int KB, int groups) {
-  const Plan plan = make_plan(M, N, KB, groups);
+size_t fp8_matmul_workspace(int M, int N, int KB, int groups, bool out_bf16) {
+  const Plan plan = make_plan(M, N, KB, groups, !out_bf16);
   if (groups) return 256 + (size_t)grouped_tiles(M, groups, plan.bm) * sizeof(Tile);
   return plan.splits > 1 ? (size_t)plan.splits * M * N * sizeof(float) : 0;
 }
 
 hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws, hipStream_t s) {
-  const Plan plan = make_plan(p.M, p.N, p.KB, p.groups);
+  const Plan plan = make_plan(p.M, p.N, p.KB, p.groups, !out_bf16);
   p.splits = plan.splits;
   if (p.groups) {
     const int max_tiles = grouped_tiles(p.M, p.groups, plan.bm);
@@ -973,7 +1000,8 @@ hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws
   if (p.splits > 1) {
     void* y = p.y;
     p.y = ws;
-    const hipError_t e = launch_dense<float>(p, plan, s);
+    const hipError_t e =
+        out_bf16 ? launch_dense<false, float>(p, plan, s) : launch_dense<true, float>(p, plan, s);
     if (e != hipSuccess) return e;
     const long n4 = (long)p.M * p.N / 4;
     const long grid = (n4 + 255) / 256;
@@ -984,7 +1012,8 @@ hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws
       fp8_add_kernel<<<grid, 256, 0, s>>>(part, p.splits, n4, static_cast<float*>(y));
     return hipGetLastError();
   }
-  return out_bf16 ? launch_dense<uint16_t>(p, plan, s) : launch_dense<float>(p, plan, s);
+  return out_bf16 ? launch_dense<false, uint16_t>(p, plan, s)
+                  : launch_dense<true, float>(p, plan, s);
 }
 
 Fp8Plan fp8_expert_plan(int rows, int experts, int KB, int path) {

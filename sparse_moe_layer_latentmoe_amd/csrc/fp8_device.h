@@ -22,6 +22,33 @@ __device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
                                                           0, 0, 0);
 }
 
+// The same product with each operand converted to bf16 (exactly): the sum is
+// then an fp32 sum.  The 8-bit instruction keeps about 17 bits of it (measured
+// on normally distributed blocks of 128: off by up to 2^-15.9 of the sum of
+// the products' magnitudes, against 2^-25.4 here) at twice the rate.
+struct Bf16Frag {
+  bf16x8 v[4];
+};
+__device__ __forceinline__ Bf16Frag fp8_to_bf16(i32x8 a) {
+  Bf16Frag r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)a[i], 1.f, false);
+    const auto hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)a[i], 1.f, true);
+    r.v[i >> 1][4 * (i & 1)] = lo[0];
+    r.v[i >> 1][4 * (i & 1) + 1] = lo[1];
+    r.v[i >> 1][4 * (i & 1) + 2] = hi[0];
+    r.v[i >> 1][4 * (i & 1) + 3] = hi[1];
+  }
+  return r;
+}
+__device__ __forceinline__ f32x4 mfma_fp8(const Bf16Frag& a, const Bf16Frag& b) {
+  f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = mfma_bf16(a.v[i], b.v[i], c);
+  return c;
+}
+
 // Four values within [-448, 448] (up to rounding) as e4m3 codes, lowest byte
 // first, rounded to nearest, ties to even.
 __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {

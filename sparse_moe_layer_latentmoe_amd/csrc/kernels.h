@@ -166,7 +166,7 @@ struct Fp8Gemm {
   float* ys = nullptr;  // [M, NB]: the scales of a quantised output
 };
 // bytes of `ws`: the groups' row tiles, or the partial sums of a split of k
-size_t fp8_matmul_workspace(int M, int N, int KB, int groups);
+size_t fp8_matmul_workspace(int M, int N, int KB, int groups, bool out_bf16);
 hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws,
                       hipStream_t s);
 

@@ -328,7 +328,8 @@ lmoe_status lmoe_quantize_fp8_weight(const void* w, int32_t w_type, int64_t matr
 
 size_t lmoe_fp8_matmul_workspace_size(const lmoe_fp8_matmul_args* a) {
   if (check_fp8(a) != LMOE_OK || a->M == 0) return 0;
-  return fp8_matmul_workspace(a->M, a->N, a->K / 128, a->n_groups);
+  return fp8_matmul_workspace(a->M, a->N, a->K / 128, a->n_groups,
+                              a->y_type == LMOE_BF16);
 }
 
 lmoe_status lmoe_fp8_matmul(const lmoe_fp8_matmul_args* a, void* workspace, size_t workspace_bytes,
@@ -336,7 +337,8 @@ lmoe_status lmoe_fp8_matmul(const lmoe_fp8_matmul_args* a, void* workspace, size
   const lmoe_status st = check_fp8(a);
   if (st != LMOE_OK) return st;
   if (a->M == 0) return LMOE_OK;
-  const size_t need = fp8_matmul_workspace(a->M, a->N, a->K / 128, a->n_groups);
+  const size_t need = fp8_matmul_workspace(a->M, a->N, a->K / 128, a->n_groups,
+                              a->y_type == LMOE_BF16);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return LMOE_ERR_WORKSPACE;
   const int64_t G = a->n_groups ? a->n_groups : 1, kb = a->K / 128, nb = (a->N + 127) / 128;

@@ -123,6 +123,26 @@ def test_many_rows(M, N, K, dtype):
     check(operands(M, N, K, seed=M + N + K), dtype=dtype)
 
 
+@pytest.mark.parametrize("groups", [0, 7])
+@pytest.mark.parametrize("M,K", [(9, 128), (40, 128), (300, 128), (300, 1024), (900, 512),
+                                 (2100, 256), (4500, 128)])
+def test_fp32_results_are_fp32_sums(M, K, groups):
+    """fp32 results come from fp32 sums, through every kind of tile: each of a
+    block's 128 additions, the two scalings and the addition to the running sum
+    rounds by at most 2^-24 of a partial sum, which is at most the sum of the
+    magnitudes."""
+    xc, xs, wc, ws = operands(M, 256, K, groups or None, seed=M)
+    off = None
+    if groups:
+        off = torch.tensor([M * i // groups for i in range(groups + 1)], dtype=torch.int32,
+                           device=DEV)
+    y = pkg.fp8_matmul(xc, xs, wc, ws, offsets=off, out_dtype=F)
+    want, mag, _ = R.fp8_matmul(bits(xc), xs.cpu().numpy(), bits(wc), ws.cpu().numpy(),
+                                None if off is None else off.tolist(), None)
+    err = np.abs(y.double().cpu().numpy() - want)
+    assert np.all(err <= (128 + 3 * (K // 128)) * 2.0 ** -24 * mag), float((err / mag).max())
+
+
 def test_long_k():
     check(operands(70, 32, 65536, seed=1))
     check(operands(5, 32, 65536, seed=2))
