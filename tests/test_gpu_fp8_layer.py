@@ -92,6 +92,40 @@ def test_layer_matches_oracle(shape, tokens, path):
     layer.close()
 
 
+@pytest.fixture(scope="module")
+def full():
+    wl = li.workload("decode")
+    weights = li.make_weights(wl, DEV)
+    return weights, fp8_weights(li.make_inputs(wl, DEV, weights=weights))
+
+
+@pytest.mark.fullshape
+@pytest.mark.parametrize("name,tokens,rows", [("decode", None, [31]),
+                                              ("mtp_verify", None, [100]),
+                                              ("prefill", 21504, [0, 21503])])
+def test_layer_at_full_shape(full, name, tokens, rows):
+    """Streamed experts, 64-row tiles and the long batch on 192-row tiles (more
+    than 2 GiB of hidden codes): properties on every token, and the whole
+    output of a token or two against the oracle, which quantises the experts
+    they use."""
+    wl = li.workload(name) if tokens is None else li.workload(name, tokens=tokens)
+    print(f"[fp8 full {name} T={wl.tokens}]", flush=True)
+    weights, w = full
+    inp = li.make_inputs(wl, DEV, weights=weights)
+    layer = pkg.LatentMoE(wl.shape, w, wl.tokens, expert_format=pkg.EXPERTS_FP8)
+    g = run_gpu(layer, inp.x)
+    check_properties(g, wl.shape, wl.tokens)
+    hw = li.HostWeights(inp)
+    up, down = Coded(hw.expert_up), Coded(hw.expert_down)
+    r, y = oracle(li.bf16_bits(inp.x[rows]), hw, oracle_config(wl.shape), up, down, g.idx[rows])
+    assert normwise_rel(g.r[rows], r) <= OUT_REL
+    assert normwise_rel(g.y[rows].float().cpu().numpy(), y) <= OUT_REL
+    e = int(g.idx[rows[0], 0])
+    assert np.array_equal(w["expert_up_fp8"][e].view(torch.uint8).cpu().numpy(), up[e][0])
+    assert np.array_equal(w["expert_down_fp8_scale"][e].cpu().numpy(), down[e][1])
+    layer.close()
+
+
 def test_layer_refuses_widths_that_are_not_whole_blocks():
     sh = li.LayerShape(256, 192, 16, 4, 256, 512, 5.0)
     inp = li.make_inputs(li.Workload("fp8", sh, 4), DEV)
