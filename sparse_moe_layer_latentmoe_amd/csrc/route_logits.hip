@@ -23,8 +23,8 @@
 // several slots it runs on one key a lane: first on the lanes' largest keys,
 // whose K-th largest bounds the K-th largest of all from below; then the few
 // keys that reach that bound move to one a lane (through LDS, ids ascending)
-// and are searched again.  Where more than 64 reach it (equal keys), or the
-// border turns out closer than the scores' error, all slots are searched.
+// and are searched again.  Where more than 64 reach it (equal keys), all slots
+// are searched.
 #include <cfloat>
 #include <type_traits>
 
@@ -147,11 +147,22 @@ __device__ __forceinline__ F group_best(const F* row, int lane, int n_group, int
   return __shfl(r, lane < n_group ? lane << sh : 0, 64);
 }
 
+// How many of the first n lanes' keys come before this lane's: larger ones,
+// and equal ones of lower lanes.  Each key in turn is broadcast to all lanes,
+// three instructions a key.
+__device__ __forceinline__ int rank_of(uint32_t key, int n, int lane) {
+  int r = 0;
+  for (int i = 0; i < n; ++i) {
+    const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)key, i);
+    r += k > key || (k == key && i < lane);
+  }
+  return r;
+}
+
 // The lanes of the n largest keys (one per lane; equal keys: lower lanes).
-template <class U>
-__device__ __forceinline__ uint64_t best_lanes(U key, int n, uint64_t below) {
-  const U k[1] = {key};
-  const U v = border<U, 1>(k, n);
+__device__ __forceinline__ uint64_t best_lanes(uint64_t key, int n, uint64_t below) {
+  const uint64_t k[1] = {key};
+  const uint64_t v = border<uint64_t, 1>(k, n);
   const uint64_t gt = __ballot(key > v), eq = __ballot(key == v);
   const int room = n - __popcll(gt);
   return gt | __ballot(key == v && __popcll(eq & below) < room);
@@ -220,7 +231,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
     key[j] = e < E ? (on ? key32(bias ? b[j] : l[j]) : kKeyMinusInf) : 0u;
   }
 
-  // biased score of slot j in 64 bits (only where the border is close)
+  // biased scores in 64 bits (only where the border is close)
   double m64 = 0.0, inv64 = 1.0;
   bool have64 = false;
   auto prepare64 = [&]() {
@@ -235,12 +246,12 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
     sum = wave_sum(sum);
     inv64 = sum > 0.0 ? 1.0 / sum : 0.0;
   };
-  auto biased64 = [&](int j) -> double {
-    if (!(l[j] > -INFINITY)) return -INFINITY;
-    const double v = p.softmax ? exp((double)l[j] - m64) * inv64
-                               : 1.0 / (1.0 + exp(-(double)l[j]));
-    return bias ? v + (double)bias[j * 64 + lane] : v;
+  auto value64 = [&](float x, int e) -> double {
+    if (!(x > -INFINITY)) return -INFINITY;
+    const double v = p.softmax ? exp((double)x - m64) * inv64 : 1.0 / (1.0 + exp(-(double)x));
+    return bias ? v + (double)bias[e] : v;
   };
+  auto biased64 = [&](int j) { return value64(l[j], j * 64 + lane); };
 
   if (p.n_group > 1) {
     const int G = E / p.n_group;
@@ -252,9 +263,10 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
     const bool has = lane < p.n_group;
     const float gs0 = group_best(row, lane, p.n_group, G, p.best);
     const float gs = has ? gs0 : -INFINITY;
-    const uint32_t gk[1] = {has ? key32(gs) : 0u};
-    const uint32_t gv = border<uint32_t, 1>(gk, p.topk_group);
-    const float gt = key32_value(gv);
+    const uint32_t gk = has ? key32(gs) : 0u;
+    const int rank = has ? rank_of(gk, p.n_group, lane) : 64;
+    const uint64_t at = __ballot(rank == p.topk_group - 1);  // the last kept group
+    const float gt = key32_value((uint32_t)__builtin_amdgcn_readlane((int)gk, __builtin_ctzll(at)));
     // a group's score is off by at most two scores' bounds and two roundings
     const float gerr = 4.f * serr + 0x1p-21f * fabsf(gt);
     const int over = __popcll(__ballot(has && gs >= gt + 2.f * gerr));
@@ -269,9 +281,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
         if (j * 64 + lane < E) row64[j * 64 + lane] = biased64(j);
       wave_lds_fence();
       const double g64 = group_best(row64, lane, p.n_group, G, p.best);
-      kept = best_lanes<uint64_t>(has ? key64(g64) : 0ull, p.topk_group, below);
+      kept = best_lanes(has ? key64(g64) : 0ull, p.topk_group, below);
     } else {
-      kept = best_lanes<uint32_t>(gk[0], p.topk_group, below);
+      kept = __ballot(rank < p.topk_group);
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -288,7 +300,14 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
     uint32_t top[1] = {key[0]};
 #pragma unroll
     for (int j = 1; j < NJ; ++j) top[0] = key[j] > top[0] ? key[j] : top[0];
-    const uint32_t low = border<uint32_t, 1>(top, K);
+    const uint32_t low0 = border<uint32_t, 1>(top, K);
+    // with a bias also those that the scores' error may put above it
+    const auto reach = [&](float b) { return 2.f * serr + 0x1p-22f * fabsf(b); };
+    uint32_t low = low0;
+    if (bias && low0 > kKeyMinusInf) {
+      const float b0 = key32_value(low0);
+      low = key32(b0 - 5.f * reach(b0));
+    }
     uint64_t in[NJ];
     int n = 0;
 #pragma unroll
@@ -314,32 +333,42 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
       const uint32_t k1[1] = {lane < n ? ck[lane] : 0u};
       const int id = ck[64 + lane];
       const float sc = __uint_as_float(ck[128 + lane]);
-      // at least `low`, so that no key left out lies above it
+      // at least low0, so that no key left out lies above it (or, with a bias,
+      // within 4 times the scores' error below it)
       uint32_t v = border<uint32_t, 1>(k1, K);
-      v = v > low ? v : low;
-      bool far = true;  // no key within the scores' error of the border
+      v = v > low0 ? v : low0;
+      const uint64_t gt = __ballot(k1[0] > v), eq = __ballot(k1[0] == v);
+      bool on = k1[0] > v || (k1[0] == v && __popcll(eq & below) < K - __popcll(gt));
       if (bias) {
-        const float bt = key32_value(v), kv = key32_value(k1[0]);
-        const float err = 2.f * serr + 0x1p-22f * fabsf(bt);
+        const float bt = key32_value(v), kv = key32_value(k1[0]), err = reach(bt);
         const int over = __popcll(__ballot(lane < n && kv >= bt + 2.f * err));
         const int upto = __popcll(__ballot(lane < n && kv > bt - 2.f * err));
-        // keys below `low` are not among these: it has to be out of reach too
-        far = (over == K || upto == K) && (over == K || bt - 2.f * err >= key32_value(low));
-      }
-      if (far) {
-        const uint64_t gt = __ballot(k1[0] > v), eq = __ballot(k1[0] == v);
-        const int room = K - __popcll(gt);
-        const bool on = k1[0] > v || (k1[0] == v && __popcll(eq & below) < room);
-        const uint64_t mk = __ballot(on);
-        const float sum = wave_sum(on ? sc : 0.f);
-        if (on) {
-          const size_t at = (size_t)t * K + __popcll(mk & below);
-          idx_out[at] = id;
-          w_out[at] = p.renorm ? sc * (p.rho / (sum + 1e-20f)) : sc * p.rho;
+        if (over < K && upto > K) {
+          // those next to the border are ordered by their 64-bit values, those
+          // above are in
+          prepare64();
+          const bool sure = lane < n && kv >= bt + 4.f * err;
+          const bool near = lane < n && !sure && kv > bt - 4.f * err;
+          const uint64_t k64 = near ? key64(value64(clean_logit(route_load(lp + id)), id)) : 0ull;
+          int rank = __popcll(__ballot(sure));
+          for (uint64_t left = __ballot(near); left; left &= left - 1) {
+            const int o = __builtin_ctzll(left);
+            const uint64_t ko =
+                (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k64 >> 32), o) << 32 |
+                (uint32_t)__builtin_amdgcn_readlane((int)k64, o);
+            rank += ko > k64 || (ko == k64 && o < lane);
+          }
+          on = sure || (near && rank < K);
         }
-        return;
       }
-      wave_lds_fence();
+      const uint64_t mk = __ballot(on);
+      const float sum = wave_sum(on ? sc : 0.f);
+      if (on) {
+        const size_t at = (size_t)t * K + __popcll(mk & below);
+        idx_out[at] = id;
+        w_out[at] = p.renorm ? sc * (p.rho / (sum + 1e-20f)) : sc * p.rho;
+      }
+      return;
     }
   }
 
