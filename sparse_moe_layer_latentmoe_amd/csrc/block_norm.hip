@@ -14,7 +14,10 @@
 //
 // Both are bound by HBM: a work-group (or one wave, for narrow rows) keeps a
 // row in registers, so each value is read once and written once; sums are
-// fp32, the results round once.  The backward computes h' again from h and y
+// fp32, the results round once.  4099 rows of 8192, fp32 stream, bf16 block,
+// bf16 gate [T, D]: forward 99 us (470 MB, 4.7 TB/s), backward 151 us (739 MB,
+// 4.9 TB/s) and 5.8 us for the column sums; a large copy reaches 4.8 TB/s.  32
+// rows forward: 5.1 us, a launch and two reductions.  The backward computes h' again from h and y
 // rather than reading it: dalpha needs h anyway.  Column sums: each of a
 // fixed number of work-groups keeps the sums of its rows in registers and
 // writes them once; a second kernel adds those in order (no atomics, the same
@@ -395,7 +398,8 @@ __global__ __launch_bounds__(TPR* rows_per_group<TPR>()) void block_norm_backwar
 // The training step's usual case (y, dh_out, dx, dh and dy all there, wide
 // loads, rows up to 8192): the next row's loads are issued before the current
 // row is worked on (a row of 8192 is 115 KB a CU, enough to cover HBM's
-// latency), and the [D] parameters lie in LDS (1 where absent).  Registers
+// latency; the general kernel above, which does not, took 220 us for the case
+// at the top against 151), and the [D] parameters lie in LDS (1 where absent).  Registers
 // are what limits it: the sums take 64 of a thread's 256 and each of the two
 // rows up to 72, so a row stays as it was loaded and is converted again in
 // each of its passes.  GATE: 0 a gate of [D], [T] or none, 1 [T, D] in bf16, 2

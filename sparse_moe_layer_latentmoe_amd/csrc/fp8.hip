@@ -105,6 +105,8 @@ __device__ __forceinline__ float max8(const float (&v)[8]) {
 }  // namespace
 
 // Activations: 16 lanes to a block of 128 values, each block on its own.
+// Bound by HBM: 8191 x 8192 bf16 34 us (6.0 TB/s; two bytes read to one
+// written), 192 x 10240 3.3 us.
 template <class T, bool VEC>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(const T* __restrict__ x, long rows,
                                                            int cols, long stride, int nb,
@@ -269,6 +271,8 @@ __device__ __forceinline__ i32x4 fp8_permute(const i32x4& a, const i32x4& b, int
 // fixed order.  A wave instruction loads 8 rows x 128 bytes; ds_bpermute
 // moves the pieces to the MFMA's lanes (the layout that the bf16 streaming
 // GEMM measured fastest).  Work-group: 16 RG weight rows x 16 token rows.
+// Bound by HBM: 1 x 10240 x 8192 15 us (5.6 TB/s), 32 tokens' 704 rows over 512
+// experts 589 us at 5120 x 2048 (6.9 TB/s).
 template <bool GROUPED, int NW, int RG, int U, class OUT>
 __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Tile* tiles,
                                                              const int* ntiles) {
@@ -422,6 +426,12 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
 // eight blocks of k at a time (32 bytes of a row of scales), an eighth of the
 // rows with each token block: one block at a time, every 4-byte load was a
 // cache line of its own, half as many line requests as the data itself.
+//
+// 8192 x 10240 x 8192: 543 us, 2.53 PFLOP/s (a library's product of the same
+// codes without scales: 505); 180224 rows over 512 experts, 2048 x 5120: 2.15
+// ms, 1.76 PFLOP/s.  A step of a 256 x 256 tile takes 1.59 us and a tile 6.4 us
+// beside its steps (192 x 256 grouped: 1.28 to 1.44 and 5.8): first copies and
+// the store of the result, which the next tile's work-group waits for.
 //
 // Split over k (dense, few tiles): work-group (x, y) computes tile x over the
 // y-th part of the blocks and writes fp32 partial sums to part y of `y`.
