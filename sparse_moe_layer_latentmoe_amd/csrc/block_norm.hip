@@ -17,11 +17,12 @@
 // fp32, the results round once.  4099 rows of 8192, fp32 stream, bf16 block,
 // bf16 gate [T, D]: forward 99 us (470 MB, 4.7 TB/s), backward 151 us (739 MB,
 // 4.9 TB/s) and 5.8 us for the column sums; a large copy reaches 4.8 TB/s.  32
-// rows forward: 5.1 us, a launch and two reductions.  The backward computes h' again from h and y
-// rather than reading it: dalpha needs h anyway.  Column sums: each of a
-// fixed number of work-groups keeps the sums of its rows in registers and
-// writes them once; a second kernel adds those in order (no atomics, the same
-// bits every time).
+// rows forward: 5.1 us, a launch and two reductions.
+//
+// The backward computes h' again from h and y rather than reading it: dalpha
+// needs h anyway.  Column sums: each of a fixed number of work-groups keeps
+// the sums of its rows in registers and writes them once; a second kernel
+// adds those in order (no atomics, the same bits every time).
 #include <type_traits>
 
 #include "gemm_device.h"

@@ -105,7 +105,7 @@ __device__ __forceinline__ float max8(const float (&v)[8]) {
 }  // namespace
 
 // Activations: 16 lanes to a block of 128 values, each block on its own.
-// Bound by HBM: 8191 x 8192 bf16 34 us (6.0 TB/s; two bytes read to one
+// Bound by HBM: 8192 x 8192 bf16 34 us (6.0 TB/s; two bytes read to one
 // written), 192 x 10240 3.3 us.
 template <class T, bool VEC>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(const T* __restrict__ x, long rows,
