@@ -174,7 +174,7 @@ __global__ __launch_bounds__(1024) void fp8_tiles_kernel(const int32_t* __restri
   int beg = 0, n = 0;
   if (g < G) {
     beg = min(max(offsets[g], 0), rows);
-    n = max(min(offsets[g + 1], rows) - beg, 0);
+    n = max(min(max(offsets[g + 1], 0), rows) - beg, 0);
   }
   const int nt = (n + tile_m - 1) / tile_m;
   int inc = nt;

@@ -161,6 +161,21 @@ def test_no_rows_and_untouched_rows():
     assert torch.equal(full[:5], src[:5]) and bool((full[5:] == 7).all() & (xo[5:] == 7).all())
 
 
+def test_rows_further_apart_than_32_bits():
+    D = 64
+    h, y, dh, dx = (rand(2, D, seed=5 + i, dtype=B) for i in range(4))
+    far = [torch.empty(2, 2 ** 31, dtype=B, device=DEV)[:, :D] for _ in range(2)]
+    for f, v in zip(far, (h, y)):
+        f.copy_(v)
+    par = dict(pre_weight=rand(D, seed=1), post_weight=rand(D, seed=2), gate=rand(2, D, seed=3))
+    out = []
+    for a, b in ((h, y), far):
+        h2, x, st = pkg.block_norm(a, b, want_stats=True, **par)
+        g = pkg.block_norm_backward(a, b, st, dh_out=dh, dx=dx, **par)
+        out.append([h2, x, st, g.dh, g.dy, g.dpre_weight, g.dpost_weight, g.dgate])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
 def test_streams_and_graph_replays():
     T, D = 300, 1024
     par = dict(pre_weight=rand(D, seed=1), post_weight=rand(D, seed=2), gate=rand(D, seed=3),

@@ -170,6 +170,37 @@ def test_backward_ignores_bad_ids_and_adds_equal_ones():
         assert np.all(np.abs(got - want) <= 2.0 ** -15 * mag + 1e-37)
 
 
+def test_rows_further_apart_than_32_bits():
+    r = pkg.make_router(70, 4)
+    l, dw = logits(2, 70, 26), logits(2, 4, 27)
+    far = torch.empty(2, 2 ** 31, device=DEV)[:, :70]
+    far.copy_(l)
+    idx, w = pkg.route_logits(r, l)
+    i2, w2 = pkg.route_logits(r, far)
+    assert torch.equal(idx, i2) and torch.equal(w, w2)
+    assert torch.equal(pkg.route_logits_backward(r, l, idx, dw),
+                       pkg.route_logits_backward(r, far, idx, dw))
+
+
+@pytest.mark.parametrize("gap", [0.0, 2.0 ** -24, 2.0 ** -22, 2.0 ** -20])
+@pytest.mark.parametrize("softmax", [False, True])
+def test_many_keys_next_to_the_border(gap, softmax):
+    """More than 64 biased scores within the scores' error of each other, a few
+    of them (which fit one a lane), and a border between equal ones."""
+    l = logits(6, 512, 28)
+    for t, n in enumerate((2, 20, 40, 64, 100, 512)):
+        pick = torch.randperm(512, generator=torch.Generator().manual_seed(t))[:n].to(DEV)
+        l[t, pick] = 2.0 + gap * torch.randint(0, 3, (n,), generator=torch.Generator()
+                                               .manual_seed(t + 9)).to(DEV)
+    b = bias_of(512, 29)
+    b[::2] = 0.25                                      # equal biases of half the experts
+    for K, kw in ((8, {}), (22, {}), (22, dict(n_group=8, topk_group=4)), (64, {})):
+        r = pkg.make_router(512, K, pkg.SCORE_SOFTMAX if softmax else pkg.SCORE_SIGMOID, **kw)
+        idx, _ = pkg.route_logits(r, l, b)
+        want, _ = R.route(exact(l), exact(b), K, softmax=softmax, **kw)
+        assert np.array_equal(idx.cpu().numpy(), want)
+
+
 def test_replayed_from_a_graph():
     r = pkg.make_router(512, 22, n_group=8, topk_group=4, scale=5.0)
     l, b, dw = logits(32, 512, 23), bias_of(512, 24), logits(32, 22, 25)
