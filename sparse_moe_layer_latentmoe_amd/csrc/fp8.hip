@@ -856,20 +856,20 @@ Plan grouped_plan(int rows, int groups, int KB) {
 // against 21 for tiles).  Above that the tile shape and the split of k with
 // the least estimated time: rounds of tiles over the 256 CUs, each so many
 // blocks of k long (256 x 256 tiles: 1.65 us a block, 128 x 256: 0.96; 64 x
-// 128 tiles, two of which fit a CU: 0.45, or 0.34 for each 256 of them), plus
+// 128 tiles, two of which fit a CU: 0.36, or 0.34 for each 256 of them), plus
 // what a tile takes to start and end and, for a split, the second launch and
-// the partial sums' traffic.  187 x 2048 x 8192: 24 us unsplit, 14.6 split;
-// 32 x 10240 x 8192: 31 and 21.  fp32 results (`exact`: twice the MFMA time and
+// the partial sums' traffic.  187 x 2048 x 8192: 24 us unsplit, 14.6 in 4 parts,
+// 16.7 in 8; 32 x 10240 x 8192: 31 unsplit, 19.5 in 4.  fp32 results (`exact`: twice the MFMA time and
 // the conversions) run on the same estimate without 256 x 256 tiles, whose
 // converted fragments do not fit the registers; the better of the other two
 // is at most 12% faster than what that picks, from 17 rows to 8192 (8192 x
-// 10240 x 8192: 1160 us, 1.19 PFLOP/s, against 540 in bf16).
+// 10240 x 8192: 1160 us, 1.19 PFLOP/s, against 543 in bf16).
 struct DenseTile {
   int bm, bn;
 };
 constexpr DenseTile kDenseTiles[3] = {{256, 256}, {128, 256}, {64, 128}};
 double tile_us(const DenseTile& t, long n) {
-  if (t.bm == 64) return n * (0.34 / 256) > 0.45 ? n * (0.34 / 256) : 0.45;
+  if (t.bm == 64) return n * (0.34 / 256) > 0.36 ? n * (0.34 / 256) : 0.36;
   return (double)((n + 255) / 256) * (t.bm == 256 ? 1.65 : 0.96);
 }
 Plan dense_plan(int M, int N, int KB, bool exact) {
