@@ -98,8 +98,10 @@ DECODE_SOURCES = ("gemm_stream.hip", "router.hip", "dispatch.hip", "gemm_problem
                   "lmoe_device.h")
 TRAFFIC_PROFILES = {
     "decode": ("traffic_decode_T32.json", DECODE_SOURCES),
-    "mtp_verify": ("traffic_mtp_verify_T192.json", DECODE_SOURCES + ("gemm_tiled.hip",)),
-    "prefill": ("traffic_prefill_T8192.json", DECODE_SOURCES + ("gemm_tiled.hip",)),
+    "mtp_verify": ("traffic_mtp_verify_T192.json",
+                   DECODE_SOURCES + ("gemm_tiled.hip", "gemm_device.h")),
+    "prefill": ("traffic_prefill_T8192.json",
+                DECODE_SOURCES + ("gemm_tiled.hip", "gemm_device.h")),
 }
 
 

@@ -27,6 +27,7 @@
 
 #include "gemm_device.h"
 #include "kernels.h"
+#include "wave_device.h"
 
 namespace lmoe {
 

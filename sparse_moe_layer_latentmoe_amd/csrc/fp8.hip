@@ -23,6 +23,7 @@
 #include "fp8_device.h"
 #include "gemm_device.h"
 #include "kernels.h"
+#include "wave_device.h"
 
 namespace lmoe {
 

@@ -6,9 +6,7 @@
 namespace lmoe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
@@ -41,37 +39,6 @@ __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
-
-// v combined (by op) over each 16 consecutive lanes, in all of them: four DPP
-// moves (lane ^ 1, lane ^ 2, mirrored halves, mirrored row), no LDS crossbar.
-template <class Op>
-__device__ __forceinline__ float row16_reduce(float v, Op op) {
-#define LMOE_DPP(CTRL) \
-  __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true))
-  v = op(v, LMOE_DPP(0xB1));
-  v = op(v, LMOE_DPP(0x4E));
-  v = op(v, LMOE_DPP(0x141));
-  v = op(v, LMOE_DPP(0x140));
-#undef LMOE_DPP
-  return v;
-}
-
-// v combined over the wave, in every lane (all lanes active).
-template <class Op>
-__device__ __forceinline__ float wave_reduce(float v, Op op) {
-  v = row16_reduce(v, op);
-  float r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16 * i));
-  return op(op(r[0], r[1]), op(r[2], r[3]));
-}
-struct AddOp {
-  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-struct MaxOp {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
 
 __device__ __forceinline__ bf16x8 load8(const uint16_t* p) {
   return *reinterpret_cast<const bf16x8*>(p);

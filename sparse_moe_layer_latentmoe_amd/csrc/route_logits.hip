@@ -34,7 +34,7 @@
 #include <type_traits>
 
 #include "kernels.h"
-#include "lmoe_device.h"
+#include "wave_device.h"
 
 namespace lmoe {
 
