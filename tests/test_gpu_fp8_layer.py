@@ -48,8 +48,10 @@ class Coded:
         return self.made[e]
 
 
-def oracle(x_bits, hw, cfg, up, down, idx):
-    x = O.bf16_bits_to_f64(x_bits)
+def oracle(x, hw, cfg, up, down, idx):
+    """(r, y) of the layer on x: bf16 bits, or float64 rows."""
+    if x.dtype != np.float64:
+        x = O.bf16_bits_to_f64(x)
     z32 = O.latent_projection(x, O.bf16_bits_to_f64(hw.fc1_latent)).astype(np.float32)
     _, s = O.router_scores(z32, hw.router)
     want, _, gap = O.select_experts(s, hw.router_bias, cfg.num_experts_per_tok, cfg.n_group,
@@ -137,6 +139,37 @@ def test_layer_refuses_widths_that_are_not_whole_blocks():
         pkg.LatentMoE(SMALL, w, 4, expert_format=pkg.EXPERTS_FP8)
 
 
+def test_layer_with_fewer_tokens_than_it_was_made_for():
+    inp = li.make_inputs(li.Workload("fp8", MEDIUM, 900), DEV)
+    w = fp8_weights(inp)
+    large = pkg.LatentMoE(MEDIUM, w, 900, expert_format=pkg.EXPERTS_FP8)
+    for T in (900, 1, 150, 400, 37):
+        one = pkg.LatentMoE(MEDIUM, w, T, expert_format=pkg.EXPERTS_FP8)
+        assert torch.equal(large.forward(inp.x[:T]), one.forward(inp.x[:T]))
+        one.close()
+    large.close()
+
+
+@pytest.mark.parametrize("tokens", [5, 300])
+def test_layer_inside_its_block(tokens):
+    """The fused pre-norm and residual around FP8 experts: their epilogues hand
+    the quantiser the normalised latent."""
+    wl = li.Workload("fp8", SMALL, tokens)
+    inp = li.make_inputs(wl, DEV)
+    gamma = li.make_norm_weight(wl, DEV)
+    w = dict(fp8_weights(inp), norm_weight=gamma)
+    layer = pkg.LatentMoE(SMALL, w, tokens, expert_format=pkg.EXPERTS_FP8, fuse=pkg.FUSE_BLOCK)
+    g = run_gpu(layer, inp.x)
+    hw = li.HostWeights(inp, eager_experts=True)
+    h = li.bf16_bits(inp.x)
+    xt, rn = O.rms_prenorm(h, li.bf16_bits(gamma))
+    r, y = oracle(rn[:, None] * O.bf16_bits_to_f64(xt), hw, oracle_config(SMALL),
+                  Coded(hw.expert_up), Coded(hw.expert_down), g.idx)
+    assert normwise_rel(g.r, r) <= OUT_REL
+    assert normwise_rel(g.y.float().cpu().numpy(), O.bf16_bits_to_f64(h) + y) <= OUT_REL
+    layer.close()
+
+
 def test_layer_replays_from_a_graph():
     T = 48
     inp = li.make_inputs(li.Workload("fp8", MEDIUM, T), DEV)
@@ -207,7 +240,8 @@ def test_operators_as_one_block():
     # sum is 2/pi sqrt(256) = 10.2 times u's root mean square.  So h = u^2 and the
     # scale of its block may each be off by 2 * 10.2 * 2^-15.9 = 2^-11.5 of h, and
     # with codes at least 2^-4 apart a fraction of 2 * 2^-11.5 / 2^-4 = 2^-6.5 of
-    # them may be neighbours, at most 2^-3 away: normwise sqrt(2^-6.5) 2^-3 =
-    # 1.3e-2, and 2^-8 for the bf16 rows.
+    # them may be neighbours, at most 2^-3 away: sqrt(2^-6.5) 2^-3 = 1.3e-2 of
+    # the values (root mean squares; the largest error and the largest value of
+    # as many sums stand in the same ratio), and 2^-8 for the bf16 rows.
     assert normwise_rel(rr.cpu().numpy(), e64(taps.r_latent)) <= 1.3e-2 + 2.0 ** -8
     layer.close()
