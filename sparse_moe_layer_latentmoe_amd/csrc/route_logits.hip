@@ -28,8 +28,8 @@
 //
 // Bound by the searches' instructions and, for few tokens, by one wave's chain
 // of them, not by memory.  512 experts, fp32 logits, sigmoid, bias, top-22:
-// 8192 tokens 10.6 us (18 MB, 1.7 TB/s), with 8 groups 16 us; 32 tokens 6.2
-// us.  Searching all slots instead took 20, 37 and 9.1 us.
+// 8192 tokens 10.6 us (18 MB, 1.7 TB/s), with 8 groups 16 to 19 us (a token
+// whose groups need 64 bits ends last); 32 tokens 6.2 us.  Searching all slots instead took 20, 37 and 9.1 us.
 #include <cfloat>
 #include <type_traits>
 
@@ -278,15 +278,21 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
     const int upto = __popcll(__ballot(has && gs > gt - 2.f * gerr));
     uint64_t kept;
     if (over < p.topk_group && upto > p.topk_group) {
+      // the groups next to the border are ordered by their 64-bit scores, those
+      // above are in (slots that hold no expert of such a group skip the work)
       prepare64();
+      const bool near = has && gs < gt + 4.f * gerr && gs > gt - 4.f * gerr;
+      const uint64_t close = __ballot(near), sure = __ballot(has && gs >= gt + 4.f * gerr);
       double* row64 = reinterpret_cast<double*>(rows[wv]);
       wave_lds_fence();  // the fp32 row has been read
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (j * 64 + lane < E) row64[j * 64 + lane] = biased64(j);
+      for (int j = 0; j < NJ; ++j) {
+        const int e = j * 64 + lane;
+        if (e < E) row64[e] = (close >> (e / G)) & 1ull ? biased64(j) : (double)b[j];
+      }
       wave_lds_fence();
       const double g64 = group_best(row64, lane, p.n_group, G, p.best);
-      kept = best_lanes(has ? key64(g64) : 0ull, p.topk_group, below);
+      kept = sure | best_lanes(near ? key64(g64) : 0ull, p.topk_group - __popcll(sure), below);
     } else {
       kept = __ballot(rank < p.topk_group);
     }
