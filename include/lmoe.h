@@ -328,7 +328,8 @@ typedef struct {
 } lmoe_block_norm_args;
 
 /* h_out [T, D] (h_type), x [T, D] (y_type) or NULL, stats fp32 [T, 2] (the
- * two reciprocal roots, what the backward needs) or NULL; all dense. */
+ * two reciprocal roots, what the backward needs; 1 in place of the first
+ * without post_weight and of the second without x) or NULL; all dense. */
 lmoe_status lmoe_block_norm(const lmoe_block_norm_args *a, void *h_out, void *x, float *stats,
                             void *stream);
 
@@ -347,7 +348,8 @@ size_t lmoe_block_norm_workspace_size(const lmoe_block_norm_args *a,
                                       const lmoe_block_norm_grads *g);
 
 /* From the forward's arguments and stats, dh_out [T, D] (h_type) and dx
- * [T, D] (y_type), either may be NULL (0), the gradients in g.  workspace:
+ * [T, D] (y_type; NULL if the forward made no x), either may be NULL (0), the
+ * gradients in g.  workspace:
  * 16-byte aligned device memory of the size above; calls that may overlap
  * need one each.  T = 0 writes zeros to the [D] gradients. */
 lmoe_status lmoe_block_norm_backward(const lmoe_block_norm_args *a, const float *stats,

@@ -29,7 +29,8 @@
 // Bound by the searches' instructions and, for few tokens, by one wave's chain
 // of them, not by memory.  512 experts, fp32 logits, sigmoid, bias, top-22:
 // 8192 tokens 10.6 us (18 MB, 1.7 TB/s), with 8 groups 16 to 19 us (a token
-// whose groups need 64 bits ends last); 32 tokens 6.2 us.  Searching all slots instead took 20, 37 and 9.1 us.
+// whose groups need 64 bits ends last); 32 tokens 6.2 us.  Searching all slots
+// instead took 20, 37 and 9.1 us.
 #include <cfloat>
 #include <type_traits>
 
