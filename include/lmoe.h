@@ -94,9 +94,10 @@ typedef enum { LMOE_PATH_AUTO = 0, LMOE_PATH_STREAM = 1, LMOE_PATH_TILED = 2 } l
  * be multiples of 128).  Everything else stays bf16 / fp32.
  * FP8: the *_fp8 / *_fp8_scale fields, weights as lmoe_quantize_fp8_weight
  * writes them; the expert projections run on 8-bit activations too: the
- * latent (from its fp32 values) and the hidden rows relu(.)^2 (from the fp32
- * sums) are quantised as by lmoe_quantize_fp8, the sums are fp32.  R and F
- * must be multiples of 128. */
+ * latent (from its fp32 values) and the hidden rows relu(.)^2 (from the
+ * unrounded sums) are quantised as by lmoe_quantize_fp8, and the products are
+ * summed as by lmoe_fp8_matmul with bf16 y.  R and F must be multiples of 128,
+ * max_tokens * R below 2^31. */
 typedef enum {
   LMOE_EXPERTS_BF16 = 0,
   LMOE_EXPERTS_MXFP4 = 1,
