@@ -9,6 +9,8 @@ neighbouring code: such a step is at most 2^-3 of one of F terms, the bf16
 rounding of the expert outputs 2^-8; the layer's bar of 2e-2 normwise covers
 both."""
 
+import concurrent.futures
+
 import numpy as np
 import pytest
 import torch
@@ -168,6 +170,43 @@ def test_layer_inside_its_block(tokens):
     assert normwise_rel(g.r, r) <= OUT_REL
     assert normwise_rel(g.y.float().cpu().numpy(), O.bf16_bits_to_f64(h) + y) <= OUT_REL
     layer.close()
+
+
+def test_operators_on_two_streams_at_once():
+    """Calls that run at the same time share nothing: the bits of calls made alone."""
+    g = torch.Generator().manual_seed(3)
+    rnd = lambda *n: torch.randn(*n, generator=g).to(DEV)  # noqa: E731
+    wc, ws = pkg.quantize_fp8_weight(rnd(6, 512, 1024) * 0.02)
+    dc, ds = pkg.quantize_fp8_weight(rnd(256, 1024) * 0.02)
+    post, gate = rnd(1024), rnd(1024)
+    router = pkg.make_router(64, 8, n_group=8, topk_group=4)
+
+    def work(x, y, stream):
+        c, sc = pkg.quantize_fp8(x, stream=stream)
+        off = torch.tensor([0, 7, 7, 90, 91, 250, x.shape[0]], dtype=torch.int32).to(DEV)
+        torch.cuda.synchronize()
+        out = []
+        for _ in range(8):
+            h, n, st = pkg.block_norm(x, y, pre_weight=gate, post_weight=post, gate=gate,
+                                      want_stats=True, stream=stream)
+            gr = pkg.block_norm_backward(x, y, st, dh_out=x, dx=y, pre_weight=gate,
+                                         post_weight=post, gate=gate, stream=stream)
+            out.append([pkg.fp8_matmul(c, sc, wc, ws, off, stream=stream),      # tile list
+                        pkg.fp8_matmul(c, sc, dc, ds, stream=stream),           # parts of k
+                        *pkg.route_logits(router, x[:, :64], stream=stream),
+                        h, n, gr.dh, gr.dy, gr.dpre_weight, gr.dpost_weight, gr.dgate])
+        return out
+
+    xs, ys = [rnd(400, 1024) for _ in range(2)], [rnd(400, 1024) for _ in range(2)]
+    want = [work(x, y, None)[0] for x, y in zip(xs, ys)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    with concurrent.futures.ThreadPoolExecutor(2) as pool:
+        got = list(pool.map(work, xs, ys, streams))
+    torch.cuda.synchronize()
+    for runs, alone in zip(got, want):
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(r, alone))
 
 
 def test_layer_replays_from_a_graph():
