@@ -20,6 +20,7 @@
 // takes the 16-byte chunks q and 4 + q of row r's 128 bytes.
 #include <type_traits>
 
+#include "fp8_copies.h"
 #include "fp8_device.h"
 #include "gemm_device.h"
 #include "kernels.h"
@@ -440,7 +441,7 @@ template <bool GROUPED, int BM, int BN, int WM, int WD, bool EXACT, class OUT>
 __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, const int* ntiles) {
   constexpr int BH = BN / 2, WN = 8 / WM, NW = 8;
   constexpr int TM = BM / WM / 16, TH = BH / WN / 16;
-  constexpr int RPI = 8, ROWB = 128;
+  constexpr int RPI = kFp8CopyRows, ROWB = 128;
   constexpr int NIA = BM / RPI / NW, NIH = BH / RPI / NW;  // copies a wave and unit
   constexpr int ABUF = BM * ROWB, HBUF = BH * ROWB;
   constexpr int NSB = BN / 128;  // scale blocks of the tile's weight rows
@@ -484,9 +485,8 @@ __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, cons
   // c ^ (r / 2) % 8).  Token rows past the tile's count are past the buffer's
   // bound and read as 0 (nothing is fetched, and products of zeros take less
   // power: 1% faster than reading the first row again where 11% of the rows
-  // are such).  Weight rows past N read on into the next matrix, or past the
-  // last one, where the buffer's bound makes them 0 (their columns are not
-  // stored).
+  // are such).  Weight rows past N read the matrix's last rows again (their
+  // columns are not stored).
   const int lr = lane >> 3;
   const int sw = ((4 * (w & 1)) + (lr >> 1)) & 7;
   const uint32_t chunk = (uint32_t)(((lane & 7) ^ sw) * 16);
@@ -504,7 +504,7 @@ __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, cons
   const size_t w0 = ((size_t)e * p.N + n0) * K + kb0 * ROWB;
   const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(
       p.w + w0, (size_t)(GROUPED ? p.groups : 1) * p.N * K - w0);
-  uint32_t ao[NIA], bo = (uint32_t)lr * (uint32_t)K + chunk;
+  uint32_t ao[NIA], bo = fp8_weight_lane(lane, chunk, (uint32_t)K);
 #pragma unroll
   for (int j = 0; j < NIA; ++j) {
     bool ok;
@@ -528,7 +528,7 @@ __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, cons
   auto copy_w = [&](int kb, int h, int r, int j) __attribute__((always_inline)) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rb, (lds_void*)(smem + W00 + r + h * HBUF + (w + NW * j) * RPI * ROWB), 16, bo,
-        kb * ROWB + (h * BH + (w + NW * j) * RPI) * K, 0, 0);
+        fp8_weight_scalar(h * BH + (w + NW * j) * RPI, p.N - n0, kb, K), 0, 0);
   };
   // Token scales of blocks 8 g .. 8 g + 7: instruction i fills rows 8 i .. + 7,
   // lane l row 8 i + l / 8, place l % 8, which holds block (l % 8) ^ 4 (i % 2)
@@ -544,7 +544,7 @@ __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, cons
     const int i = j * (BM / 64) + sg;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rs, (lds_void*)(sxs + ((g & 1) * BM + 8 * i) * 8), 4,
-        row + (uint32_t)(((lane & 7) ^ ((i & 1) << 2)) * 4), g * 32, 0, 0);
+        fp8_xscale_lane(row, lane, i, g), 0, 0, 0);
   };
   // weight scales of the tile: wave w takes 64 blocks of one of its 128-row
   // blocks (places past K hold what follows in memory, or 0 past its end)
@@ -556,8 +556,8 @@ __device__ __forceinline__ void fp8_pipe_body(Fp8Gemm p, const Tile* tiles, cons
     const int b = w % NSB, i = w / NSB;
     if (i < kFp8MaxBlocks / 64)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rws, (lds_void*)(sws + b * kFp8MaxBlocks + i * 64), 4, lane * 4,
-          (b * KBT + i * 64) * 4, 0, 0);
+          rws, (lds_void*)(sws + b * kFp8MaxBlocks + i * 64), 4,
+          fp8_wscale_lane(lane, b, i, KBT), 0, 0, 0);
   }
   // what the first MFMAs need, then what step 0 reads, then what it need not
   // wait for
