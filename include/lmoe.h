@@ -96,7 +96,8 @@ typedef enum { LMOE_PATH_AUTO = 0, LMOE_PATH_STREAM = 1, LMOE_PATH_TILED = 2 } l
  * writes them; the expert projections run on 8-bit activations too: the
  * latent (from its fp32 values) and the hidden rows relu(.)^2 (from the
  * unrounded sums) are quantised as by lmoe_quantize_fp8, and the products are
- * summed as by lmoe_fp8_matmul with bf16 y.  R and F must be multiples of 128,
+ * summed as by lmoe_fp8_matmul with bf16 y (the up projection's always by the
+ * 8-bit matrix instruction).  R and F must be multiples of 128,
  * max_tokens * R below 2^31. */
 typedef enum {
   LMOE_EXPERTS_BF16 = 0,
@@ -377,16 +378,23 @@ lmoe_status lmoe_quantize_fp8_weight(const void *w, int32_t w_type, int64_t matr
                                      int32_t cols, uint8_t *codes, float *scales, void *stream);
 
 /* The product of such activations and weights, y [M, N] = x w^T, rounded once
- * to y_type (fp32 y: fp32 sums throughout; bf16 y: the sum over a block of k is
- * the 8-bit matrix instruction's, which keeps about 17 bits of it, and the
- * blocks are scaled and added in fp32):
+ * to y_type:
  *   y[m][n] = sum_b xs[r][b] ws[n / 128][b] sum_{k in block b} x[r][k] w[n][k]
  * with r = rows[m], or m when rows is NULL.  With n_groups >= 1 there are
  * that many weight matrices and row m takes matrix g of the range offsets[g]
  * <= m < offsets[g + 1] (a sparse layer's rows sorted by expert; empty groups
  * are fine); rows of no group are not written.  Offsets are cut to [0, M];
  * they must ascend.  A row index outside [0, x_rows) gives a row of zeros
- * (if row 0 of x is finite). */
+ * (if row 0 of x is finite).
+ *
+ * Sums are fp32 where y is fp32, and where few rows stream the weights (M up to
+ * 16, or groups of up to 4 rows on average).  Other bf16 y take the 8-bit matrix
+ * instruction: the blocks of k are scaled and added in fp32, but within a block
+ * the products of each eight neighbouring k are cut 13 bits below the largest
+ * power of two among them before they are added.  Of the sum of the terms'
+ * magnitudes that is about 2^-16 on normally distributed values, and up to
+ * 2^-10 where a few values are far larger than the rest; callers who need more
+ * take an fp32 y (half the rate). */
 typedef struct {
   const uint8_t *x;       /* [x_rows, K] codes, 16-byte aligned */
   const float *x_scales;  /* [x_rows, K / 128] */

@@ -8,10 +8,12 @@
 // Each block's sum of code products is one MFMA 16x16x128 from a zero
 // accumulator; it is scaled in fp32 into the running sum (four fused
 // multiply-adds per MFMA and lane, which run beside the next MFMA).  That
-// instruction keeps about 17 bits of the block's sum, well below what the
-// result keeps where it is rounded to bf16 or e4m3; fp32 results take the
-// bf16 MFMA on converted codes instead (EXACT: four 16x16x32, sums in fp32).
-// Weights
+// instruction cuts products far below the largest of their eight (see
+// fp8_device.h): on ordinary values well below what a result rounded to bf16 or
+// e4m3 keeps, with a few large values among small ones about as much.  It is
+// taken only where its rate is the bound (tiles) and the result is bf16 or
+// e4m3.  fp32 results, and bf16 ones where weights are streamed, take the bf16
+// MFMA on converted codes (EXACT: four 16x16x32, sums in fp32).  Weights
 // are the MFMA's A operand and tokens its B operand, so a lane's four results
 // are consecutive columns of one token and the scale is one factor per lane.
 //
@@ -273,13 +275,18 @@ __device__ __forceinline__ i32x4 fp8_permute(const i32x4& a, const i32x4& b, int
 // fixed order.  A wave instruction loads 8 rows x 128 bytes; ds_bpermute
 // moves the pieces to the MFMA's lanes (the layout that the bf16 streaming
 // GEMM measured fastest).  Work-group: 16 RG weight rows x 16 token rows.
-// Bound by HBM: 1 x 10240 x 8192 15 us (5.6 TB/s), 32 tokens' 704 rows over 512
-// experts 589 us at 5120 x 2048 (6.9 TB/s).
+// Bound by HBM: 1 x 10240 x 8192 15.5 us (5.4 TB/s; 14.8 with the 8-bit
+// instruction's sums), 32 tokens' 704 rows over 512 experts 577 to 591 us at
+// 5120 x 2048 (6.9 to 7.0 TB/s; 583 to 588).
 template <bool GROUPED, int NW, int RG, int U, class OUT>
 __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Tile* tiles,
                                                              const int* ntiles) {
   static_assert(RG <= 8, "one scale block");
-  constexpr bool EXACT = std::is_same<OUT, float>::value;
+  // HBM is the bound, so sums are fp32 unless the result is rounded to e4m3
+  // anyway (its eight row groups and both forms of the fragments need 263
+  // registers: one work-group a CU, the decode batch's up projection 0.78 ms
+  // against 0.575).
+  constexpr bool EXACT = !std::is_same<OUT, Relu2Fp8>::value;
   __shared__ f32x4 red[NW][RG][64];
   const int nblocks = (p.N + 16 * RG - 1) / (16 * RG);
   const int nb = blockIdx.x % nblocks;
@@ -943,7 +950,6 @@ hipError_t launch_dense(const Fp8Gemm& p, const Plan& plan, hipStream_t s) {
   if (plan.stream) {
     constexpr int RG = 1, NW = 8;
     const long grid = (p.N + 16 * RG - 1) / (16 * RG);
-    // (never split, so EXACT is what OUT says)
     fp8_stream_kernel<false, NW, RG, 2, OUT><<<grid, NW * 64, 0, s>>>(p, nullptr, nullptr);
   } else {
     auto go = [&](auto bm, auto bn, auto wm, auto wd) {
