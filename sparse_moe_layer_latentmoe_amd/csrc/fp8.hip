@@ -43,10 +43,11 @@ __device__ __forceinline__ float fp8_scale(float amax) {
 // x / s, correctly rounded: r = 1 / s correctly rounded, then one Markstein
 // correction of x r (exact residual by a fused multiply-add), three
 // operations instead of a division.  The residual must not underflow, so
-// very small scales take the division itself.
+// very small scales take the division itself.  The sign is x's (s > 0): for
+// x = -0 the residual is +0 and would lose it.
 __device__ __forceinline__ float fp8_ratio(float x, float s, float r) {
   const float q = x * r;
-  return fmaf(fmaf(-q, s, x), r, q);
+  return copysignf(fmaf(fmaf(-q, s, x), r, q), x);
 }
 constexpr float kFastScale = 0x1p-90f;
 
