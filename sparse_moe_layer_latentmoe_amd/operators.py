@@ -8,7 +8,8 @@ binding: they check tensors, allocate the outputs and marshal pointers; the
 kernels do the work.  ``stream`` is a torch stream or a raw handle of the
 tensors' device (None: that device's current stream); outputs and scratch are
 allocated for that stream, and tensors of a device that is not the current
-one are fine.
+one are fine.  Nothing is recorded for autograd: the gradients are calls of
+their own.
 """
 
 from __future__ import annotations
@@ -98,6 +99,17 @@ def _check(t, what: str, dtypes, ndim=None, shape=None, device=None, dense: bool
         raise ValueError(f"{what}: on {t.device}, expected cuda:{device}")
 
 
+def _no_graph(where: str, *tensors) -> None:
+    """Raise where autograd would expect ``where`` to record a gradient."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if getattr(t, "requires_grad", False):
+                raise ValueError(
+                    f"{where}: an input requires a gradient, which this call does not record; "
+                    f"call it from a torch.autograd.Function whose backward is {where}_backward, "
+                    "or under torch.no_grad()")
+
+
 def _type(t) -> int:
     return F32 if t is None else _TYPE[t.dtype]
 
@@ -163,7 +175,9 @@ def make_router(n_experts: int, top_k: int, score: int = SCORE_SIGMOID, n_group:
 def route_logits(router: LmoeRouter, logits, bias=None, stream=None):
     """(topk_idx int32 [T, K], ascending ids; topk_w fp32 [T, K]) from logits
     [T, E] (fp32 or bf16; rows may be strided) and an optional fp32 [E] bias
-    that only orders the experts."""
+    that only orders the experts.  Logits that require a gradient are refused
+    where autograd is recording (route_logits_backward computes it)."""
+    _no_graph("route_logits", logits)
     _check(logits, "logits", _TYPE, ndim=2, dense=False)
     T, E = logits.shape
     if E != router.n_experts:
@@ -254,7 +268,10 @@ def block_norm(h, y=None, pre_weight=None, post_weight=None, gate=None, res_scal
     h: residual stream [T, D]; y: the block's output [T, D] (None: 0); each
     fp32 or bf16, rows may be strided.  pre_weight, post_weight, res_scale:
     [D] or None.  gate: [D], [T, 1], [T, D] or None.  h_out has h's dtype, x
-    has y's (bf16 without y).  stats (want_stats) is what the backward needs."""
+    has y's (bf16 without y).  stats (want_stats) is what the backward needs.
+    Inputs that require a gradient are refused where autograd is recording
+    (block_norm_backward computes it)."""
+    _no_graph("block_norm", h, y, pre_weight, post_weight, gate, res_scale)
     a = _norm_args(h, y, pre_weight, post_weight, gate, res_scale, eps)
     T, D = h.shape
     with _launch(h.get_device(), stream) as s:
