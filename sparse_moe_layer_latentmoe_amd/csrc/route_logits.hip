@@ -115,7 +115,8 @@ __device__ __forceinline__ float clean_logit(float v) {
 }
 
 // Sums of the `best` (1 or 2) largest of each group's G values in the wave's
-// LDS row; lane g returns group g's.  Each group is walked by P lanes (the
+// LDS row (fp32: half the sum of two, the same order, which cannot overflow);
+// lane g returns group g's.  Each group is walked by P lanes (the
 // largest power of two with n_group P <= 64), whose two largest are then
 // merged; the walk starts at a different place in each group, so that groups
 // a multiple of 64 apart do not meet in one LDS bank.
@@ -149,7 +150,8 @@ __device__ __forceinline__ F group_best(const F* row, int lane, int n_group, int
     t2 = fmax(fmax(t2, o2), fmin(t1, o1));
     t1 = fmax(t1, o1);
   }
-  const F r = best == 2 ? t1 + t2 : t1;
+  const F half = std::is_same<F, float>::value ? F(0.5) : F(1);
+  const F r = best == 2 ? half * t1 + half * t2 : t1;
   return __shfl(r, lane < n_group ? lane << sh : 0, 64);
 }
 
