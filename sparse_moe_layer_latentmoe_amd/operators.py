@@ -93,17 +93,19 @@ def _check(t, what: str, dtypes, ndim=None, shape=None, device=None, dense: bool
             raise ValueError(f"{what}: must be contiguous")
         if t.shape[-1] > 1 and t.stride(-1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
             raise ValueError(f"{what}: rows must be contiguous and not overlap")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: must be a GPU tensor, got one on {t.device}")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"{what}: on {t.device}, expected cuda:{device}")
+    if t.get_device() != device:        # -1 where it is not a GPU tensor
+        if not t.is_cuda:
+            raise ValueError(f"{what}: must be a GPU tensor, got one on {t.device}")
+        if device is not None:
+            raise ValueError(f"{what}: on {t.device}, expected cuda:{device}")
 
 
 def _no_graph(where: str, *tensors) -> None:
-    """Raise where autograd would expect ``where`` to record a gradient."""
+    """Raise where autograd would expect ``where`` to record a gradient
+    (``_check`` speaks up for what is no tensor)."""
     if torch.is_grad_enabled():
         for t in tensors:
-            if getattr(t, "requires_grad", False):
+            if t is not None and getattr(t, "requires_grad", False):
                 raise ValueError(
                     f"{where}: an input requires a gradient, which this call does not record; "
                     f"call it from a torch.autograd.Function whose backward is {where}_backward, "
