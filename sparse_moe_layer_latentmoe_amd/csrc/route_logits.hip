@@ -380,7 +380,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
       if (on) {
         const size_t at = (size_t)t * K + __popcll(mk & below);
         idx_out[at] = id;
-        w_out[at] = p.renorm ? sc * (p.rho / (sum + 1e-20f)) : sc * p.rho;
+        // the quotient first: at most 1, where rho / sum could overflow
+        w_out[at] = (p.renorm ? sc / (sum + 1e-20f) : sc) * p.rho;
       }
       return;
     }
@@ -450,6 +451,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
 //   softmax        dl_i = s_i (ds_i - c), c = sum ds_k s_k; renormalised, that
 //                  sum is rho D / S (1 - (S - 1e-20) / S) = rho D / S 1e-20 / S,
 //                  taken in that form so that nothing cancels
+// ds goes without its factor 1 / S (up to 1e20), which is taken with the score or
+// the slope, both at most S for a selected expert, so that nothing overflows
+// that the gradient does not.
 // One wavefront per token; ds goes through an LDS row to the lanes that own
 // the experts.  Equal ids add up, in order; ids outside [0, E) are ignored.
 // 8111 tokens x 509 experts, bf16, softmax, top-8: 9.4 us (17 MB), two loads'
@@ -466,8 +470,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_backward_kernel
   const LT* lp = logits + (size_t)t * p.stride;
   const int id = lane < K ? idx[(size_t)t * K + lane] : -1;
   const bool valid = id >= 0 && id < E;
-  const float g = valid ? dw[(size_t)t * K + lane] : 0.f;
   const float lk = valid ? clean_logit(route_load(lp + id)) : -INFINITY;
+  // experts that are not available take no part
+  const float g = lk > -INFINITY ? dw[(size_t)t * K + lane] : 0.f;
 
   float s[NJ];
   float m = 0.f, inv = 1.f;
@@ -501,17 +506,18 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_backward_kernel
     sk = lk > -INFINITY ? (lk >= 0.f ? r : ex * r) : 0.f;
     slope = ex * r * r;
   }
-  float ds = p.rho * g, c = 0.f;
+  float ds = p.rho * g, c = 0.f, scale = 1.f;
   if (p.renorm) {
     const float S = wave_sum(sk) + 1e-20f;
     const float D = wave_sum(g * sk);
-    ds = valid ? p.rho / S * (g - D / S) : 0.f;
+    ds = lk > -INFINITY ? p.rho * (g - D / S) : 0.f;
     c = p.rho * (D / S) * (1e-20f / S);
+    scale = 1.0f / S;
   } else if (p.softmax) {
     c = wave_sum(ds * sk);
   }
   // sigmoid: the finished gradient goes through the row; softmax: ds
-  const float put = p.softmax ? ds : ds * slope;
+  const float put = p.softmax ? ds : slope * scale * ds;
   bool dup = false;
   for (int k = 0; k + 1 < K; ++k) {
     const int o = __shfl(id, k, 64);
@@ -532,7 +538,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_backward_kernel
     const int e = j * 64 + lane;
     if (e < E) {
       const float r = row[wv][e];
-      route_store(dlogits + (size_t)t * E + e, p.softmax ? s[j] * inv * (r - c) : r);
+      const float si = s[j] * inv;
+      route_store(dlogits + (size_t)t * E + e, p.softmax ? si * scale * r - si * c : r);
     }
   }
 }
