@@ -98,7 +98,8 @@ typedef enum { LMOE_PATH_AUTO = 0, LMOE_PATH_STREAM = 1, LMOE_PATH_TILED = 2 } l
  * unrounded sums) are quantised as by lmoe_quantize_fp8, and the products are
  * summed as by lmoe_fp8_matmul with bf16 y (the up projection's always by the
  * 8-bit matrix instruction).  R and F must be multiples of 128,
- * max_tokens * R below 2^31. */
+ * max_tokens * R below 2^31 (and with LMOE_PATH_STREAM max_tokens * K / 16 *
+ * max(F / 128, R / 64) below about 2^24). */
 typedef enum {
   LMOE_EXPERTS_BF16 = 0,
   LMOE_EXPERTS_MXFP4 = 1,
@@ -384,7 +385,9 @@ lmoe_status lmoe_quantize_fp8_weight(const void *w, int32_t w_type, int64_t matr
  * that many weight matrices and row m takes matrix g of the range offsets[g]
  * <= m < offsets[g + 1] (a sparse layer's rows sorted by expert; empty groups
  * are fine); rows of no group are not written.  Offsets are cut to [0, M];
- * they must ascend.  A row index outside [0, x_rows) gives a row of zeros
+ * they must ascend.  Products whose launch would need 2^32 threads or more are
+ * LMOE_ERR_UNSUPPORTED (streamed groups of K above 32768: rows / 16 * N / 64 from
+ * 2^24 on).  A row index outside [0, x_rows) gives a row of zeros
  * (if row 0 of x is finite).
  *
  * Sums are fp32 where y is fp32, and where few rows stream the weights (M up to

@@ -917,6 +917,21 @@ long xcd_grid(long work) { return kXcds * ((work + kXcds - 1) / kXcds); }
 // A launch has fewer than 2^32 threads.
 bool too_many(long grid, int threads) { return grid >= (1L << 32) / threads; }
 
+// Grouped launches: row groups of 16 weight rows that a streaming work-group
+// takes (a whole block of 128 where it quantises its output), weight rows of a
+// tile, threads and work-groups.
+constexpr int stream_groups(bool quantised) { return quantised ? 8 : 4; }
+constexpr int kStreamWaves = 4, kGroupedBN = 256, kTileThreads = 512;
+long grouped_grid(const Plan& plan, long max_tiles, int N, bool quantised) {
+  const int bn = plan.stream ? 16 * stream_groups(quantised) : kGroupedBN;
+  const long work = max_tiles * ((N + bn - 1) / bn);
+  return plan.stream ? work : xcd_grid(work);
+}
+bool grouped_fits(const Plan& plan, long max_tiles, int N, bool quantised) {
+  return !too_many(grouped_grid(plan, max_tiles, N, quantised),
+                   plan.stream ? kStreamWaves * 64 : kTileThreads);
+}
+
 // Four waves x 4 row groups: 589 and 559 us for the decode batch's up and down
 // projection, against 644 and 557 for 8 x 2, 615 and 563 for 4 x 2, 928 and
 // 601 for 8 x 1; 595 and 565 for 4 x 8, which quantises its output.
@@ -924,19 +939,17 @@ template <class OUT>
 hipError_t launch_grouped(const Fp8Gemm& p, const Plan& plan, const Tile* tiles, const int* ntiles,
                           int max_tiles, hipStream_t s) {
   using std::integral_constant;
+  constexpr bool Q = std::is_same<OUT, Relu2Fp8>::value;
+  if (!grouped_fits(plan, max_tiles, p.N, Q)) return hipErrorInvalidConfiguration;
+  const long grid = grouped_grid(plan, max_tiles, p.N, Q);
   if (plan.stream) {
-    constexpr int RG = std::is_same<OUT, Relu2Fp8>::value ? 8 : 4, NW = 4;
-    const long grid = (long)max_tiles * ((p.N + 16 * RG - 1) / (16 * RG));
-    if (too_many(grid, NW * 64)) return hipErrorInvalidConfiguration;
+    constexpr int RG = stream_groups(Q), NW = kStreamWaves;
     fp8_stream_kernel<true, NW, RG, 1, OUT><<<grid, NW * 64, 0, s>>>(p, tiles, ntiles);
   } else {
-    constexpr int BN = 256;
-    const long grid = xcd_grid((long)max_tiles * ((p.N + BN - 1) / BN));
-    if (too_many(grid, 512)) return hipErrorInvalidConfiguration;
     auto go = [&](auto bm, auto wm) {
-      fp8_pipe_kernel<true, decltype(bm)::value, BN, decltype(wm)::value, 3,
+      fp8_pipe_kernel<true, decltype(bm)::value, kGroupedBN, decltype(wm)::value, 3,
                       std::is_same<OUT, float>::value, OUT>
-          <<<grid, 512, 0, s>>>(p, tiles, ntiles);
+          <<<grid, kTileThreads, 0, s>>>(p, tiles, ntiles);
     };
     if (plan.bm == 64) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     else if (plan.bm == 128) go(integral_constant<int, 128>{}, integral_constant<int, 2>{});
@@ -1000,6 +1013,15 @@ hipError_t fp8_quantize_weight(const void* w, bool bf16, long matrices, int rows
   return hipGetLastError();
 }
 
+bool fp8_matmul_fits(int M, int N, int KB, int groups, bool out_bf16) {
+  const Plan plan = make_plan(M, N, KB, groups, !out_bf16);
+  if (groups) return grouped_fits(plan, grouped_tiles(M, groups, plan.bm), N, false);
+  if (plan.stream) return true;  // up to 16 rows
+  const int bn = plan.bm == 64 ? 128 : 256;
+  return !too_many(xcd_grid((long)((M + plan.bm - 1) / plan.bm) * ((N + bn - 1) / bn)),
+                   kTileThreads);
+}
+
 size_t fp8_matmul_workspace(int M, int N, int KB, int groups, bool out_bf16) {
   const Plan plan = make_plan(M, N, KB, groups, !out_bf16);
   if (groups) return 256 + (size_t)grouped_tiles(M, groups, plan.bm) * sizeof(Tile);
@@ -1041,6 +1063,10 @@ hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws
 Fp8Plan fp8_expert_plan(int rows, int experts, int KB, int path) {
   if (KB > kFp8MaxBlocks || path == 1) return {true, kStreamTileM, 1};
   return path == 2 ? tiled_plan((double)rows / experts) : grouped_plan(rows, experts, KB);
+}
+
+bool fp8_experts_fit(const Fp8Plan& plan, long max_tiles, int F, int R) {
+  return grouped_fits(plan, max_tiles, F, true) && grouped_fits(plan, max_tiles, R, false);
 }
 
 hipError_t fp8_exp_up(const Fp8Gemm& p, const Fp8Plan& plan, const Tile* tiles, const int* ntiles,

@@ -165,6 +165,8 @@ struct Fp8Gemm {
   int splits = 1;       // of k: set by fp8_matmul
   float* ys = nullptr;  // [M, NB]: the scales of a quantised output
 };
+// whether the product's launches stay below 2^32 threads
+bool fp8_matmul_fits(int M, int N, int KB, int groups, bool out_bf16);
 // bytes of `ws`: the groups' row tiles, or the partial sums of a split of k
 size_t fp8_matmul_workspace(int M, int N, int KB, int groups, bool out_bf16);
 hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws,
@@ -181,6 +183,8 @@ struct Fp8Plan {
   int splits;   // of k (dense tiles)
 };
 Fp8Plan fp8_expert_plan(int rows, int experts, int KB, int path);
+// whether both projections (F hidden, R latent columns) can be launched
+bool fp8_experts_fit(const Fp8Plan& plan, long max_tiles, int F, int R);
 hipError_t fp8_exp_up(const Fp8Gemm& p, const Fp8Plan& plan, const Tile* tiles, const int* ntiles,
                       int max_tiles, hipStream_t s);
 hipError_t fp8_exp_down(const Fp8Gemm& p, const Fp8Plan& plan, const Tile* tiles,

@@ -62,6 +62,18 @@ bool tiled_dims_ok(const lmoe_config& c) {
          c.moe_intermediate_size % bn == 0 && c.moe_latent_size % bn == 0;
 }
 
+// Upper bound on the tile count of the expert tile list for T tokens.
+long max_tiles(const lmoe_config& c, long T, int tile_m) {
+  const long slots = T * c.num_experts_per_tok;
+  return std::min<long>(c.n_routed_experts, slots) + slots / tile_m + 1;
+}
+
+// How T tokens' FP8 expert projections run.
+Fp8Plan plan_fp8(const lmoe_config& c, int T) {
+  return fp8_expert_plan(T * c.num_experts_per_tok, c.n_routed_experts,
+                         std::max(c.moe_latent_size, c.moe_intermediate_size) / 128, c.path);
+}
+
 lmoe_status check_config(const lmoe_config* c) {
   if (!c) return LMOE_ERR_INVALID_ARG;
   if (c->hidden_size <= 0 || c->moe_latent_size <= 0 || c->n_routed_experts <= 0 ||
@@ -104,13 +116,14 @@ lmoe_status check_config(const lmoe_config* c) {
     return LMOE_ERR_INVALID_ARG;
   if (c->max_tokens > (1 << 22)) return LMOE_ERR_UNSUPPORTED;
   if (c->path == LMOE_PATH_TILED && !tiled_dims_ok(*c)) return LMOE_ERR_UNSUPPORTED;
+  // FP8 experts streamed by request: the launches of the longest batch
+  if (c->expert_format == LMOE_EXPERTS_FP8) {
+    const Fp8Plan plan = plan_fp8(*c, c->max_tokens);
+    if (!fp8_experts_fit(plan, max_tiles(*c, c->max_tokens, plan.bm), c->moe_intermediate_size,
+                         c->moe_latent_size))
+      return LMOE_ERR_UNSUPPORTED;
+  }
   return LMOE_OK;
-}
-
-// Upper bound on the tile count of the expert tile list for T tokens.
-long max_tiles(const lmoe_config& c, long T, int tile_m) {
-  const long slots = T * c.num_experts_per_tok;
-  return std::min<long>(c.n_routed_experts, slots) + slots / tile_m + 1;
 }
 
 struct Layout {
@@ -261,8 +274,7 @@ lmoe_status run_forward(const lmoe_config& c, const lmoe_weights& w, const Layou
       tiled_ok && (c.path == LMOE_PATH_TILED ||
                    (c.path == LMOE_PATH_AUTO && static_cast<long>(T) * K > 32L * E));
   const bool fp8 = c.expert_format == LMOE_EXPERTS_FP8;
-  const Fp8Plan plan8 =
-      fp8 ? fp8_expert_plan(T * K, E, std::max(R, F) / 128, c.path) : Fp8Plan{};
+  const Fp8Plan plan8 = fp8 ? plan_fp8(c, T) : Fp8Plan{};
   const int tile_m = fp8 ? plan8.bm : (expert_tiled ? tiled_block_m() : kStreamTileM);
   const int ntile_max = static_cast<int>(max_tiles(c, T, tile_m));
 

@@ -166,6 +166,8 @@ lmoe_status check_fp8(const lmoe_fp8_matmul_args* a) {
   if (!a->rows && a->x_rows < a->M) return LMOE_ERR_INVALID_ARG;
   if (a->rows && static_cast<int64_t>(a->x_rows) * a->K >= (int64_t{1} << 31))
     return LMOE_ERR_UNSUPPORTED;
+  if (!fp8_matmul_fits(a->M, a->N, a->K / 128, a->n_groups, a->y_type == LMOE_BF16))
+    return LMOE_ERR_UNSUPPORTED;
   const int64_t G = a->n_groups ? a->n_groups : 1, kb = a->K / 128, nb = (a->N + 127) / 128;
   if (!disjoint({{a->x, static_cast<int64_t>(a->x_rows) * a->K},
                  {a->x_scales, a->x_rows * kb * 4},
