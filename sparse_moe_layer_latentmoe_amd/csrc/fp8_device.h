@@ -61,4 +61,11 @@ __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d
   return (uint32_t)v;
 }
 
+// A raw buffer over `bytes` from `base` (at most 2 GiB of them).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0,
+                                           (int)(bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0),
+                                           0x00020000);
+}
+
 }  // namespace lmoe

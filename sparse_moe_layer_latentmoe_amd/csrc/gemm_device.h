@@ -14,14 +14,6 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// s_waitcnt with only the LDS counter set, to 0: this wave's LDS writes are
-// done (stage_barrier does not wait for them).
-__device__ __forceinline__ void wait_lgkmcnt0() {
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-}
-
 // Workgroup barrier without a memory fence: the direct-to-LDS loads are
 // waited for explicitly (wait_vmcnt) so that later stages stay in flight.
 // The signal fences keep the compiler from moving LDS accesses across it.
@@ -123,13 +115,6 @@ __device__ __forceinline__ void stage_barrier_hard() {
   __builtin_amdgcn_sched_barrier(0);
   stage_barrier();
   __builtin_amdgcn_sched_barrier(0);
-}
-
-// The same over `bytes` from `base` (at most 2 GiB of them).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, size_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0,
-                                           (int)(bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0),
-                                           0x00020000);
 }
 
 // work_item with the tile list's fields read into scalar registers.

@@ -1,4 +1,5 @@
-// Reductions over the lanes of a wave, and vector types beside lmoe_device.h's.
+// Reductions over the lanes of a wave, the wait for its LDS accesses, and vector
+// types beside lmoe_device.h's.
 #pragma once
 #include "lmoe_device.h"
 
@@ -37,5 +38,13 @@ struct AddOp {
 struct MaxOp {
   __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
+
+// s_waitcnt with only the LDS counter set, to 0: this wave's LDS writes are
+// done (stage_barrier does not wait for them).
+__device__ __forceinline__ void wait_lgkmcnt0() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
 
 }  // namespace lmoe
