@@ -33,20 +33,25 @@ if ROOT not in sys.path:
 METRIC = "LatentMoE layer tokens/s; % HBM roofline (decode) / % bf16 MFMA peak (prefill)"
 HBM_PEAK_GBS = 8000.0        # MI355X HBM3E
 BF16_PEAK_TFLOPS = 2500.0    # MI355X dense bf16 MFMA
+FP8_PEAK_TFLOPS = 5000.0     # MI355X dense fp8 MFMA
 HBM_BOUND = {"tiny", "decode", "mtp_verify", "decode_grouped", "decode_mxfp4",
              "mtp_verify_mxfp4"}
 MXFP4_BYTES = 0.5 + 1.0 / 32
+FP8_WEIGHT_BYTES = 1.0 + 4.0 / (128 * 128)
+FP8_ROW_BYTES = 1.0 + 4.0 / 128
 # Batches of at most this many tokens stream the dense weights, and run the
 # shared expert's down projection on the auxiliary stream (timed with
 # shared_up); the output projection then covers fc2_latent only.
 STREAM_DENSE_MAX_TOKENS = 64
 
 
-def stage_work(sh, T, U, expert_weight_bytes=2.0, block=False):
+def stage_work(sh, T, U, expert_weight_bytes=2.0, block=False, expert_row_bytes=2.0):
     """Algorithmic bytes and flops of each stage for T tokens touching U
     distinct experts (weights read once, activations read/written once);
     expert weights take ``expert_weight_bytes`` per element (2 for bf16,
-    0.5 + 1/32 for MXFP4: half a byte per element plus a scale byte per 32).
+    0.5 + 1/32 for MXFP4: half a byte per element plus a scale byte per 32),
+    their latent and hidden rows ``expert_row_bytes`` (2 for bf16; FP8 experts:
+    a byte plus 4 per 128).
     ``block``: the block's pre-norm (timed inside proj_latent: h and gamma
     read, bf16(gamma h) and 1/rms written) and residual (h read by proj_out)
     are fused in.  For weight-streaming batches (T <= STREAM_DENSE_MAX_TOKENS)
@@ -62,8 +67,9 @@ def stage_work(sh, T, U, expert_weight_bytes=2.0, block=False):
         "router_logits": E * R * 4 + T * R * 4 + T * E * 4,
         "router_select": T * E * 4 + E * 4 + slots * 8,
         "dispatch": slots * 4 * 4 + E * 12,
-        "expert_up": int(U * F * R * expert_weight_bytes) + slots * R * 2 + slots * F * 2,
-        "expert_down": int(U * R * F * expert_weight_bytes) + slots * F * 2 + slots * R * 2,
+        "expert_up": int(U * F * R * expert_weight_bytes) + int(slots * (R + F) * expert_row_bytes),
+        "expert_down": (int(U * R * F * expert_weight_bytes) + int(slots * F * expert_row_bytes)
+                        + slots * R * 2),
         "combine": slots * R * 2 + slots * 8 + T * R * 2,
         "proj_out": D * (R + S) * 2 + T * (R + S) * 2 + T * D * 2,
     }
@@ -322,22 +328,24 @@ FULL_CONFIGS = ("decode", "mtp_verify", "prefill", "skewed")
 ALL_CONFIGS = ("tiny",) + FULL_CONFIGS
 WORKLOADS = ["all", "tiny", "decode", "mtp_verify", "prefill", "skewed", "decode_grouped",
              "decode_mxfp4", "mtp_verify_mxfp4", "decode_block", "mtp_verify_block",
-             "prefill_block", "decode_mxfp4_block", "prefill_mxfp4"]
+             "prefill_block", "decode_mxfp4_block", "prefill_mxfp4", "decode_fp8",
+             "mtp_verify_fp8", "prefill_fp8"]
 
 
 def parse_workload(name):
-    """(layer workload, MXFP4 experts?, block steps fused?) of a --workload name."""
+    """(layer workload, experts' format: "" (bf16), "mxfp4" or "fp8", block steps
+    fused?) of a --workload name."""
     import lmoe_inputs as li
     block = name.endswith("_block")
     base = name[:-len("_block")] if block else name
-    mxfp4 = base.endswith("_mxfp4")
-    return li.workload(base[:-len("_mxfp4")] if mxfp4 else base), mxfp4, block
+    fmt = next((f for f in ("mxfp4", "fp8") if base.endswith("_" + f)), "")
+    return li.workload(base[:-len(fmt) - 1] if fmt else base), fmt, block
 
 
 def build_layer(torch, pkg, li, name, dev, weights=None):
     """Inputs and a layer for the --workload ``name``; full-shape workloads
     reuse ``weights`` (the skewed one with its own correction bias)."""
-    wl, mxfp4, block = parse_workload(name)
+    wl, fmt, block = parse_workload(name)
     if weights is not None and wl.bias_recipe == "zipf":
         weights = dict(weights)
         weights["router_bias"] = torch.from_numpy(
@@ -350,25 +358,33 @@ def build_layer(torch, pkg, li, name, dev, weights=None):
     if block:
         # the block's pre-norm and residual fused: x is the residual stream
         lw["norm_weight"] = li.make_norm_weight(wl, dev)
-    if mxfp4:
+    if fmt == "mxfp4":
         # routed experts stored as MXFP4, quantised by the library's kernel
         up_c, up_s = pkg.quantize_mxfp4(inp.expert_up)
         dn_c, dn_s = pkg.quantize_mxfp4(inp.expert_down)
         lw.update(expert_up=None, expert_down=None, expert_up_mxfp4=up_c,
                   expert_up_scale=up_s, expert_down_mxfp4=dn_c, expert_down_scale=dn_s)
+    elif fmt == "fp8":
+        # as e4m3 codes with a scale for each 128 x 128 block, likewise
+        up_c, up_s = pkg.quantize_fp8_weight(inp.expert_up)
+        dn_c, dn_s = pkg.quantize_fp8_weight(inp.expert_down)
+        lw.update(expert_up=None, expert_down=None, expert_up_fp8=up_c,
+                  expert_up_fp8_scale=up_s, expert_down_fp8=dn_c, expert_down_fp8_scale=dn_s)
     layer = pkg.LatentMoE(wl.shape, lw, max_tokens=wl.tokens,
-                          expert_format=pkg.EXPERTS_MXFP4 if mxfp4 else pkg.EXPERTS_BF16,
+                          expert_format={"": pkg.EXPERTS_BF16, "mxfp4": pkg.EXPERTS_MXFP4,
+                                         "fp8": pkg.EXPERTS_FP8}[fmt],
                           fuse=pkg.FUSE_BLOCK if block else 0)
     return inp, layer
 
 
-def describe(name, sh, T, mxfp4, block):
+def describe(name, sh, T, fmt, block):
     return (f"{name}: LatentMoE layer forward, T={T} tokens, hidden {sh.hidden_size}, latent "
             f"{sh.moe_latent_size}, {sh.n_routed_experts} experts top-{sh.num_experts_per_tok}, "
             f"expert MLP {sh.moe_intermediate_size}, shared "
             f"{sh.moe_shared_expert_intermediate_size}, "
-            + ("MXFP4 routed-expert weights (decoded to bf16), other weights bf16"
-               if mxfp4 else "bf16 weights")
+            + {"": "bf16 weights",
+               "mxfp4": "MXFP4 routed-expert weights (decoded to bf16), other weights bf16",
+               "fp8": "FP8 (e4m3) routed-expert weights and activations, others bf16"}[fmt]
             + ", fp32 router"
             + (", block pre-norm RMSNorm and residual add fused" if block else ""))
 
@@ -377,7 +393,7 @@ def measure(torch, pkg, name, inp, layer, steps, warmup, use_graph=False):
     """Time one workload: K forwards with nothing else on the stream (the
     value), then K more with per-stage HIP events (the per-kernel times the
     rooflines use).  Returns the workload's result block."""
-    wl, mxfp4, block = parse_workload(name)
+    wl, fmt, block = parse_workload(name)
     sh, T = wl.shape, wl.tokens
     dev = inp.x.device
     y = torch.empty_like(inp.x)
@@ -432,7 +448,8 @@ def measure(torch, pkg, name, inp, layer, steps, warmup, use_graph=False):
     ms_events = (t3 - t2) * 1e3 / steps
     stage_ms = {k: v / max(nf, 1) for k, v in stages.items()}
 
-    sb, sf = stage_work(sh, T, U, MXFP4_BYTES if mxfp4 else 2.0, block)
+    sb, sf = stage_work(sh, T, U, {"": 2.0, "mxfp4": MXFP4_BYTES, "fp8": FP8_WEIGHT_BYTES}[fmt],
+                        block, FP8_ROW_BYTES if fmt == "fp8" else 2.0)
     hbm = parse_workload(name)[0].name in HBM_BOUND
     dom = max(stage_ms, key=stage_ms.get)
     if hbm:
@@ -457,8 +474,11 @@ def measure(torch, pkg, name, inp, layer, steps, warmup, use_graph=False):
             layer_roof["measured_bytes"] = None
     else:
         ach = sf[dom] / (stage_ms[dom] * 1e-3) / 1e12
-        roof = {"bound": "mfma", "achieved": round(ach, 1), "peak": BF16_PEAK_TFLOPS,
-                "unit": "TFLOP/s", "frac": round(ach / BF16_PEAK_TFLOPS, 4),
+        # FP8 experts: their products against the fp8 peak, the others bf16's
+        peak = {k: FP8_PEAK_TFLOPS if fmt == "fp8" and k.startswith("expert_")
+                else BF16_PEAK_TFLOPS for k in sf}
+        roof = {"bound": "mfma", "achieved": round(ach, 1), "peak": peak[dom],
+                "unit": "TFLOP/s", "frac": round(ach / peak[dom], 4),
                 "traffic": measured_traffic(name, dom),
                 "kernel": dom, "algorithmic_flops_per_launch": sf[dom],
                 "avg_launch_ms": round(stage_ms[dom], 5)}
@@ -466,8 +486,14 @@ def measure(torch, pkg, name, inp, layer, steps, warmup, use_graph=False):
         layer_ach = fl / (ms * 1e-3) / 1e12
         layer_roof = {"bound": "mfma", "achieved": round(layer_ach, 1), "unit": "TFLOP/s",
                       "frac": round(layer_ach / BF16_PEAK_TFLOPS, 4), "algorithmic_bf16_flops": fl}
+        if fmt == "fp8":
+            ex = sf["expert_up"] + sf["expert_down"]
+            least = (fl - ex) / BF16_PEAK_TFLOPS + ex / FP8_PEAK_TFLOPS
+            layer_roof = {"bound": "mfma", "achieved": round(layer_ach, 1), "unit": "TFLOP/s",
+                          "frac": round(least / 1e12 / (ms * 1e-3), 4),
+                          "algorithmic_bf16_flops": fl - ex, "algorithmic_fp8_flops": ex}
     return {
-        "workload": describe(name, sh, T, mxfp4, block),
+        "workload": describe(name, sh, T, fmt, block),
         "tokens": T, "seed": wl.seed,
         "ms_per_step": round(ms, 5), "us_per_layer": round(ms * 1e3, 2),
         "tokens_per_s": round(T / (ms * 1e-3), 1),
@@ -553,7 +579,7 @@ def main():
         "higher_is_better": True,
         "scaling": "weak",
         "vs_baseline": None,
-        "dtype": "bf16",
+        "dtype": "bf16, experts fp8" if parse_workload(head_name)[1] == "fp8" else "bf16",
         "data": "synthetic",
         "config": {"workload": head["workload"], "tokens": head["tokens"], "seed": head["seed"],
                    "unique_experts": head["unique_experts"],
@@ -572,8 +598,8 @@ def main():
     if len(blocks) > 1:
         out["configs"] = {n: {k: v for k, v in b.items() if k != "touched_experts"}
                           for n, b in blocks.items()}
-    wl_head, mx_head, blk_head = parse_workload(head_name)
-    if not args.no_cpu_baseline and not mx_head and not blk_head and wl_head.shape == li.FULL:
+    wl_head, fmt_head, blk_head = parse_workload(head_name)
+    if not args.no_cpu_baseline and not fmt_head and not blk_head and wl_head.shape == li.FULL:
         tiny_inp = keep.get("tiny") or li.make_inputs(li.workload("tiny"), dev)
         out["cpu_baseline"] = cpu_baseline(keep[head_name], wl_head.shape,
                                            head["touched_experts"], tiny_inp)
