@@ -308,7 +308,8 @@ lmoe_status lmoe_route_logits_backward(const lmoe_router *router, const void *lo
  * h is the residual stream before the block, y the block's output (NULL: 0,
  * the norm ahead of a first block), x the next block's input.  h_out and x
  * round once from fp32 values (x is computed from the unrounded h_out).
- * Values and their squares' means must be finite. */
+ * Values must be finite, and so must the fp32 sums over a row of y^2 (with
+ * post_weight) and of h_out^2. */
 typedef enum {
   LMOE_GATE_NONE = 0,    /* 1 */
   LMOE_GATE_CHANNEL = 1, /* [D] */
@@ -381,7 +382,8 @@ lmoe_status lmoe_quantize_fp8_weight(const void *w, int32_t w_type, int64_t matr
 /* The product of such activations and weights, y [M, N] = x w^T, rounded once
  * to y_type:
  *   y[m][n] = sum_b xs[r][b] ws[n / 128][b] sum_{k in block b} x[r][k] w[n][k]
- * with r = rows[m], or m when rows is NULL.  With n_groups >= 1 there are
+ * with r = rows[m], or m when rows is NULL.  The product of two scales is an
+ * fp32 number: it must be below 2^128, and keeps fewer bits below 2^-126.  With n_groups >= 1 there are
  * that many weight matrices and row m takes matrix g of the range offsets[g]
  * <= m < offsets[g + 1] (a sparse layer's rows sorted by expert; empty groups
  * are fine); rows of no group are not written.  Offsets are cut to [0, M];

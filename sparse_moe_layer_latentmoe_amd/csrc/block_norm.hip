@@ -12,12 +12,23 @@
 //   b  = post g G, yn = y ry            dy = ry (b - yn mean(b yn))
 //   dpost = sum_t g G yn                dpre = sum_t dx hn
 //
-// Both are bound by HBM: a work-group (or one wave, for narrow rows) keeps a
-// row in registers, so each value is read once and written once; sums are
-// fp32, the results round once.  4099 rows of 8192, fp32 stream, bf16 block,
-// bf16 gate [T, D]: forward 99 us (470 MB, 4.7 TB/s), backward 151 us (739 MB,
-// 4.9 TB/s) and 5.8 us for the column sums; a large copy reaches 4.8 TB/s.  32
-// rows forward: 5.1 us, a launch and two reductions.
+// A work-group (or one wave, for narrow rows) keeps a row in registers, so each
+// value is read once and written once; sums are fp32, the results round once.
+// 4099 rows of 8192, fp32 stream, bf16 block, bf16 gate [T, D]: forward 99 us
+// (470 MB, 4.7 TB/s), backward 152 us (739 MB, 4.9 TB/s) and 5.8 us for the
+// column sums; a large copy reaches 4.8 TB/s.  32 rows forward: 5.1 us, a launch
+// and two reductions.
+//
+// HBM bounds the forward at 4096 to 16384 columns (96 to 107 us for as many
+// values) and the look-ahead backward below at 4096 to 8192 (141 to 152 us).
+// Widths just past a step of the launch shapes leave threads idle (2112: 155 and
+// 191 us; 576: 152 and 210; 1024: 103 and 163).  The backward's other forms do
+// not fit the registers and are bound by the traffic of what the compiler
+// spills (a thread, at 4099 x 8192 values): fp32 stream and block 136 to 180
+// bytes, 278 us (bf16 stream, fp32 block 28 to 92: 155 us);
+// rows wider than 8192 384 to 436 bytes, 408 us; 2049 to 8192 columns without
+// wide loads (a width that is no multiple of 8, or arrays not 16-byte aligned)
+// 1.2 KB, 1238 us, and the forward there, one value a load, 225 us.
 //
 // The backward computes h' again from h and y rather than reading it: dalpha
 // needs h anyway.  Column sums: each of a fixed number of work-groups keeps
@@ -401,7 +412,7 @@ __global__ __launch_bounds__(TPR* rows_per_group<TPR>()) void block_norm_backwar
 // loads, rows up to 8192): the next row's loads are issued before the current
 // row is worked on (a row of 8192 is 115 KB a CU, enough to cover HBM's
 // latency; the general kernel above, which does not, took 220 us for the case
-// at the top against 151), and the [D] parameters lie in LDS (1 where absent).  Registers
+// at the top against 152), and the [D] parameters lie in LDS (1 where absent).  Registers
 // are what limits it: the sums take 64 of a thread's 256 and each of the two
 // rows up to 72, so a row stays as it was loaded and is converted again in
 // each of its passes.  GATE: 0 a gate of [D], [T] or none, 1 [T, D] in bf16, 2

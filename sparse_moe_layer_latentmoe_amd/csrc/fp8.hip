@@ -437,9 +437,9 @@ __global__ __launch_bounds__(NW * 64) void fp8_stream_kernel(Fp8Gemm p, const Ti
 // rows with each token block: one block at a time, every 4-byte load was a
 // cache line of its own, half as many line requests as the data itself.
 //
-// 8192 x 10240 x 8192: 543 us, 2.53 PFLOP/s (a library's product of the same
-// codes without scales: 505); 180224 rows over 512 experts, 2048 x 5120: 2.15
-// ms, 1.76 PFLOP/s.  A step of a 256 x 256 tile takes 1.59 us and a tile 6.4 us
+// 8192 x 10240 x 8192: 528 to 558 us, 2.46 to 2.60 PFLOP/s (a library's product
+// of the same codes without scales: 505); 180224 rows over 512 experts, 2048 x
+// 5120: 2.10 to 2.14 ms, 1.77 to 1.80 PFLOP/s.  A step of a 256 x 256 tile takes 1.59 us and a tile 6.4 us
 // beside its steps (192 x 256 grouped: 1.28 to 1.44 and 5.8): first copies and
 // the store of the result, which the next tile's work-group waits for.
 //
@@ -934,7 +934,8 @@ bool grouped_fits(const Plan& plan, long max_tiles, int N, bool quantised) {
 
 // Four waves x 4 row groups: 589 and 559 us for the decode batch's up and down
 // projection, against 644 and 557 for 8 x 2, 615 and 563 for 4 x 2, 928 and
-// 601 for 8 x 1; 595 and 565 for 4 x 8, which quantises its output.
+// 601 for 8 x 1; 595 and 565 for 4 x 8, which quantises its output (all with the
+// 8-bit sums; fp32 sums change 4 x 4 by less than these runs differ).
 template <class OUT>
 hipError_t launch_grouped(const Fp8Gemm& p, const Plan& plan, const Tile* tiles, const int* ntiles,
                           int max_tiles, hipStream_t s) {

@@ -29,7 +29,7 @@
 // Bound by the searches' instructions and, for few tokens, by one wave's chain
 // of them, not by memory.  512 experts, fp32 logits, sigmoid, bias, top-22:
 // 8192 tokens 10.6 us (18 MB, 1.7 TB/s), with 8 groups 16 to 19 us (a token
-// whose groups need 64 bits ends last); 32 tokens 6.2 us.  Searching all slots
+// whose groups need 64 bits ends last); 32 tokens 6.1 us.  Searching all slots
 // instead took 20, 37 and 9.1 us.
 #include <cfloat>
 #include <type_traits>
@@ -456,8 +456,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(
 // that the gradient does not.
 // One wavefront per token; ds goes through an LDS row to the lanes that own
 // the experts.  Equal ids add up, in order; ids outside [0, E) are ignored.
-// 8111 tokens x 509 experts, bf16, softmax, top-8: 9.4 us (17 MB), two loads'
-// latency (ids, then their logits) and the row's exponentials.
+// 8111 tokens x 509 experts, bf16, softmax, top-8: 9.1 us (17 MB): the ids'
+// latency before their logits' (a second load, of values that the softmax form
+// holds in other lanes), the look for equal ids and the row's exponentials.
 template <class LT, int NJ>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_backward_kernel(
     const LT* __restrict__ logits, const int32_t* __restrict__ idx, const float* __restrict__ dw,
