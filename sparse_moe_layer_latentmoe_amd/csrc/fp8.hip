@@ -865,8 +865,10 @@ Plan grouped_plan(int rows, int groups, int KB) {
   return tiled_plan((double)rows / groups);
 }
 
-// Dense: up to 16 rows stream the weights (16 rows x 10240 x 8192: 18 us
-// against 21 for tiles).  Above that the tile shape and the split of k with
+// Dense: up to 16 rows stream the weights (1 / 16 rows x 2048 x 8192: 9.5 / 10.3
+// us a call, 17 in tiles 13.6; 1 / 4 / 8 / 16 rows x 10240 x 8192: 16.5 / 17.2 /
+// 19.6 / 24.7, 17 in tiles 19.0: with that many work-groups, each reading all
+// of x, tiles would win from about 8 rows on).  Above that the tile shape and the split of k with
 // the least estimated time: rounds of tiles over the 256 CUs, each so many
 // blocks of k long (256 x 256 tiles: 1.65 us a block, 128 x 256: 0.96; 64 x
 // 128 tiles, two of which fit a CU: 0.36, or 0.34 for each 256 of them), plus
