@@ -383,23 +383,23 @@ lmoe_status lmoe_quantize_fp8_weight(const void *w, int32_t w_type, int64_t matr
  * to y_type:
  *   y[m][n] = sum_b xs[r][b] ws[n / 128][b] sum_{k in block b} x[r][k] w[n][k]
  * with r = rows[m], or m when rows is NULL.  The product of two scales is an
- * fp32 number: it must be below 2^128, and keeps fewer bits below 2^-126.  With n_groups >= 1 there are
- * that many weight matrices and row m takes matrix g of the range offsets[g]
- * <= m < offsets[g + 1] (a sparse layer's rows sorted by expert; empty groups
- * are fine); rows of no group are not written.  Offsets are cut to [0, M];
+ * fp32 number: it must be below 2^128, and keeps fewer bits below 2^-126.  With
+ * n_groups >= 1 there are that many weight matrices and row m takes matrix g of
+ * the range offsets[g] <= m < offsets[g + 1] (a sparse layer's rows sorted by
+ * expert; empty groups are fine); rows of no group are not written.  Offsets are cut to [0, M];
  * they must ascend.  Products whose launch would need 2^32 threads or more are
  * LMOE_ERR_UNSUPPORTED (streamed groups of K above 32768: rows / 16 * N / 64 from
  * 2^24 on).  A row index outside [0, x_rows) gives a row of zeros
  * (if row 0 of x is finite).
  *
- * Sums are fp32 where y is fp32, and where few rows stream the weights (M up to
- * 16, or groups of up to 4 rows on average).  Other bf16 y take the 8-bit matrix
+ * Sums are fp32 where y is fp32, and where the weights are streamed (M up to 16;
+ * groups of up to 4 rows on average, or with K above 32768).  Other bf16 y take the 8-bit matrix
  * instruction: the blocks of k are scaled and added in fp32, but within a block
  * the products of each eight neighbouring k are cut 13 bits below the largest
  * power of two among them before they are added.  Of the sum of the terms'
- * magnitudes that is about 2^-16 on normally distributed values, and up to
- * 2^-10 where a few values are far larger than the rest; callers who need more
- * take an fp32 y (half the rate). */
+ * magnitudes that is about 2^-16 on normally distributed values, and 2^-10 was
+ * measured where a few values are far larger than the rest; callers who need
+ * more take an fp32 y (half the rate). */
 typedef struct {
   const uint8_t *x;       /* [x_rows, K] codes, 16-byte aligned */
   const float *x_scales;  /* [x_rows, K / 128] */
