@@ -43,11 +43,11 @@ __device__ __forceinline__ float fp8_scale(float amax) {
 // x / s, correctly rounded: r = 1 / s correctly rounded, then one Markstein
 // correction of x r (exact residual by a fused multiply-add), three
 // operations instead of a division.  The residual must not underflow, so
-// very small scales take the division itself.  The sign is x's (s > 0): for
-// x = -0 the residual is +0 and would lose it.
+// very small scales take the division itself.  For x = -0 the residual is +0
+// and the sum +0: where x may be -0, the sign is x's (s > 0).
 __device__ __forceinline__ float fp8_ratio(float x, float s, float r) {
   const float q = x * r;
-  return copysignf(fmaf(fmaf(-q, s, x), r, q), x);
+  return fmaf(fmaf(-q, s, x), r, q);
 }
 constexpr float kFastScale = 0x1p-90f;
 
@@ -57,7 +57,7 @@ __device__ __forceinline__ u32x2 fp8_pack8(const float (&v)[8], float s) {
   if (s >= kFastScale) {
     const float r = 1.0f / s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = fp8_ratio(v[i], s, r);
+    for (int i = 0; i < 8; ++i) q[i] = copysignf(fp8_ratio(v[i], s, r), v[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = v[i] / s;
@@ -237,7 +237,7 @@ __device__ __forceinline__ Frag<EXACT> as_frag(i32x8 a) {
   else return a;
 }
 
-// Four values / s as codes.
+// Four values (squares: no -0 among them) / s as codes.
 __device__ __forceinline__ uint32_t fp8_codes4(f32x4 v, float s) {
   if (s >= kFastScale) {
     const float r = 1.0f / s;
