@@ -426,6 +426,54 @@ size_t lmoe_fp8_matmul_workspace_size(const lmoe_fp8_matmul_args *a);
 lmoe_status lmoe_fp8_matmul(const lmoe_fp8_matmul_args *a, void *workspace,
                             size_t workspace_bytes, void *stream);
 
+/* Microscaled 4-bit floating point (MXFP4): the codes and scales of
+ * lmoe_quantize_mxfp4 (E2M1 elements, a scale 2^(byte - 127) for each 32 along
+ * a row), for activations: x [rows, cols] (of `x_type`, rows x_stride >= cols
+ * elements apart), any cols >= 1.  Codes [rows, 16 ceil(cols / 32)], 4-byte
+ * aligned, those past cols 0; scales [rows, ceil(cols / 32)].  Same rounding,
+ * so the same bits as lmoe_quantize_mxfp4 where that takes x.  Inputs must be
+ * finite.  Fewer than 2^30 blocks. */
+lmoe_status lmoe_quantize_mxfp4_rows(const void *x, int32_t x_type, int64_t rows, int32_t cols,
+                                     int64_t x_stride, uint8_t *codes, uint8_t *scales,
+                                     void *stream);
+
+/* The way back: y [rows, cols] (dense, of y_type) from such codes and scales;
+ * exact, except that values from 2^128 on become infinite.  A scale byte of
+ * 255 gives NaN. */
+lmoe_status lmoe_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                                  int32_t cols, void *y, int32_t y_type, void *stream);
+
+/* The product of two such matrices, y [M, N] = x w^T, rounded once to y_type
+ * from fp32 sums (each addition within about 2^-22 of the magnitudes added,
+ * exact where all scales are equal); dense, grouped and gathered as
+ * lmoe_fp8_matmul.  The product of two values must be below 2^128, and keeps
+ * fewer bits below 2^-126.  A scale byte of 255 makes what it takes part in
+ * NaN. */
+typedef struct {
+  const uint8_t *x;        /* [x_rows, K / 2] codes, 16-byte aligned */
+  const uint8_t *x_scales; /* [x_rows, K / 32], 4-byte aligned */
+  const uint8_t *w;        /* [n_groups or 1, N, K / 2] codes, 16-byte aligned */
+  const uint8_t *w_scales; /* [n_groups or 1, N, K / 32], 4-byte aligned */
+  const int32_t *rows;     /* [M] or NULL (then x_rows >= M) */
+  const int32_t *offsets;  /* [n_groups + 1], NULL if n_groups is 0 */
+  void *y;                 /* [M, N], 16-byte aligned */
+  int32_t y_type;          /* lmoe_dtype */
+  int32_t n_groups;        /* 0 (one matrix, no groups) .. 1024 */
+  int32_t M;               /* 0 .. 2^24 */
+  int32_t x_rows;          /* >= 1 if M > 0; with rows, x_rows * K / 2 < 2^31 */
+  int32_t N;               /* a multiple of 16, up to 2^20 */
+  int32_t K;               /* a multiple of 128, up to 65536 */
+} lmoe_mxfp4_matmul_args;
+
+/* Bytes of workspace of lmoe_mxfp4_matmul, as of lmoe_fp8_matmul (0 where it
+ * needs none, or for arguments it refuses).  Pure host function. */
+size_t lmoe_mxfp4_matmul_workspace_size(const lmoe_mxfp4_matmul_args *a);
+
+/* workspace: 16-byte aligned device memory of that size; calls that may
+ * overlap need one each. */
+lmoe_status lmoe_mxfp4_matmul(const lmoe_mxfp4_matmul_args *a, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
 /* ---- per-kernel timing (HIP events on the forward's stream) ------------ */
 
 /* Number of timed stages of lmoe_forward and the name of stage i.  Stages

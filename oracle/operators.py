@@ -251,3 +251,54 @@ def experts_fp8(z32, idx, w, up, down):
         r[tok] += np.asarray(w, np.float64)[tok, pos][:, None] * (
             h @ dequantize(*down[int(e)], 128).T)
     return r
+
+
+# ---- microscaled 4-bit floating point --------------------------------------------
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def quantize_mxfp4_rows(x):
+    """(codes [R, 16 n], scales [R, n]) of x [R, C], n = ceil(C / 32) blocks:
+    scale 2^e with e = floor(log2 max) - 2, at least -127; elements to the
+    nearest of E2M1 (found among all of them), ties to the even code."""
+    x = np.asarray(x, np.float64)
+    R, C = x.shape
+    n = -(-C // 32)
+    p = np.zeros((R, n * 32))
+    p[:, :C] = x
+    p = p.reshape(R, n, 32)
+    amax = np.abs(p).max(2)
+    e = np.where(amax > 0, np.frexp(amax)[1] - 3, -127).clip(-127, 127)
+    d = np.abs((np.abs(p) / np.ldexp(1.0, e)[..., None])[..., None] - E2M1)
+    # equal distances: an even code counts as half a grain nearer
+    c = np.argmin(np.where(d == d.min(-1, keepdims=True), np.arange(8) % 2, 2), -1)
+    c = (c + 8 * ((p < 0) & (c > 0))).reshape(R, n * 32)
+    return (c[:, 0::2] | (c[:, 1::2] << 4)).astype(np.uint8), (e + 127).astype(np.uint8)
+
+
+def dequantize_mxfp4(codes, scales):
+    """Values [.., 32 n]; NaN where the scale byte is 255."""
+    c = np.stack([codes & 15, codes >> 4], -1).reshape(*scales.shape, 32)
+    v = np.where(c & 8, -1.0, 1.0) * E2M1[c & 7]
+    s = np.where(scales == 255, np.nan, np.ldexp(1.0, scales.astype(int) - 127))
+    return (v * s[..., None]).reshape(*scales.shape[:-1], -1)
+
+
+def grouped_product(x, weights, offsets=None, rows=None):
+    """(y, magnitude, written) of x [X, K] and float64 weights [N, K] or
+    [G, N, K], rows and groups as fp8_matmul's."""
+    if rows is not None:
+        ok = (rows >= 0) & (rows < x.shape[0])
+        x = np.where(ok[:, None], x[np.where(ok, rows, 0)], 0.0)
+    M = x.shape[0]
+    if offsets is None:
+        return x @ weights.T, np.abs(x) @ np.abs(weights).T, np.ones(M, bool)
+    N = weights.shape[1]
+    y, mag, done = np.zeros((M, N)), np.zeros((M, N)), np.zeros(M, bool)
+    for g in range(weights.shape[0]):
+        a, b = (min(max(int(o), 0), M) for o in offsets[g:g + 2])
+        if b > a:
+            w = weights[g]
+            y[a:b], mag[a:b], done[a:b] = x[a:b] @ w.T, np.abs(x[a:b]) @ np.abs(w).T, True
+    return y, mag, done

@@ -1031,6 +1031,21 @@ size_t fp8_matmul_workspace(int M, int N, int KB, int groups, bool out_bf16) {
   return plan.splits > 1 ? (size_t)plan.splits * M * N * sizeof(float) : 0;
 }
 
+hipError_t group_tiles(const int32_t* offsets, int groups, int rows, int tile_m, int max_tiles,
+                       Tile* tiles, int32_t* ntiles, hipStream_t s) {
+  fp8_tiles_kernel<<<1, 1024, 0, s>>>(offsets, groups, rows, tile_m, max_tiles, tiles, ntiles);
+  return hipGetLastError();
+}
+
+hipError_t add_parts(const float* part, int splits, long n, void* y, bool bf16, hipStream_t s) {
+  const long n4 = n / 4, grid = (n4 + 255) / 256;
+  if (bf16)
+    fp8_add_kernel<<<grid, 256, 0, s>>>(part, splits, n4, static_cast<uint16_t*>(y));
+  else
+    fp8_add_kernel<<<grid, 256, 0, s>>>(part, splits, n4, static_cast<float*>(y));
+  return hipGetLastError();
+}
+
 hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws, hipStream_t s) {
   const Plan plan = make_plan(p.M, p.N, p.KB, p.groups, !out_bf16);
   p.splits = plan.splits;
@@ -1038,8 +1053,7 @@ hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws
     const int max_tiles = grouped_tiles(p.M, p.groups, plan.bm);
     int32_t* ntiles = static_cast<int32_t*>(ws);
     Tile* tiles = reinterpret_cast<Tile*>(static_cast<char*>(ws) + 256);
-    fp8_tiles_kernel<<<1, 1024, 0, s>>>(offsets, p.groups, p.M, plan.bm, max_tiles, tiles, ntiles);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = group_tiles(offsets, p.groups, p.M, plan.bm, max_tiles, tiles, ntiles, s);
     if (e != hipSuccess) return e;
     return out_bf16 ? launch_grouped<uint16_t>(p, plan, tiles, ntiles, max_tiles, s)
                     : launch_grouped<float>(p, plan, tiles, ntiles, max_tiles, s);
@@ -1050,14 +1064,7 @@ hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws
     const hipError_t e =
         out_bf16 ? launch_dense<false, float>(p, plan, s) : launch_dense<true, float>(p, plan, s);
     if (e != hipSuccess) return e;
-    const long n4 = (long)p.M * p.N / 4;
-    const long grid = (n4 + 255) / 256;
-    const float* part = static_cast<const float*>(ws);
-    if (out_bf16)
-      fp8_add_kernel<<<grid, 256, 0, s>>>(part, p.splits, n4, static_cast<uint16_t*>(y));
-    else
-      fp8_add_kernel<<<grid, 256, 0, s>>>(part, p.splits, n4, static_cast<float*>(y));
-    return hipGetLastError();
+    return add_parts(static_cast<const float*>(ws), p.splits, (long)p.M * p.N, y, out_bf16, s);
   }
   return out_bf16 ? launch_dense<false, uint16_t>(p, plan, s)
                   : launch_dense<true, float>(p, plan, s);

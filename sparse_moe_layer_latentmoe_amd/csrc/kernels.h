@@ -172,6 +172,13 @@ size_t fp8_matmul_workspace(int M, int N, int KB, int groups, bool out_bf16);
 hipError_t fp8_matmul(Fp8Gemm p, const int32_t* offsets, bool out_bf16, void* ws,
                       hipStream_t s);
 
+// The row tiles (at most tile_m rows each) of the groups offsets[g] ..
+// offsets[g + 1] - 1 of `rows` rows, at most 1024 groups, and their number.
+hipError_t group_tiles(const int32_t* offsets, int groups, int rows, int tile_m, int max_tiles,
+                       Tile* tiles, int32_t* ntiles, hipStream_t s);
+// y = the sum of `splits` arrays of n fp32 numbers (a multiple of 4), in order.
+hipError_t add_parts(const float* part, int splits, long n, void* y, bool bf16, hipStream_t s);
+
 // The layer's expert projections in that format, on the dispatch's tile list
 // (tiles of plan.bm rows; groups = experts, N and K multiples of 128):
 //   up    y = e4m3 codes and ys = scales of relu(z[rows] Wup[e]^T)^2
@@ -189,6 +196,30 @@ hipError_t fp8_exp_up(const Fp8Gemm& p, const Fp8Plan& plan, const Tile* tiles, 
                       int max_tiles, hipStream_t s);
 hipError_t fp8_exp_down(const Fp8Gemm& p, const Fp8Plan& plan, const Tile* tiles,
                         const int* ntiles, int max_tiles, hipStream_t s);
+
+// Microscaled 4-bit floating point (layout: lmoe_quantize_mxfp4).  Rows [rows,
+// cols] `stride` apart -> codes [rows, 16 ceil(cols / 32)] and scales [rows,
+// ceil(cols / 32)], and back to dense rows.
+hipError_t mx4_quantize(const void* x, bool bf16, long rows, int cols, long stride,
+                        uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t mx4_dequantize(const uint8_t* codes, const uint8_t* scales, long rows, int cols,
+                          void* y, bool bf16, hipStream_t s);
+// The product of two such matrices, as fp8_matmul's (K a multiple of 128, N of
+// 16).
+struct Mx4Gemm {
+  const uint8_t* x;     // [x_rows, K / 2]
+  const uint8_t* xs;    // [x_rows, K / 32]
+  const uint8_t* w;     // [groups or 1, N, K / 2]
+  const uint8_t* ws;    // [groups or 1, N, K / 32]
+  const int32_t* rows;  // [M] or null
+  void* y;              // [M, N], bf16 or fp32
+  int M, N, K, x_rows, groups;
+  int splits = 1;  // of k: set by mx4_matmul
+};
+// whether the product's launches stay below 2^32 threads
+bool mx4_matmul_fits(int M, int N, int K, int groups);
+size_t mx4_matmul_workspace(int M, int N, int K, int groups);
+hipError_t mx4_matmul(Mx4Gemm p, const int32_t* offsets, bool out_bf16, void* ws, hipStream_t s);
 
 // r = sum_k w[t][k] O[inv[t][k]] -> r16 (bf16) and, if r32 != NULL, fp32.
 hipError_t combine(const uint16_t* o, const int32_t* inv, const float* w, int T, int K, int R,

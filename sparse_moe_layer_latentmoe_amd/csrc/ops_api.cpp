@@ -180,6 +180,39 @@ lmoe_status check_fp8(const lmoe_fp8_matmul_args* a) {
   return LMOE_OK;
 }
 
+lmoe_status check_mxfp4(const lmoe_mxfp4_matmul_args* a) {
+  if (!a) return LMOE_ERR_INVALID_ARG;
+  if (a->M < 0 || a->N <= 0 || a->K <= 0 || a->n_groups < 0 || !is_type(a->y_type) ||
+      (a->M > 0 && a->x_rows < 1))
+    return LMOE_ERR_INVALID_ARG;
+  if (a->N % 16 || a->K % 128 || a->N > (1 << 20) || a->K > 65536 ||
+      a->n_groups > 1024 || a->M > (1 << 24))
+    return LMOE_ERR_UNSUPPORTED;
+  if (a->M == 0) return LMOE_OK;
+  if (!a->x || !a->x_scales || !a->w || !a->w_scales || !a->y || !aligned(a->x, 16) ||
+      !aligned(a->w, 16) || !aligned(a->y, 16) || !aligned(a->x_scales, 4) ||
+      !aligned(a->w_scales, 4) || !aligned(a->rows, 4) || !aligned(a->offsets, 4))
+    return LMOE_ERR_INVALID_ARG;
+  if ((a->n_groups > 0) != (a->offsets != nullptr)) return LMOE_ERR_INVALID_ARG;
+  if (!a->rows && a->x_rows < a->M) return LMOE_ERR_INVALID_ARG;
+  if (a->rows && static_cast<int64_t>(a->x_rows) * a->K / 2 >= (int64_t{1} << 31))
+    return LMOE_ERR_UNSUPPORTED;
+  if (!mx4_matmul_fits(a->M, a->N, a->K, a->n_groups)) return LMOE_ERR_UNSUPPORTED;
+  return LMOE_OK;
+}
+// No output (y, the workspace) on an input or on each other.
+bool mxfp4_disjoint(const lmoe_mxfp4_matmul_args& a, const void* workspace, size_t bytes) {
+  const int64_t G = a.n_groups ? a.n_groups : 1, K = a.K;
+  return disjoint({{a.x, a.x_rows * (K / 2)},
+                   {a.x_scales, a.x_rows * (K / 32)},
+                   {a.w, G * a.N * (K / 2)},
+                   {a.w_scales, G * a.N * (K / 32)},
+                   {a.rows, static_cast<int64_t>(a.M) * 4},
+                   {a.offsets, (G + 1) * 4}},
+                  {{a.y, static_cast<int64_t>(a.M) * a.N * type_size(a.y_type)},
+                   {workspace, static_cast<int64_t>(bytes)}});
+}
+
 lmoe_status status(hipError_t e) { return e == hipSuccess ? LMOE_OK : LMOE_ERR_HIP; }
 
 }  // namespace
@@ -358,6 +391,60 @@ lmoe_status lmoe_fp8_matmul(const lmoe_fp8_matmul_args* a, void* workspace, size
                   a->M,    a->N,        a->K,
                   a->K / 128, (a->N + 127) / 128, a->x_rows, a->n_groups};
   return status(fp8_matmul(p, a->offsets, a->y_type == LMOE_BF16, workspace,
+                           static_cast<hipStream_t>(stream)));
+}
+
+lmoe_status lmoe_quantize_mxfp4_rows(const void* x, int32_t x_type, int64_t rows, int32_t cols,
+                                     int64_t x_stride, uint8_t* codes, uint8_t* scales,
+                                     void* stream) {
+  if (rows < 0 || cols <= 0 || !is_type(x_type) || x_stride < cols) return LMOE_ERR_INVALID_ARG;
+  if (rows > kMaxElements / cols || x_stride > (int64_t{1} << 31)) return LMOE_ERR_UNSUPPORTED;
+  if (rows == 0) return LMOE_OK;
+  const int64_t nb = (static_cast<int64_t>(cols) + 31) / 32, el = type_size(x_type);
+  // a launch has fewer than 2^32 threads: four to a block
+  if (rows * nb >= (int64_t{1} << 30)) return LMOE_ERR_UNSUPPORTED;
+  if (!x || !codes || !scales || !aligned(x, el) || !aligned(codes, 4))
+    return LMOE_ERR_INVALID_ARG;
+  if (!disjoint({{x, strided(rows, x_stride, cols, el)}},
+                {{codes, rows * nb * 16}, {scales, rows * nb}}))
+    return LMOE_ERR_INVALID_ARG;
+  return status(mx4_quantize(x, x_type == LMOE_BF16, rows, cols, x_stride, codes, scales,
+                             static_cast<hipStream_t>(stream)));
+}
+
+lmoe_status lmoe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                  int32_t cols, void* y, int32_t y_type, void* stream) {
+  if (rows < 0 || cols <= 0 || !is_type(y_type)) return LMOE_ERR_INVALID_ARG;
+  if (rows > kMaxElements / cols) return LMOE_ERR_UNSUPPORTED;
+  if (rows == 0) return LMOE_OK;
+  const int64_t nb = (static_cast<int64_t>(cols) + 31) / 32, el = type_size(y_type);
+  if (rows * nb >= (int64_t{1} << 30)) return LMOE_ERR_UNSUPPORTED;
+  if (!codes || !scales || !y || !aligned(codes, 4) || !aligned(y, el))
+    return LMOE_ERR_INVALID_ARG;
+  if (!disjoint({{codes, rows * nb * 16}, {scales, rows * nb}}, {{y, rows * cols * el}}))
+    return LMOE_ERR_INVALID_ARG;
+  return status(mx4_dequantize(codes, scales, rows, cols, y, y_type == LMOE_BF16,
+                               static_cast<hipStream_t>(stream)));
+}
+
+size_t lmoe_mxfp4_matmul_workspace_size(const lmoe_mxfp4_matmul_args* a) {
+  if (check_mxfp4(a) != LMOE_OK || a->M == 0) return 0;
+  return mx4_matmul_workspace(a->M, a->N, a->K, a->n_groups);
+}
+
+lmoe_status lmoe_mxfp4_matmul(const lmoe_mxfp4_matmul_args* a, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  const lmoe_status st = check_mxfp4(a);
+  if (st != LMOE_OK) return st;
+  if (a->M == 0) return LMOE_OK;
+  const size_t need = mx4_matmul_workspace(a->M, a->N, a->K, a->n_groups);
+  if (!mxfp4_disjoint(*a, nullptr, 0)) return LMOE_ERR_INVALID_ARG;
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return LMOE_ERR_WORKSPACE;
+  if (!mxfp4_disjoint(*a, workspace, need)) return LMOE_ERR_INVALID_ARG;
+  const Mx4Gemm p{a->x, a->x_scales, a->w, a->w_scales, a->rows,  a->y,
+                  a->M, a->N,        a->K, a->x_rows,   a->n_groups};
+  return status(mx4_matmul(p, a->offsets, a->y_type == LMOE_BF16, workspace,
                            static_cast<hipStream_t>(stream)));
 }
 

@@ -58,11 +58,16 @@ class LmoeFp8MatmulArgs(ctypes.Structure):
         (n, ctypes.c_int32) for n in ("y_type", "n_groups", "M", "x_rows", "N", "K")]
 
 
+class LmoeMxfp4MatmulArgs(ctypes.Structure):
+    _fields_ = LmoeFp8MatmulArgs._fields_
+
+
 def declare(lib: ctypes.CDLL) -> None:
     """Declare the C signatures of this module's entry points."""
     P, I, L, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-    R, A, G, M = (ctypes.POINTER(t) for t in (LmoeRouter, LmoeBlockNormArgs, LmoeBlockNormGrads,
-                                              LmoeFp8MatmulArgs))
+    R, A, G, M, X = (ctypes.POINTER(t) for t in (
+        LmoeRouter, LmoeBlockNormArgs, LmoeBlockNormGrads, LmoeFp8MatmulArgs,
+        LmoeMxfp4MatmulArgs))
     for name, args, res in (
             ("lmoe_route_logits", [R, P, I, L, P, I, P, P, P], ctypes.c_int),
             ("lmoe_route_logits_backward", [R, P, I, L, P, P, I, P, P], ctypes.c_int),
@@ -72,7 +77,11 @@ def declare(lib: ctypes.CDLL) -> None:
             ("lmoe_quantize_fp8", [P, I, L, I, L, P, P, P], ctypes.c_int),
             ("lmoe_quantize_fp8_weight", [P, I, L, I, I, P, P, P], ctypes.c_int),
             ("lmoe_fp8_matmul_workspace_size", [M], Z),
-            ("lmoe_fp8_matmul", [M, P, Z, P], ctypes.c_int)):
+            ("lmoe_fp8_matmul", [M, P, Z, P], ctypes.c_int),
+            ("lmoe_quantize_mxfp4_rows", [P, I, L, I, L, P, P, P], ctypes.c_int),
+            ("lmoe_dequantize_mxfp4", [P, P, L, I, P, I, P], ctypes.c_int),
+            ("lmoe_mxfp4_matmul_workspace_size", [X], Z),
+            ("lmoe_mxfp4_matmul", [X, P, Z, P], ctypes.c_int)):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
 
@@ -402,4 +411,109 @@ def fp8_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=torc
         nbytes = int(lib.lmoe_fp8_matmul_workspace_size(a))
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         _done(lib.lmoe_fp8_matmul(a, _ptr(ws), nbytes, s), "lmoe_fp8_matmul")
+    return y
+
+
+# ---- microscaled 4-bit floating point ------------------------------------------
+
+
+def _no_gradient(where: str, *tensors) -> None:
+    """Raise where autograd would expect a gradient of ``where``, which has none."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and getattr(t, "requires_grad", False):
+                raise ValueError(f"{where}: an input requires a gradient, and this call has none; "
+                                 "call it under torch.no_grad()")
+
+
+def quantize_mxfp4_rows(x, stream=None):
+    """(codes uint8 [T, 16 ceil(K / 32)], scales uint8 [T, ceil(K / 32)]) of
+    activations x [T, K] (fp32 or bf16, rows may be strided) in MXFP4: E2M1
+    elements, two to a byte, the first in the low half, and a scale
+    2^(byte - 127) for each 32 of a row.  K is padded with zeros to a multiple
+    of 32.  The rounding is quantize_mxfp4's."""
+    _no_gradient("quantize_mxfp4_rows", x)
+    _check(x, "x", _TYPE, ndim=2, dense=False)
+    T, K = x.shape
+    nb = (K + 31) // 32
+    with _launch(x.get_device(), stream) as s:
+        codes = torch.empty((T, 16 * nb), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((T, nb), dtype=torch.uint8, device=x.device)
+        _done(load_library().lmoe_quantize_mxfp4_rows(
+            _ptr(x), _TYPE[x.dtype], T, K, _row_stride(x), _ptr(codes), _ptr(scales), s),
+            "lmoe_quantize_mxfp4_rows")
+    return codes, scales
+
+
+def dequantize_mxfp4(codes, scales, cols=None, out_dtype=torch.bfloat16, stream=None):
+    """The values (bf16 or fp32, exact) [..., cols] of MXFP4 codes
+    [..., 16 n] and scales [..., n] (quantize_mxfp4, quantize_mxfp4_rows);
+    cols: how many of a row (None: all 32 n)."""
+    u8 = (torch.uint8,)
+    _check(scales, "scales", u8)
+    if scales.dim() < 1:
+        raise ValueError("scales: 0 dimensions, expected at least 1")
+    n = scales.shape[-1]
+    lead = tuple(scales.shape[:-1])
+    _check(codes, "codes", u8, shape=(*lead, 16 * n), device=scales.get_device())
+    cols = 32 * n if cols is None else int(cols)
+    if not 32 * (n - 1) < cols <= 32 * n:
+        raise ValueError(f"cols: {cols}, the codes hold {n} blocks of 32")
+    if out_dtype not in _TYPE:
+        raise TypeError(f"out_dtype: {out_dtype}, expected torch.bfloat16 or torch.float32")
+    rows = 1
+    for d in lead:
+        rows *= d
+    with _launch(scales.get_device(), stream) as s:
+        y = torch.empty((*lead, cols), dtype=out_dtype, device=scales.device)
+        if y.numel():
+            _done(load_library().lmoe_dequantize_mxfp4(_ptr(codes), _ptr(scales), rows, cols,
+                                                       _ptr(y), _TYPE[out_dtype], s),
+                  "lmoe_dequantize_mxfp4")
+    return y
+
+
+def mxfp4_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=torch.bfloat16,
+                 out=None, stream=None):
+    """y [M, N] = x w^T of MXFP4 matrices (quantize_mxfp4_rows, quantize_mxfp4).
+
+    x: codes [X, K / 2] with scales [X, K / 32]; w: codes [N, K / 2] with
+    scales [N, K / 32]; K a multiple of 128, N of 16.  ``rows`` (int32 [M]):
+    row m of y reads x's row rows[m] (else row m; a row outside x is zeros).
+    ``offsets`` (int32 [G + 1], ascending) with w [G, N, K / 2]: rows
+    offsets[g] .. offsets[g + 1] - 1 take matrix g; rows of no group are not
+    written (pass ``out`` to keep what they hold).  out_dtype: bf16 or fp32."""
+    u8, i32 = (torch.uint8,), (torch.int32,)
+    _check(x, "x", u8, ndim=2)
+    dev, gpu = x.device, x.get_device()
+    X, K = x.shape[0], 2 * x.shape[1]
+    _check(w, "w", u8, ndim=2 if offsets is None else 3, device=gpu)
+    N = w.shape[-2]
+    if w.shape[-1] * 2 != K:
+        raise ValueError(f"w: {w.shape[-1]} bytes a row, x has {K // 2}")
+    if K % 128:
+        raise ValueError(f"x: K = {K}, expected a multiple of 128")
+    _check(x_scales, "x_scales", u8, shape=(X, K // 32), device=gpu)
+    _check(w_scales, "w_scales", u8, shape=(*w.shape[:-1], K // 32), device=gpu)
+    if offsets is not None:
+        if w.shape[0] < 1:
+            raise ValueError("w: no groups")
+        _check(offsets, "offsets", i32, shape=(w.shape[0] + 1,), device=gpu)
+    M = X
+    if rows is not None:
+        _check(rows, "rows", i32, ndim=1, device=gpu)
+        M = rows.shape[0]
+    if out is not None:
+        _check(out, "out", _TYPE, shape=(M, N), device=gpu)
+    elif out_dtype not in _TYPE:
+        raise TypeError(f"out_dtype: {out_dtype}, expected torch.bfloat16 or torch.float32")
+    lib = load_library()
+    with _launch(gpu, stream) as s:
+        y = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
+        a = LmoeMxfp4MatmulArgs(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(rows),
+                                _ptr(offsets), _ptr(y), _TYPE[y.dtype],
+                                0 if offsets is None else w.shape[0], M, X, N, K)
+        nbytes = int(lib.lmoe_mxfp4_matmul_workspace_size(a))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        _done(lib.lmoe_mxfp4_matmul(a, _ptr(ws), nbytes, s), "lmoe_mxfp4_matmul")
     return y

@@ -1,0 +1,288 @@
+"""4-bit block-scaled matrices on the GPU against the float64 oracle.
+
+Codes, scales and values are defined by exact steps, so they are compared bit
+for bit.  A product: an instruction adds up to 128 products and its running sum;
+its result is within 2^-22 of the sum of those magnitudes (an fp32 addition rounds
+by 2^-24; the instruction's own measured at most 2^-22.3), there are at most
+K / 64 of them in a row, and at most 8 partial sums of k are added after that:
+(K / 64 + 8) * 2^-22 of the sum of the terms' magnitudes, then one rounding to
+the output type."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_moe_layer_latentmoe_amd as pkg
+from oracle import operators as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F, B = torch.float32, torch.bfloat16
+
+
+def rand(*shape, seed, dtype=F, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype).to(DEV)
+
+
+def check_quantize(x):
+    c, s = pkg.quantize_mxfp4_rows(x)
+    wc, ws = R.quantize_mxfp4_rows(x.float().cpu().numpy())
+    assert np.array_equal(s.cpu().numpy(), ws)
+    assert np.array_equal(c.cpu().numpy(), wc)
+    want = R.dequantize_mxfp4(wc, ws)[:, :x.shape[1]]
+    for dt in (B, F):
+        y = pkg.dequantize_mxfp4(c, s, x.shape[1], dt)
+        assert y.shape == x.shape and y.dtype == dt
+        with np.errstate(over="ignore"):
+            w32 = want.astype(np.float32)
+        assert np.array_equal(y.float().cpu().numpy(), w32)
+
+
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("T,K", [(1, 1), (1, 32), (3, 100), (7, 33), (17, 640), (33, 1000), (5, 31),
+                                 (64, 2048), (2, 10240), (1, 7)])
+def test_rows(T, K, dtype):
+    check_quantize(rand(T, K, seed=T + K, dtype=dtype) *
+                   torch.exp(3 * rand(T, 1, seed=1)).to(dtype))
+
+
+def test_values_at_the_edges():
+    x = rand(16, 64, seed=3)
+    x[0] = 0
+    x[1] *= 1e-42                       # denormal numbers: the scale stops at 2^-127
+    x[2] *= 1e-37
+    x[3] *= 1e-31
+    x[4] *= 1e36
+    x[5, :] = torch.finfo(F).max
+    x[6, :32] = torch.arange(32, device=DEV) * 0.25         # every tie, with 6 and above
+    x[6, 32:] = -x[6, :32]
+    x[7, :32] = torch.arange(32, device=DEV) * 0.125 - 2
+    x[8, 1:] = 0
+    x[9] = -0.0
+    x[10, :] = 0.1
+    x[10, 5] = -7.9                     # small next to a large one: rounds to 0, sign lost
+    x[11] = 2.0 ** -126
+    x[12] = 2.0 ** -149
+    x[13, :32] = torch.tensor([5.0, 4.999999, 5.000001, 2.5, 2.4999998, 2.5000002, 6.5, 7.99] * 4)
+    x[14] = torch.exp2(torch.arange(64, device=DEV).float() - 140)
+    check_quantize(x)
+    big = torch.finfo(B).max
+    check_quantize(x.clamp(-big, big).to(B))
+
+
+def test_same_bits_as_the_weight_quantiser():
+    w = rand(48, 512, seed=8, dtype=B, std=0.02)
+    for a, b in zip(pkg.quantize_mxfp4(w), pkg.quantize_mxfp4_rows(w)):
+        assert torch.equal(a, b)
+
+
+def test_strided_and_unaligned_rows():
+    wide = rand(19, 700, seed=4, dtype=B)
+    for sl in (np.s_[:, 8:136], np.s_[:, 3:259], np.s_[:, 1:2], np.s_[:, 0:640], np.s_[2:, 16:529]):
+        check_quantize(wide[sl])
+    check_quantize(wide.float()[:, 4:260])
+
+
+def test_rows_further_apart_than_32_bits():
+    x = torch.empty(2, 2 ** 31, dtype=B, device=DEV)[:, :300]
+    x.copy_(rand(2, 300, seed=3))
+    check_quantize(x)
+
+
+def test_every_code_and_scale_back():
+    codes = torch.arange(256, device=DEV, dtype=torch.int32).to(torch.uint8).view(16, 16)
+    codes = codes.repeat(16, 1)[:, None, :].expand(256, 2, 16).reshape(256, 32).contiguous()
+    scales = torch.arange(256, device=DEV, dtype=torch.int32).to(torch.uint8)
+    scales = torch.stack([scales, scales.flip(0)], 1).contiguous()
+    want = R.dequantize_mxfp4(codes.cpu().numpy(), scales.cpu().numpy())
+    for dt in (B, F):
+        got = pkg.dequantize_mxfp4(codes, scales, out_dtype=dt).float().cpu().numpy()
+        with np.errstate(over="ignore"):
+            assert np.array_equal(got, want.astype(np.float32), equal_nan=True)
+
+
+def operands(X, N, K, G=None, seed=0, spread=0.0):
+    x = rand(X, K, seed=seed) * torch.exp(spread * rand(X, K // 32, seed=seed + 5)
+                                          ).repeat_interleave(32, 1)
+    w = rand(*((N, K) if G is None else (G, N, K)), seed=seed + 1, std=0.02)
+    w = w * torch.exp(spread * rand(*w.shape[:-1], 1, seed=seed + 6))
+    xc, xs = pkg.quantize_mxfp4_rows(x)
+    wc, ws = pkg.quantize_mxfp4_rows(w.flatten(0, -2))
+    return xc, xs, wc.view(*w.shape[:-1], K // 2), ws.view(*w.shape[:-1], K // 32)
+
+
+def check(ops, offsets=None, rows=None, dtype=B):
+    xc, xs, wc, ws = ops
+    M = xc.shape[0] if rows is None else len(rows)
+    N, K = wc.shape[-2], 2 * wc.shape[-1]
+    i32 = lambda v: None if v is None else torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    out = torch.full((M, N), 7.0, dtype=dtype, device=DEV)
+    y = pkg.mxfp4_matmul(xc, xs, wc, ws, offsets=i32(offsets), rows=i32(rows), out=out)
+    cpu = [t.cpu().numpy() for t in ops]
+    want, mag, done = R.grouped_product(
+        R.dequantize_mxfp4(*cpu[:2]), R.dequantize_mxfp4(*cpu[2:]), offsets,
+        None if rows is None else np.asarray(rows))
+    got = y.double().cpu().numpy()
+    assert np.all(got[~done] == 7.0)
+    unit = torch.finfo(dtype).eps / 2
+    err = np.abs(got - want)[done]
+    ok = ((K // 64 + 8) * 2.0 ** -22 * (1 + unit) * mag + unit * np.abs(want))[done]
+    assert np.all(err <= ok), float((err / np.maximum(ok, 1e-300)).max())
+    return y
+
+
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 33, 64])
+@pytest.mark.parametrize("N,K", [(16, 128), (48, 256), (144, 1152), (400, 640), (64, 4096)])
+def test_few_rows(M, N, K, dtype):
+    check(operands(M, N, K, seed=M + N + K), dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("M,N,K", [(65, 16, 128), (100, 272, 256), (187, 512, 384), (256, 256, 512),
+                                   (257, 128, 640), (300, 400, 1152), (511, 784, 896),
+                                   (130, 1040, 2048), (1200, 2064, 1408)])
+def test_many_rows(M, N, K, dtype):
+    check(operands(M, N, K, seed=M + N + K, spread=2.0), dtype=dtype)
+
+
+def test_scales_far_apart():
+    for M in (5, 200):
+        check(operands(M, 256, 1280, seed=M, spread=8.0), dtype=F)
+
+
+def test_long_k():
+    check(operands(70, 32, 65536, seed=1))
+    check(operands(5, 32, 65536, seed=2))
+
+
+def test_a_scale_that_is_not_a_number_stays_in_its_row():
+    """K ends inside a line of 256: what follows a row is the next row's."""
+    for M in (3, 300):
+        xc, xs, wc, ws = operands(M, 64, 384, seed=1)
+        want = pkg.mxfp4_matmul(xc, xs, wc, ws)
+        bad, wbad = xs.clone(), ws.clone()
+        bad[1] = 255
+        wbad[17] = 255
+        y = pkg.mxfp4_matmul(xc, bad, wc, wbad)
+        assert bool(y[1].isnan().all()) and bool(y[:, 17].isnan().all())
+        keep = torch.ones(M, dtype=torch.bool, device=DEV)
+        keep[1] = False
+        cols = torch.ones(64, dtype=torch.bool, device=DEV)
+        cols[17] = False
+        assert torch.equal(y[keep][:, cols], want[keep][:, cols])
+
+
+def offsets_of(counts):
+    return [0] + list(np.cumsum(counts))
+
+
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 1], [16, 17, 1, 0, 40], [0, 0, 0, 5],
+                                    [200, 0, 129, 64, 1, 300], [128, 256, 127, 257], [600]])
+@pytest.mark.parametrize("N,K", [(16, 128), (272, 384), (528, 256)])
+def test_groups(counts, N, K, dtype):
+    M, G = sum(counts), len(counts)
+    check(operands(M, N, K, G, seed=M + N), offsets_of(counts), dtype=dtype)
+    g = np.random.default_rng(M)
+    check(operands(37, N, K, G, seed=M + N), offsets_of(counts), list(g.integers(0, 37, M)),
+          dtype=dtype)
+
+
+@pytest.mark.parametrize("mean", [0.5, 3, 40])
+def test_many_groups(mean):
+    counts = np.random.default_rng(3).poisson(mean, 1024)
+    check(operands(int(counts.sum()), 32, 128, 1024, seed=9), offsets_of(counts))
+
+
+def test_rows_of_no_group_and_bad_indices():
+    ops = operands(90, 48, 256, 3, seed=11)
+    check(ops, [4, 10, 10, 70])                       # rows before and behind the groups
+    check(ops, [0, 0, 0, 0])
+    check(operands(30, 48, 256, 3, seed=12), [0, 40, 41, 100],
+          [-1, 30, 2 ** 31 - 1, -2 ** 31] + [i % 30 for i in range(96)])
+    check(operands(30, 48, 256, seed=12), rows=[29, -7, 3, 3, 30] + [5] * 200)
+    check(operands(30, 48, 256, seed=12), rows=[29, -7, 3, 3, 30])
+    check(ops, [0, 50, 95, 200])
+    # offsets that do not ascend stay in bounds
+    xc, xs, wc, ws = ops
+    for bad in ([50, 20, 90, 10], [-5, 90, -1, 90], [2 ** 31 - 1, -2 ** 31, 0, 90], [0, 90, 0, 90]):
+        guard = torch.full((92, 48), 7.0, dtype=B, device=DEV)
+        pkg.mxfp4_matmul(xc, xs, wc, ws, torch.tensor(bad, dtype=torch.int32, device=DEV),
+                         out=guard[1:91])
+        torch.cuda.synchronize()
+        assert bool((guard[0] == 7).all()) and bool((guard[91] == 7).all())
+
+
+def test_no_rows():
+    xc, xs, wc, ws = operands(1, 32, 128)
+    assert pkg.mxfp4_matmul(xc[:0], xs[:0], wc, ws).shape == (0, 32)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    assert pkg.mxfp4_matmul(xc, xs, wc, ws, rows=none).shape == (0, 32)
+    c, s = pkg.quantize_mxfp4_rows(rand(0, 100, seed=0))
+    assert c.shape == (0, 64) and s.shape == (0, 4)
+    assert pkg.dequantize_mxfp4(c, s, 100).shape == (0, 100)
+
+
+def test_same_bits_on_another_stream_and_in_two_graphs():
+    counts = [70, 0, 300, 5]
+    off = torch.tensor(offsets_of(counts), dtype=torch.int32, device=DEV)
+    x = rand(sum(counts), 512, seed=1, dtype=B)
+    w, ws = pkg.quantize_mxfp4(rand(4, 320, 512, seed=2, std=0.02, dtype=B))
+
+    def step(stream=None):
+        q, s = pkg.quantize_mxfp4_rows(x, stream=stream)
+        y = pkg.mxfp4_matmul(q, s, w, ws, off, stream=stream)
+        return y, pkg.mxfp4_matmul(q, s, w[0], ws[0], out_dtype=F, stream=stream)
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        y1 = step()
+    with torch.cuda.graph(g2):
+        y2 = step()
+    for seed in range(3):
+        x.copy_(rand(*x.shape, seed=20 + seed, dtype=B))
+        g1.replay()
+        g2.replay()
+        torch.cuda.synchronize()
+        want = step()
+        assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(y1, want, y2))
+
+
+def test_experts_in_four_bits_end_to_end():
+    """Routing, sorted slots, both grouped products with the activation and its
+    quantisation between them, against the oracle fed what each step wrote."""
+    T, E, K, D, H = 45, 12, 3, 256, 384
+    x = rand(T, D, seed=1, dtype=B)
+    up = pkg.quantize_mxfp4(rand(E, H, D, seed=2, std=0.06, dtype=B))
+    down = pkg.quantize_mxfp4(rand(E, D, H, seed=3, std=0.06, dtype=B))
+    router = pkg.make_router(E, K, scale=2.0)
+    idx, w = pkg.route_logits(router, rand(T, E, seed=4))
+    order = idx.flatten().argsort(stable=True)
+    off = torch.nn.functional.pad(torch.bincount(idx.flatten(), minlength=E).cumsum(0), (1, 0)).int()
+    xq = pkg.quantize_mxfp4_rows(x)
+    u = pkg.mxfp4_matmul(*xq, *up, offsets=off, rows=(order // K).int(), out_dtype=F)
+    hq = pkg.quantize_mxfp4_rows(torch.relu(u) ** 2)
+    o = pkg.mxfp4_matmul(*hq, *down, offsets=off, out_dtype=F)
+    y = torch.zeros(T, D, device=DEV).index_add_(0, order // K, o * w.flatten()[order][:, None])
+
+    cpu = lambda q: R.dequantize_mxfp4(*[t.cpu().numpy() for t in q])  # noqa: E731
+    offs = off.tolist()
+    wu, mu, _ = R.grouped_product(cpu(xq), cpu(up), offs, (order // K).cpu().numpy())
+    assert np.all(np.abs(u.double().cpu().numpy() - wu) <= (D // 64 + 8) * 2.0 ** -22 * mu
+                  + 2.0 ** -24 * np.abs(wu))
+    wo, mo, _ = R.grouped_product(cpu(hq), cpu(down), offs)
+    wy, my = np.zeros((T, D)), np.zeros((T, D))
+    ww = w.flatten()[order].double().cpu().numpy()[:, None]
+    np.add.at(wy, (order // K).cpu().numpy(), wo * ww)
+    np.add.at(my, (order // K).cpu().numpy(), mo * ww)
+    # K products rounded and added in fp32 on top of the product's own bound
+    ok = ((H // 64 + 8) * 2.0 ** -22 + (K + 2) * 2.0 ** -24) * my
+    assert np.all(np.abs(y.double().cpu().numpy() - wy) <= ok)
