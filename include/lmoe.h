@@ -474,6 +474,51 @@ size_t lmoe_mxfp4_matmul_workspace_size(const lmoe_mxfp4_matmul_args *a);
 lmoe_status lmoe_mxfp4_matmul(const lmoe_mxfp4_matmul_args *a, void *workspace,
                               size_t workspace_bytes, void *stream);
 
+/* A whole sparse layer for a few tokens, in two kernels:
+ *   l = x gate^T;  (I, w) = routing of l as by lmoe_route_logits
+ *   y = sum_k w_k act(x up[I_k]^T) down[I_k]^T  (+ act(x shared_up^T)
+ *       shared_down^T)
+ *   act(u) = relu(u)^2 or, gated, silu(first half of u) * second half
+ * Weights of all experts are of one expert_format, as elsewhere in this file
+ * (bf16; e4m3 with a scale for each 128 x 128 block; MXFP4); activations are
+ * not quantised.  Logits are 64-bit sums rounded once to fp32; products and
+ * sums are fp32 (the hidden rows are kept in fp32), w_k is applied to an
+ * expert's fp32 output, and y rounds once.  Each used expert's weights are
+ * read once.  Inputs must be finite. */
+typedef enum { LMOE_ACT_RELU2 = 0, LMOE_ACT_SWIGLU = 1 } lmoe_activation;
+typedef struct {
+  lmoe_router router;
+  const void *x;        /* [T, D], rows x_stride elements apart, 16-byte aligned */
+  int64_t x_stride;     /* >= D, a multiple of 8 */
+  const void *gate;     /* [E, D] router weight, 16-byte aligned */
+  const float *bias;    /* [E], finite, or NULL */
+  /* codes (or bf16) and scales (NULL for bf16), 16-byte aligned; H = F, or 2 F
+   * with LMOE_ACT_SWIGLU (the first F rows: the gate's), likewise S */
+  const void *up;          /* [E, H, D] */
+  const void *down;        /* [E, D, F] */
+  const void *shared_up;   /* [S or 2 S, D]; NULL if S is 0 */
+  const void *shared_down; /* [D, S]; NULL if S is 0 */
+  const void *up_scales, *down_scales, *shared_up_scales, *shared_down_scales;
+  void *y;              /* [T, D], 16-byte aligned */
+  int32_t *topk_idx;    /* [T, K] the experts, ascending */
+  float *topk_w;        /* [T, K] */
+  int32_t x_type, gate_type, y_type; /* lmoe_dtype */
+  int32_t expert_format;             /* lmoe_expert_format */
+  int32_t activation;                /* lmoe_activation */
+  int32_t T;                         /* 0..16 */
+  int32_t D, F, S;  /* S may be 0; multiples of 64 (bf16) or 128, up to 32768; a
+                       matrix must be below 2^32 bytes */
+} lmoe_moe_tokens_args;
+
+/* Bytes of workspace of lmoe_moe_tokens (logits, hidden and output rows,
+ * counters; 0 for arguments it refuses).  Pure host function. */
+size_t lmoe_moe_tokens_workspace_size(const lmoe_moe_tokens_args *a);
+
+/* workspace: 256-byte aligned device memory of that size, in any state; calls
+ * that may overlap need one each. */
+lmoe_status lmoe_moe_tokens(const lmoe_moe_tokens_args *a, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
 /* ---- per-kernel timing (HIP events on the forward's stream) ------------ */
 
 /* Number of timed stages of lmoe_forward and the name of stage i.  Stages

@@ -302,3 +302,44 @@ def grouped_product(x, weights, offsets=None, rows=None):
             w = weights[g]
             y[a:b], mag[a:b], done[a:b] = x[a:b] @ w.T, np.abs(x[a:b]) @ np.abs(w).T, True
     return y, mag, done
+
+
+# ---- a sparse layer for a few tokens ----------------------------------------------
+
+
+def moe_expert(x, up, down, swiglu, unit, ulps):
+    """(y, bound) of act(x up^T) down^T for float64 matrices: bound is what y may
+    be off by where every sum of n terms is off by (n + ulps) unit of the sum of
+    their magnitudes, and the activation by 8 unit of itself."""
+    u, du = x @ up.T, (x.shape[1] + ulps) * unit * (np.abs(x) @ np.abs(up).T)
+    if swiglu:
+        n = u.shape[1] // 2
+        g, v, dg, dv = u[:, :n], u[:, n:], du[:, :n], du[:, n:]
+        s = g / (1.0 + np.exp(-g))
+        h = s * v
+        # the slope of silu is at most 1.1
+        dh = 1.1 * dg * (np.abs(v) + dv) + np.abs(s) * dv
+    else:
+        r = np.maximum(u, 0.0)
+        h, dh = r * r, 2.0 * r * du + du * du
+    dh = dh + 8 * unit * (np.abs(h) + dh)
+    y = h @ down.T
+    return y, (dh + (down.shape[1] + ulps) * unit * (np.abs(h) + dh)) @ np.abs(down).T
+
+
+def moe_tokens(x, idx, w, up, down, shared=None, swiglu=False, unit=2.0 ** -24, ulps=64):
+    """(y, bound) of the layer for given experts idx and weights w [T, K]; up(e),
+    down(e): float64 matrices; shared: (up, down) or None."""
+    x, w = np.asarray(x, np.float64), np.asarray(w, np.float64)
+    y, b, top = (np.zeros_like(x) for _ in range(3))
+    n = idx.shape[1]
+    for e in np.unique(idx):
+        t, k = np.nonzero(idx == e)
+        o, d = moe_expert(x[t], up(int(e)), down(int(e)), swiglu, unit, ulps)
+        y[t] += w[t, k][:, None] * o
+        b[t] += np.abs(w[t, k][:, None]) * d
+        top[t] += np.abs(w[t, k][:, None] * o)
+    if shared is not None:
+        o, d = moe_expert(x, *shared, swiglu, unit, ulps)
+        y, b, top = y + o, b + d, top + np.abs(o)
+    return y, b + (n + 3) * unit * (top + b)

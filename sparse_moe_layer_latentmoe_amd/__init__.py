@@ -41,7 +41,7 @@ EXPORTED = (
     "lmoe_block_norm_workspace_size", "lmoe_block_norm_backward", "lmoe_quantize_fp8",
     "lmoe_quantize_fp8_weight", "lmoe_fp8_matmul_workspace_size", "lmoe_fp8_matmul",
     "lmoe_quantize_mxfp4_rows", "lmoe_dequantize_mxfp4", "lmoe_mxfp4_matmul_workspace_size",
-    "lmoe_mxfp4_matmul",
+    "lmoe_mxfp4_matmul", "lmoe_moe_tokens_workspace_size", "lmoe_moe_tokens",
 )
 
 
@@ -395,9 +395,9 @@ class LatentMoE:
 
 # The operators around the layer (their own module; the same binding style).
 from .operators import (  # noqa: E402
-    GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, SCORE_SIGMOID, SCORE_SOFTMAX,
-    BlockNormGrads, LmoeBlockNormArgs, LmoeBlockNormGrads, LmoeFp8MatmulArgs, LmoeMxfp4MatmulArgs,
-    LmoeRouter, block_norm, block_norm_backward, dequantize_mxfp4, fp8_matmul, make_router,
-    mxfp4_matmul, quantize_fp8, quantize_fp8_weight, quantize_mxfp4_rows, route_logits,
+    ACT_RELU2, ACT_SWIGLU, GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, SCORE_SIGMOID, SCORE_SOFTMAX,
+    BlockNormGrads, LmoeBlockNormArgs, LmoeBlockNormGrads, LmoeFp8MatmulArgs, LmoeMoeTokensArgs,
+    LmoeMxfp4MatmulArgs, LmoeRouter, block_norm, block_norm_backward, dequantize_mxfp4, fp8_matmul,
+    make_router, moe_tokens, mxfp4_matmul, quantize_fp8, quantize_fp8_weight, quantize_mxfp4_rows, route_logits,
     route_logits_backward)
 from .operators import declare as _declare_operators  # noqa: E402

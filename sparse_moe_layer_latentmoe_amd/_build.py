@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "liblmoe.so")
 SOURCES = ["lmoe_api.cpp", "gemm_stream.hip", "gemm_tiled.hip", "router.hip", "dispatch.hip",
            "mxfp4.hip", "block.hip", "ops_api.cpp", "route_logits.hip", "block_norm.hip",
-           "fp8.hip", "mx4.hip"]
+           "fp8.hip", "mx4.hip", "moe_tokens.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -221,6 +221,26 @@ bool mx4_matmul_fits(int M, int N, int K, int groups);
 size_t mx4_matmul_workspace(int M, int N, int K, int groups);
 hipError_t mx4_matmul(Mx4Gemm p, const int32_t* offsets, bool out_bf16, void* ws, hipStream_t s);
 
+// A whole sparse layer for 1 <= T <= 16 tokens (T K <= 1024): router, experts,
+// weighted sum, shared expert (S > 0).  D, F and S multiples of 64, or of 128
+// where the format is not bf16; a matrix is smaller than 2^32 bytes.
+struct MoeTokens {
+  const void* x;                                 // [T, D], rows x_stride apart
+  const void* gate;                              // [E, D]
+  const float* bias;                             // [E] or null
+  const void *up, *down, *sup, *sdown;           // codes: [E, F or 2 F, D], [E, D, F], ...
+  const void *up_s, *down_s, *sup_s, *sdown_s;   // scales (not for bf16)
+  void* y;                                       // [T, D]
+  int32_t* idx;                                  // [T, K]
+  float* weights;                                // [T, K]
+  long x_stride;
+  int x_bf16, gate_bf16, y_bf16, format, gated;  // format: lmoe_expert_format
+  int T, D, F, S;
+  RouteProblem r;
+};
+size_t moe_tokens_workspace(const MoeTokens& m);
+hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s);
+
 // r = sum_k w[t][k] O[inv[t][k]] -> r16 (bf16) and, if r32 != NULL, fp32.
 hipError_t combine(const uint16_t* o, const int32_t* inv, const float* w, int T, int K, int R,
                    uint16_t* r16, float* r32, hipStream_t s);

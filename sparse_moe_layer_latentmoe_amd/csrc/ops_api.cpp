@@ -213,6 +213,110 @@ bool mxfp4_disjoint(const lmoe_mxfp4_matmul_args& a, const void* workspace, size
                    {workspace, static_cast<int64_t>(bytes)}});
 }
 
+constexpr int32_t kFewTokens = 16, kFewWidth = 32768;
+
+// Codes and scales of [rows, cols] in an expert format.
+int64_t code_bytes(int32_t format, int64_t rows, int64_t cols) {
+  return format == LMOE_EXPERTS_BF16   ? rows * cols * 2
+         : format == LMOE_EXPERTS_FP8 ? rows * cols
+                                       : rows * cols / 2;
+}
+int64_t scale_bytes(int32_t format, int64_t rows, int64_t cols) {
+  return format == LMOE_EXPERTS_BF16   ? 0
+         : format == LMOE_EXPERTS_FP8 ? rows / 128 * (cols / 128) * 4
+                                       : rows * cols / 32;
+}
+
+// Sizes and settings (what the workspace's size depends on).
+lmoe_status check_few_sizes(const lmoe_moe_tokens_args* a) {
+  if (!a) return LMOE_ERR_INVALID_ARG;
+  const lmoe_status st = check_route(&a->router, LMOE_F32, a->router.n_experts, a->T);
+  if (st != LMOE_OK) return st;
+  if (a->D <= 0 || a->F <= 0 || a->S < 0 || !is_type(a->x_type) || !is_type(a->gate_type) ||
+      !is_type(a->y_type))
+    return LMOE_ERR_INVALID_ARG;
+  if (a->expert_format != LMOE_EXPERTS_BF16 && a->expert_format != LMOE_EXPERTS_MXFP4 &&
+      a->expert_format != LMOE_EXPERTS_FP8)
+    return LMOE_ERR_INVALID_ARG;
+  if (a->activation != LMOE_ACT_RELU2 && a->activation != LMOE_ACT_SWIGLU)
+    return LMOE_ERR_INVALID_ARG;
+  if (a->T > kFewTokens) return LMOE_ERR_TOO_MANY_TOKENS;
+  const int32_t step = a->expert_format == LMOE_EXPERTS_BF16 ? 64 : 128;
+  for (int32_t n : {a->D, a->F, a->S})
+    if (n % step || n > kFewWidth) return LMOE_ERR_UNSUPPORTED;
+  const int64_t two = a->activation == LMOE_ACT_SWIGLU ? 2 : 1;
+  for (int32_t n : {a->F, a->S})
+    if (code_bytes(a->expert_format, two * n, a->D) >= (int64_t{1} << 32))
+      return LMOE_ERR_UNSUPPORTED;
+  return LMOE_OK;
+}
+
+lmoe_status check_few(const lmoe_moe_tokens_args* a) {
+  const bool sc = a->expert_format != LMOE_EXPERTS_BF16, sh = a->S > 0;
+  if (!a->x || !a->gate || !a->up || !a->down || !a->y || !a->topk_idx || !a->topk_w ||
+      (a->shared_up != nullptr) != sh || (a->shared_down != nullptr) != sh ||
+      (a->up_scales != nullptr) != sc || (a->down_scales != nullptr) != sc ||
+      (a->shared_up_scales != nullptr) != (sc && sh) ||
+      (a->shared_down_scales != nullptr) != (sc && sh))
+    return LMOE_ERR_INVALID_ARG;
+  for (const void* p : {a->x, a->gate, a->up, a->down, a->shared_up, a->shared_down, a->up_scales,
+                        a->down_scales, a->shared_up_scales, a->shared_down_scales,
+                        static_cast<const void*>(a->y)})
+    if (!aligned(p, 16)) return LMOE_ERR_INVALID_ARG;
+  if (!aligned(a->bias, 4) || !aligned(a->topk_idx, 4) || !aligned(a->topk_w, 4) ||
+      a->x_stride < a->D || a->x_stride % 8)
+    return LMOE_ERR_INVALID_ARG;
+  if (a->x_stride > (int64_t{1} << 31)) return LMOE_ERR_UNSUPPORTED;
+  return LMOE_OK;
+}
+bool few_disjoint(const lmoe_moe_tokens_args& a, const void* workspace, size_t bytes) {
+  const int64_t E = a.router.n_experts, K = a.router.top_k, T = a.T, D = a.D;
+  const int64_t two = a.activation == LMOE_ACT_SWIGLU ? 2 : 1;
+  const int32_t f = a.expert_format;
+  return disjoint({{a.x, strided(T, a.x_stride, D, type_size(a.x_type))},
+                   {a.gate, E * D * type_size(a.gate_type)},
+                   {a.bias, E * 4},
+                   {a.up, E * code_bytes(f, two * a.F, D)},
+                   {a.down, E * code_bytes(f, D, a.F)},
+                   {a.shared_up, code_bytes(f, two * a.S, D)},
+                   {a.shared_down, code_bytes(f, D, a.S)},
+                   {a.up_scales, E * scale_bytes(f, two * a.F, D)},
+                   {a.down_scales, E * scale_bytes(f, D, a.F)},
+                   {a.shared_up_scales, scale_bytes(f, two * a.S, D)},
+                   {a.shared_down_scales, scale_bytes(f, D, a.S)}},
+                  {{a.y, T * D * type_size(a.y_type)},
+                   {a.topk_idx, T * K * 4},
+                   {a.topk_w, T * K * 4},
+                   {workspace, static_cast<int64_t>(bytes)}});
+}
+MoeTokens few_problem(const lmoe_moe_tokens_args& a) {
+  return {a.x,
+          a.gate,
+          a.bias,
+          a.up,
+          a.down,
+          a.shared_up,
+          a.shared_down,
+          a.up_scales,
+          a.down_scales,
+          a.shared_up_scales,
+          a.shared_down_scales,
+          a.y,
+          a.topk_idx,
+          a.topk_w,
+          static_cast<long>(a.x_stride),
+          a.x_type == LMOE_BF16,
+          a.gate_type == LMOE_BF16,
+          a.y_type == LMOE_BF16,
+          a.expert_format,
+          a.activation == LMOE_ACT_SWIGLU,
+          a.T,
+          a.D,
+          a.F,
+          a.S,
+          route_problem(a.router, a.router.n_experts, a.T)};
+}
+
 lmoe_status status(hipError_t e) { return e == hipSuccess ? LMOE_OK : LMOE_ERR_HIP; }
 
 }  // namespace
@@ -446,6 +550,25 @@ lmoe_status lmoe_mxfp4_matmul(const lmoe_mxfp4_matmul_args* a, void* workspace,
                   a->M, a->N,        a->K, a->x_rows,   a->n_groups};
   return status(mx4_matmul(p, a->offsets, a->y_type == LMOE_BF16, workspace,
                            static_cast<hipStream_t>(stream)));
+}
+
+size_t lmoe_moe_tokens_workspace_size(const lmoe_moe_tokens_args* a) {
+  if (check_few_sizes(a) != LMOE_OK || a->T == 0) return 0;
+  return moe_tokens_workspace(few_problem(*a));
+}
+
+lmoe_status lmoe_moe_tokens(const lmoe_moe_tokens_args* a, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  lmoe_status st = check_few_sizes(a);
+  if (st != LMOE_OK || a->T == 0) return st;
+  st = check_few(a);
+  if (st != LMOE_OK) return st;
+  if (!few_disjoint(*a, nullptr, 0)) return LMOE_ERR_INVALID_ARG;
+  const MoeTokens m = few_problem(*a);
+  const size_t need = moe_tokens_workspace(m);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LMOE_ERR_WORKSPACE;
+  if (!few_disjoint(*a, workspace, need)) return LMOE_ERR_INVALID_ARG;
+  return status(moe_tokens(m, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -20,11 +20,13 @@ from dataclasses import dataclass
 
 import torch
 
-from . import LMOE_OK, LmoeError, _ptr, load_library
+from . import (EXPERTS_BF16, EXPERTS_FP8, EXPERTS_MXFP4, LMOE_OK, LmoeError, _ptr,
+               load_library)
 
 F32, BF16 = 0, 1                                    # lmoe_dtype
 SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1                 # lmoe_score
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3   # lmoe_gate
+ACT_RELU2, ACT_SWIGLU = 0, 1                        # lmoe_activation
 
 _TYPE = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -62,12 +64,21 @@ class LmoeMxfp4MatmulArgs(ctypes.Structure):
     _fields_ = LmoeFp8MatmulArgs._fields_
 
 
+class LmoeMoeTokensArgs(ctypes.Structure):
+    _fields_ = [("router", LmoeRouter), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in (
+            "gate", "bias", "up", "down", "shared_up", "shared_down", "up_scales", "down_scales",
+            "shared_up_scales", "shared_down_scales", "y", "topk_idx", "topk_w")] + [
+        (n, ctypes.c_int32) for n in (
+            "x_type", "gate_type", "y_type", "expert_format", "activation", "T", "D", "F", "S")]
+
+
 def declare(lib: ctypes.CDLL) -> None:
     """Declare the C signatures of this module's entry points."""
     P, I, L, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-    R, A, G, M, X = (ctypes.POINTER(t) for t in (
+    R, A, G, M, X, W = (ctypes.POINTER(t) for t in (
         LmoeRouter, LmoeBlockNormArgs, LmoeBlockNormGrads, LmoeFp8MatmulArgs,
-        LmoeMxfp4MatmulArgs))
+        LmoeMxfp4MatmulArgs, LmoeMoeTokensArgs))
     for name, args, res in (
             ("lmoe_route_logits", [R, P, I, L, P, I, P, P, P], ctypes.c_int),
             ("lmoe_route_logits_backward", [R, P, I, L, P, P, I, P, P], ctypes.c_int),
@@ -81,7 +92,9 @@ def declare(lib: ctypes.CDLL) -> None:
             ("lmoe_quantize_mxfp4_rows", [P, I, L, I, L, P, P, P], ctypes.c_int),
             ("lmoe_dequantize_mxfp4", [P, P, L, I, P, I, P], ctypes.c_int),
             ("lmoe_mxfp4_matmul_workspace_size", [X], Z),
-            ("lmoe_mxfp4_matmul", [X, P, Z, P], ctypes.c_int)):
+            ("lmoe_mxfp4_matmul", [X, P, Z, P], ctypes.c_int),
+            ("lmoe_moe_tokens_workspace_size", [W], Z),
+            ("lmoe_moe_tokens", [W, P, Z, P], ctypes.c_int)):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
 
@@ -517,3 +530,86 @@ def mxfp4_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=to
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         _done(lib.lmoe_mxfp4_matmul(a, _ptr(ws), nbytes, s), "lmoe_mxfp4_matmul")
     return y
+
+
+# ---- a sparse layer for a few tokens ---------------------------------------------
+
+_FORMAT = {torch.bfloat16: EXPERTS_BF16, torch.uint8: EXPERTS_MXFP4, _E4M3: EXPERTS_FP8}
+
+
+def _check_matrices(t, s, what: str, fmt: int, shape, device) -> None:
+    """Codes (or bf16 values) ``t`` of ``shape`` and scales ``s`` in a format."""
+    *lead, n, k = shape
+    dtype = next(d for d, f in _FORMAT.items() if f == fmt)
+    _check(t, what, (dtype,), shape=(*lead, n, k // 2 if fmt == EXPERTS_MXFP4 else k),
+           device=device)
+    if fmt == EXPERTS_BF16:
+        if s is not None:
+            raise ValueError(f"{what}_scales: bf16 weights have none")
+    elif fmt == EXPERTS_MXFP4:
+        _check(s, what + "_scales", (torch.uint8,), shape=(*lead, n, k // 32), device=device)
+    else:
+        _check(s, what + "_scales", (torch.float32,),
+               shape=(*lead, (n + 127) // 128, (k + 127) // 128), device=device)
+
+
+def moe_tokens(router: LmoeRouter, x, gate, up, down, bias=None, up_scales=None, down_scales=None,
+               shared_up=None, shared_down=None, shared_up_scales=None, shared_down_scales=None,
+               activation: int = ACT_RELU2, out_dtype=torch.bfloat16, stream=None):
+    """(y [T, D], topk_idx int32 [T, K], topk_w fp32 [T, K]): a whole sparse
+    layer for up to 16 tokens x [T, D] (fp32 or bf16, rows may be strided).
+
+    gate [E, D] (fp32 or bf16): the router's weight; ``router`` (make_router)
+    and the fp32 [E] bias route its logits.  up [E, F, D] and down [E, D, F]:
+    the experts, relu(u)^2 between them, or with ACT_SWIGLU up [E, 2 F, D] and
+    silu(first half) * second half.  Weights in bf16, e4m3 with the scales of
+    quantize_fp8_weight, or MXFP4 (uint8 codes) with those of quantize_mxfp4,
+    all in one format.  shared_up [S or 2 S, D], shared_down [D, S]: an expert
+    that every token takes with weight 1.  Widths are multiples of 64 (bf16) or
+    128.  out_dtype: bf16 or fp32."""
+    _no_gradient("moe_tokens", x, gate, bias, up, down, shared_up, shared_down)
+    _check(x, "x", _TYPE, ndim=2, dense=False)
+    T, D = x.shape
+    gpu = x.get_device()
+    E, K = int(router.n_experts), max(int(router.top_k), 0)
+    _check(gate, "gate", _TYPE, shape=(E, D), device=gpu)
+    if bias is not None:
+        _check(bias, "bias", (torch.float32,), shape=(E,), device=gpu)
+    _check(up, "up", _FORMAT, ndim=3, device=gpu)
+    fmt = _FORMAT[up.dtype]
+    two = 2 if activation == ACT_SWIGLU else 1
+    H = up.shape[1]
+    if H % two:
+        raise ValueError(f"up: {H} rows, expected two halves")
+    F = H // two
+    _check_matrices(up, up_scales, "up", fmt, (E, H, D), gpu)
+    _check_matrices(down, down_scales, "down", fmt, (E, D, F), gpu)
+    S = 0
+    if (shared_up is None) != (shared_down is None):
+        raise ValueError("shared_up, shared_down: both or none")
+    if shared_up is not None:
+        _check(shared_up, "shared_up", (up.dtype,), ndim=2, device=gpu)
+        H = shared_up.shape[0]
+        if H < two or H % two:
+            raise ValueError(f"shared_up: {H} rows, expected {'two halves' if two > 1 else 'some'}")
+        S = H // two
+        _check_matrices(shared_up, shared_up_scales, "shared_up", fmt, (H, D), gpu)
+        _check_matrices(shared_down, shared_down_scales, "shared_down", fmt, (D, S), gpu)
+    elif shared_up_scales is not None or shared_down_scales is not None:
+        raise ValueError("shared scales without a shared expert")
+    if out_dtype not in _TYPE:
+        raise TypeError(f"out_dtype: {out_dtype}, expected torch.bfloat16 or torch.float32")
+    lib = load_library()
+    with _launch(gpu, stream) as s:
+        y = torch.empty((T, D), dtype=out_dtype, device=x.device)
+        idx = torch.empty((T, K), dtype=torch.int32, device=x.device)
+        w = torch.empty((T, K), dtype=torch.float32, device=x.device)
+        a = LmoeMoeTokensArgs(
+            router, _ptr(x), _row_stride(x), _ptr(gate), _ptr(bias), _ptr(up), _ptr(down),
+            _ptr(shared_up), _ptr(shared_down), _ptr(up_scales), _ptr(down_scales),
+            _ptr(shared_up_scales), _ptr(shared_down_scales), _ptr(y), _ptr(idx), _ptr(w),
+            _TYPE[x.dtype], _TYPE[gate.dtype], _TYPE[out_dtype], fmt, int(activation), T, D, F, S)
+        nbytes = int(lib.lmoe_moe_tokens_workspace_size(a))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+        _done(lib.lmoe_moe_tokens(a, _ptr(ws), nbytes, s), "lmoe_moe_tokens")
+    return y, idx, w
