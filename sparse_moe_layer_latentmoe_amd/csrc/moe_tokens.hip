@@ -1,4 +1,4 @@
-// A whole sparse layer for a few tokens (up to 16) in two kernels.
+// A whole sparse layer for a few tokens (up to 16).
 //
 //   l_t = x_t Wg^T;  (I_t, w_t) = route(l_t)
 //   h_p = act(x_t Wup[e]^T)            for each pair p = (t, k), e = I_t[k]
@@ -7,24 +7,35 @@
 //
 // Bound by HBM: each used expert's weights are read once, whatever the number
 // of tokens that use it, and everything else is small; so what counts is that
-// the weights' stream starts early and never pauses.  The first kernel computes
-// the logits (64-bit sums, rounded once to fp32) and clears the second one's
-// counters.  The second one's work-groups each route all tokens by themselves
-// (a wave a token), list the used experts, and then draw items from one
-// counter: first blocks of rows of the up projections, expert by expert, then
-// blocks of the down projections.  A down item waits until its expert's hidden
-// rows are written, all of which have lower numbers; a work-group that holds
-// an up item never waits, so the item with the lowest number is always worked
-// on, whichever work-groups run.  The pairs' output rows are added by the
-// wave that finishes a block of columns last, in a fixed order: same bits every
-// time.
+// the weights' stream starts early and never pauses.  Two kernels: the first
+// computes the logits (64-bit sums, rounded once to fp32) and clears the second
+// one's counters and flags.  The second one's work-groups each route all tokens
+// by themselves (a wave a token; above kRouteHere tokens route_logits's kernel
+// does it before them), list the used experts, and then draw items: first blocks
+// of rows of the up projections, expert by expert, then of the down projections.
 //
-// Weights are the MFMA's A operand, read from HBM as whole lines into
-// registers two stages ahead (across items) and decoded exactly to bf16 (8-bit:
-// the block's scale on its sum).  The tokens' operand is bf16, too: a value that
-// is no bf16 number (fp32 x, the hidden rows) is taken as the sum of three, 24
-// bits, so products are exact to fp32 and sums are fp32 sums; the extra matrix
-// instructions run in the time that the weights take to arrive.
+// Items are drawn from kQueues counters a projection (one counter for all took
+// 25 ns an item, whatever its size), each work-group from its own until that is
+// empty and then from the others.  A down item waits until its expert's hidden
+// rows are written.  No work-group draws a down item before all up items are
+// drawn, and who holds an up item does not wait, so whatever is waited for is
+// being worked on, whichever work-groups run.  The pairs' output rows are added
+// by the wave that finishes a block of columns last, in a fixed order: the same
+// bits every time.
+//
+// Weights are the MFMA's A operand, read from HBM as whole lines into registers
+// two stages ahead (across items), brought into its layout by ds_bpermute and
+// decoded exactly to bf16 (8-bit: the block's scale on its sum).  The tokens'
+// operand is bf16, too: a value that is no bf16 number (fp32 x, the hidden rows)
+// is the sum of two such parts (y in bf16: 16 bits, its error far below y's
+// rounding) or three (24 bits), each a column of its own of the operand, of which
+// one token leaves 15 free; their results are added at the end.  An expert with
+// more rows than the 16 columns hold is taken as several, whose weights come
+// again from a cache.
+//
+// The loop is kept small and rolled: unrolled over the forms of an item, its 40 KB
+// of code did not stay in the instruction cache and it ran three times as long.
+// So did rings of lines in LDS: their copies took as long to issue as to arrive.
 #include <type_traits>
 
 #include "fp8_device.h"
@@ -37,39 +48,80 @@ namespace lmoe {
 
 namespace {
 
-constexpr int kWaves = 8, kThreads = kWaves * 64;
-constexpr int kMaxPairs = 1024;    // T K
-constexpr int kXBytes = 48 * 1024; // the tokens' operand in LDS
+constexpr int kWaves = 4, kThreads = kWaves * 64;
+constexpr int kQueues = 16, kSpread = 64;  // counters, ints apart
+constexpr int kRouteHere = 4;              // tokens that every work-group routes
+constexpr int kLines = 2;                  // lines a wave loads at a time (a stage)
 
-struct MoeParams {
-  MoeTokens m;
-  float *logits, *h, *hs, *o;
-  int32_t *next, *up_done, *down_done;
-};
-
-// Formats: k values in a line of 128 bytes, row groups of 16 that an item
-// holds, lines a wave loads at a time, fragments of 8 values in 16 bytes.
+// Formats: k values in a line of 128 bytes, fragments of 8 values in 16 bytes,
+// waves that share a row group of 16 (each takes every WK-th line).  Items are 16
+// kWaves / WK rows: 64 KB at K = 2048 in each format; a line of each wave is 256
+// values of x.
 template <int FMT>
 struct Fmt;
 template <>
 struct Fmt<0> {  // bf16
-  static constexpr int LK = 64, RG = 1, U = 2, NF = 1;
+  static constexpr int LK = 64, NF = 1, WK = 4;
 };
 template <>
 struct Fmt<1> {  // MXFP4
-  static constexpr int LK = 256, RG = 2, U = 1, NF = 4;
+  static constexpr int LK = 256, NF = 4, WK = 1;
 };
 template <>
 struct Fmt<2> {  // FP8
-  static constexpr int LK = 128, RG = 2, U = 1, NF = 2;
+  static constexpr int LK = 128, NF = 2, WK = 2;
 };
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
+// c ? a : b of values.  (A conditional of variables chooses between their
+// addresses, which keeps all that a kernel's lambdas share in memory.)
+template <class V>
+__device__ __forceinline__ V pick(bool c, V a, V b) {
+  return c ? a : b;
+}
+
+struct MoeParams {
+  MoeTokens m;
+  float *logits, *h, *hs, *o;
+  int32_t *queues, *up_done, *down_done;
+  int turn;    // rows of an expert taken at a time
+  int xbytes;  // LDS for the tokens' rows
+  int misc;    // where in LDS what is not of the loop begins
+};
+
 __device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
   const u16x4 v = *reinterpret_cast<const u16x4*>(p);
   return f32x4{bf16_to_f32(v[0]), bf16_to_f32(v[1]), bf16_to_f32(v[2]), bf16_to_f32(v[3])};
+}
+
+// What work-groups hand each other (hidden rows, output rows) is stored and
+// loaded past the XCDs' own L2 caches, by relaxed atomics of the whole device:
+// a finished store is then visible everywhere, and no cache has to be written
+// back or emptied.  (With plain stores and agent fences instead, which do that
+// for a whole L2 at every item, the kernel took five times as long.)
+__device__ __forceinline__ void put4_shared(float* p, f32x4 v) {
+  uint64_t u[2];
+  __builtin_memcpy(u, &v, 16);
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  __hip_atomic_store(q, u[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(q + 1, u[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4 get4_shared(const float* p) {
+  const uint64_t* q = reinterpret_cast<const uint64_t*>(p);
+  const uint64_t u[2] = {__hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                         __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)};
+  f32x4 v;
+  __builtin_memcpy(&v, u, 16);
+  return v;
+}
+__device__ __forceinline__ float get1_shared(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// This wave's stores are done (and none of its later accesses begins before).
+__device__ __forceinline__ void stores_done() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  wait_vmcnt<0>();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
 }  // namespace
@@ -83,8 +135,7 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const XT* __restrict__ 
   constexpr int TB = 8;
   __shared__ double part[4][TB];
   const int e = blockIdx.x, tid = threadIdx.x;
-  if (e == 0)
-    for (int i = tid; i < nsync; i += 256) sync[i] = 0;
+  for (int i = e * 256 + tid; i < nsync; i += E * 256) sync[i] = 0;
   for (int t0 = 0; t0 < T; t0 += TB) {
     double acc[TB];
 #pragma unroll
@@ -115,70 +166,102 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const XT* __restrict__ 
 
 namespace {
 
-// What a work-group works on: block `blk` of rows of expert slot u (-1: the
-// shared expert) in one of the two projections.
+// What a work-group works on: block `blk` of rows of entry u in one of the two
+// projections, K long.
 struct Item {
-  int valid, down, u, blk;
+  int down, u, blk, K;
 };
 
-// One projection of one expert.
-struct Matrix {
-  const uint8_t* w;  // codes
-  const uint8_t* s;  // scales
-  int K, rows;       // rows: of one half where gated
+// What a wave loads: its rows' lines in an item's matrix.
+struct Source {
+  const uint8_t* codes;
+  const uint32_t* scales;
+  uint32_t lane, slane;  // a lane's offset in eight rows, in the scales
+  int first, second;     // offsets of the first and the last eight rows
+  int lines, odd;        // of the item; the last is half a line
 };
+
+struct Stage {
+  u32x4 l[kLines][2];
+  uint32_t s[kLines][2];
+};
+
+constexpr int kShared = 0xFFFF;  // an entry of the shared expert
 
 }  // namespace
 
+// NJ: E is at most 64 NJ and the tokens are routed here; 0: they have been.
 template <int FMT, int NJ>
 __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   using C = Fmt<FMT>;
-  constexpr int LK = C::LK, RG = C::RG, U = C::U, NF = C::NF;
-  constexpr int LANES = kWaves * U;  // lines of a stage, over the waves
-  constexpr int RW = NJ >= 16 ? 4 : 8;
-  constexpr int RED = kWaves * RG * 64 * 16;
-  constexpr int ROUTE = RW * (256 + NJ * 512);
-  static_assert(ROUTE + kMaxPairs * 4 + 2 * 4096 <= kXBytes + RED, "prologue's room");
-  __shared__ __attribute__((aligned(16))) char smem[kXBytes + RED];
-  __shared__ float sw[kMaxPairs];               // pairs' weights
-  __shared__ uint16_t slist[kMaxPairs];         // pairs by expert
-  __shared__ uint16_t sexp[kMaxPairs], sstart[kMaxPairs + 1];  // used experts, their first pair
-  __shared__ int stick, scount[kWaves];
+  constexpr int LK = C::LK, NF = C::NF, WK = C::WK, WR = kWaves / WK, U = kLines;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
 
   const MoeTokens& m = p.m;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int w = uniform(tid >> 6);
+  const int w = uniform(tid >> 6), wk = w % WK, wr = w / WK;
   const int T = m.T, E = m.r.E, K = m.r.K, D = m.D, F = m.F, S = m.S, gated = m.gated;
   const int P = T * K;
+  int queue = blockIdx.x % kQueues;  // (wave 0's, as is the phase)
+  int phase = 0;
 
   // ---- routing and the list of used experts, in every work-group ----
-  int first = 0;
-  if (tid == 0) first = __hip_atomic_fetch_add(p.next, 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  int32_t* const sidx = reinterpret_cast<int32_t*>(smem + ROUTE);
-  uint32_t* const smask = reinterpret_cast<uint32_t*>(smem + ROUTE + kMaxPairs * 4);
-  uint32_t* const sfirst = smask + 1024;
+  int pending = 0;
+  if (tid == 0)
+    pending = __hip_atomic_fetch_add(p.queues + queue * kSpread, 2, __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+  int* const stick = reinterpret_cast<int*>(smem + p.misc);     // [2] drawn items
+  int* const scount = stick + 2;                                // [kWaves]
+  float* const sw = reinterpret_cast<float*>(scount + kWaves);  // [P] pairs' weights
+  uint16_t* const slist = reinterpret_cast<uint16_t*>(sw + P);  // [P] pairs by expert
+  // entries: expert, first of its pairs in the list, their number
+  uint16_t* const sexp = slist + P;
+  uint16_t* const sstart = sexp + P + 16;
+  uint16_t* const srows = sstart + P + 16;
+  constexpr int ROUTE = kRouteHere * (256 + NJ * 512);
+  uint32_t* const smask = reinterpret_cast<uint32_t*>(smem + ROUTE);  // [E] tokens
+  uint32_t* const sfirst = smask + E;                                 // [E]
+  int32_t* const sidx = reinterpret_cast<int32_t*>(sfirst + E);       // [P]
   for (int i = tid; i < E; i += kThreads) smask[i] = 0;
-  if (w < RW)
-    for (int t = w; t < T; t += RW)
-      route_token<float, NJ>(p.logits + (size_t)t * E, m.bias, m.r, lane,
+  if constexpr (NJ > 0) {
+    if (w < T)
+      route_token<float, NJ>(p.logits + (size_t)w * E, m.bias, m.r, lane,
                              reinterpret_cast<float*>(smem + w * 256),
-                             smem + RW * 256 + w * NJ * 512, sidx + t * K, sw + t * K);
+                             smem + kRouteHere * 256 + w * NJ * 512, sidx + w * K, sw + w * K);
+  } else {
+    for (int i = tid; i < P; i += kThreads) {
+      sidx[i] = m.idx[i];
+      sw[i] = m.weights[i];
+    }
+  }
   __syncthreads();
   for (int i = tid; i < P; i += kThreads) {
     atomicOr(&smask[sidx[i]], 1u << (i / K));
-    if (blockIdx.x == 0) {
+    if (NJ > 0 && blockIdx.x == 0) {
       m.idx[i] = sidx[i];
       m.weights[i] = sw[i];
     }
   }
   __syncthreads();
-  int nu;
+  // Entries: the shared expert's first, then the used experts', each of up to
+  // `turn` of the tokens that take it.
+  const int nsh = S > 0 ? (T + p.turn - 1) / p.turn : 0;
+  if (tid < nsh) {
+    sexp[tid] = kShared;
+    sstart[tid] = (uint16_t)(tid * p.turn);
+    srows[tid] = (uint16_t)min(p.turn, T - tid * p.turn);
+  }
+  int nexp;
   {
-    // thread i: experts 2 i and 2 i + 1; low half: used experts, high half: pairs
-    const uint32_t a = 2 * tid < E ? smask[2 * tid] : 0u;
-    const uint32_t b = 2 * tid + 1 < E ? smask[2 * tid + 1] : 0u;
-    const int va = a ? 1 | (__popc(a) << 16) : 0, vb = b ? 1 | (__popc(b) << 16) : 0;
-    int inc = va + vb;
+    // thread i: experts 4 i to 4 i + 3; low half: entries, high half: pairs
+    int v[4], inc = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = 4 * tid + j < E ? __popc(smask[4 * tid + j]) : 0;
+      v[j] = (n + p.turn - 1) / p.turn | n << 16;
+      inc += v[j];
+    }
+    const int own = inc;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int o = __shfl_up(inc, off, 64);
@@ -186,27 +269,23 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     }
     if (lane == 63) scount[w] = inc;
     __syncthreads();
-    int before = 0, total = 0;
+    int at = inc - own, all = 0;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
-      if (i < w) before += scount[i];
-      total += scount[i];
+      if (i < w) at += scount[i];
+      all += scount[i];
     }
-    nu = total & 0xFFFF;
-    const int at = before + inc - va - vb;
-    if (a) {
-      sexp[at & 0xFFFF] = (uint16_t)(2 * tid);
-      sstart[at & 0xFFFF] = (uint16_t)(at >> 16);
-      sfirst[2 * tid] = at >> 16;
-    }
-    if (b) {
-      sexp[(at + va) & 0xFFFF] = (uint16_t)(2 * tid + 1);
-      sstart[(at + va) & 0xFFFF] = (uint16_t)((at + va) >> 16);
-      sfirst[2 * tid + 1] = (at + va) >> 16;
-    }
-    if (tid == 0) {
-      sstart[nu] = (uint16_t)P;
-      stick = first;
+    nexp = nsh + uniform(all & 0xFFFF);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = v[j] >> 16, first = at >> 16;
+      if (n) sfirst[4 * tid + j] = first;
+      for (int r = 0, u = nsh + (at & 0xFFFF); r < n; r += p.turn, ++u) {
+        sexp[u] = (uint16_t)(4 * tid + j);
+        sstart[u] = (uint16_t)(first + r);
+        srows[u] = (uint16_t)min(p.turn, n - r);
+      }
+      at += v[j];
     }
   }
   __syncthreads();
@@ -214,338 +293,383 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     const int e = sidx[i], t = i / K;
     slist[sfirst[e] + __popc(smask[e] & ((1u << t) - 1u))] = (uint16_t)i;
   }
-  nu = uniform(nu);
-  const int fr = 16 * RG >> gated;  // hidden columns of an up item
-  const int nf = (F + fr - 1) / fr, ns = (S + fr - 1) / fr, nd = D / (16 * RG);
-  const int nup = ns + nu * nf, nexp = nu + (S > 0), total = nup + nexp * nd;
-  int cur = uniform(stick);
-  int next = cur + 1;
-  __syncthreads();  // (the lists; smem is free)
+  const int fr = 16 * WR >> gated;  // hidden columns of an up item
+  const int nf = F / fr, ns = S / fr, nd = D / (16 * WR), nsup = nsh * ns;
+  const int nup = nsup + (nexp - nsh) * nf, ndown = nexp * nd, total = nup + ndown;
+
+  // Wave 0: the item of draw t of the queue, or from a queue that is not empty.
+  auto items_of = [&](int ph, int q) { return (pick(ph != 0, ndown, nup) - q + kQueues - 1) / kQueues; };
+  auto draw = [&](int t) __attribute__((always_inline)) {
+    for (;;) {
+      if (t < items_of(phase, queue)) return (phase ? nup : 0) + t * kQueues + queue;
+      uint64_t some;
+      for (;;) {
+        const int q = lane & (kQueues - 1);
+        const int at = __hip_atomic_load(p.queues + (phase * kQueues + q) * kSpread,
+                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        some = __ballot(lane < kQueues && at < items_of(phase, q));
+        if (some || phase == 1) break;
+        phase = 1;
+      }
+      if (!some) return total;
+      // the next one after the own
+      const uint64_t later = some & (~0ull << queue);
+      queue = __builtin_ctzll(later ? later : some);
+      int got = 0;
+      if (lane == 0)
+        got = __hip_atomic_fetch_add(p.queues + (phase * kQueues + queue) * kSpread, 1,
+                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      t = uniform(got);
+    }
+  };
+  if (w == 0) {
+    // two draws were made at once (an item past the queue's: neither counts)
+    int t = uniform(pending);
+    const bool both = t < items_of(0, queue);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const int a = draw(t);
+      if (lane == 0) stick[i] = a;
+      t = both ? t + 1 : 1 << 30;
+    }
+  }
+  __syncthreads();  // (the lists, too; the room before them is free)
+  int cur = uniform(stick[0]), next = uniform(stick[1]);
+  __syncthreads();
 
   auto item_of = [&](int i) __attribute__((always_inline)) {
     Item it;
-    it.valid = i < total;
     it.down = i >= nup;
-    if (i < ns) {
-      it.u = -1;
-      it.blk = i;
-    } else if (i < nup) {
-      it.u = (i - ns) / nf;
-      it.blk = (i - ns) - it.u * nf;
-    } else {
-      const int j = i - nup;
-      it.u = j / nd - (S > 0);
-      it.blk = j - (j / nd) * nd;
-    }
+    const bool sh = i < nsup;
+    const int j = i - pick(it.down != 0, nup, pick(sh, 0, nsup));
+    const int n = pick(it.down != 0, nd, pick(sh, ns, nf));
+    const int u = j / n;
+    it.blk = j - u * n;
+    it.u = u + pick(it.down || sh, 0, nsh);
+    it.K = pick(it.down != 0, pick(it.u < nsh, S, F), D);
     return it;
   };
-  auto matrix_of = [&](const Item& it) __attribute__((always_inline)) {
-    Matrix x;
-    const int hid = it.u < 0 ? S : F;
-    x.K = it.down ? hid : D;
-    x.rows = it.down ? D : hid;
-    x.w = static_cast<const uint8_t*>(it.u < 0 ? (it.down ? m.sdown : m.sup)
-                                               : (it.down ? m.down : m.up));
-    x.s = static_cast<const uint8_t*>(it.u < 0 ? (it.down ? m.sdown_s : m.sup_s)
-                                               : (it.down ? m.down_s : m.up_s));
-    const size_t e = it.u < 0 ? 0 : uniform(sexp[it.u]);
-    const size_t rows = (size_t)x.rows << (gated && !it.down);
-    x.w += e * rows * (FMT == 0 ? x.K * 2 : FMT == 1 ? x.K / 2 : x.K);
-    if (FMT == 1) x.s += e * rows * (x.K / 32);
-    if (FMT == 2) x.s += e * (rows / 128) * (x.K / 128) * 4;
-    return x;
+  auto lines_of = [&](int k) __attribute__((always_inline)) { return (k + LK - 1) / LK; };
+  const int r16 = lane & 15, kq = lane >> 4;
+
+  Source src;
+  auto enter = [&](const Item& it) __attribute__((always_inline)) {
+    const bool sh = it.u < nsh, down = it.down, two = gated && !down;
+    const int rows = pick(down, D, pick(sh, S, F));  // of one half where gated
+    const int ex = uniform(sexp[it.u]);
+    const size_t e = sh ? 0 : (size_t)ex * ((size_t)rows << two);
+    const uint32_t rb = FMT == 0 ? it.K * 2 : FMT == 1 ? it.K / 2 : it.K;
+    const void* const w0 = pick(sh, pick(down, m.sdown, m.sup), pick(down, m.down, m.up));
+    const void* const s0 = pick(sh, pick(down, m.sdown_s, m.sup_s), pick(down, m.down_s, m.up_s));
+    src.codes = static_cast<const uint8_t*>(w0) + e * rb;
+    // the wave's 16 rows; where gated, eight of the gate's half and the same of
+    // the other
+    const int group = it.blk * WR + wr, first = group * (two ? 8 : 16);
+    const int second = two ? rows + first : first + 8;
+    src.first = first * rb;
+    src.second = second * rb;
+    src.lane = (uint32_t)(lane >> 3) * rb + (lane & 7) * 16;
+    const int sr = it.K / 128;  // scale words of a row (FP8: of 128 rows)
+    if (FMT == 1) {
+      src.scales = static_cast<const uint32_t*>(s0) + e * sr;
+      src.slane = (uint32_t)((r16 < 8 ? first + r16 : second + r16 - 8) * sr) * 4;
+    }
+    if (FMT == 2) {  // of the rows of the lane's results
+      src.scales = static_cast<const uint32_t*>(s0) + e / 128 * sr;
+      src.slane = (uint32_t)(pick(kq < 2, first, second) / 128 * sr) * 4;
+    }
+    src.lines = lines_of(it.K);
+    src.odd = FMT == 1 && it.K % LK != 0;
   };
-  // Row of the matrix that row r (0 .. 15) of group g of a block is: where
-  // gated, rows 0 - 7 are of the gate's half, 8 - 15 the same of the other.
-  auto row_of = [&](const Item& it, const Matrix& x, int g, int r) __attribute__((always_inline)) {
-    if (gated && !it.down) return it.blk * 8 * RG + 8 * g + (r & 7) + (r >= 8 ? x.rows : 0);
-    return it.blk * 16 * RG + 16 * g + r;
+  // Stage st: lines wk + WK (st U + u) of the wave's rows.  (MXFP4: where K ends
+  // in half a line, its second half reads the first one's bytes and scales again,
+  // and x is 0 there.)
+  auto load = [&](Stage& A, int st) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t codes = buffer_rsrc(src.codes);
+    const __amdgpu_buffer_rsrc_t scales = buffer_rsrc(src.scales);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int l = wk + WK * (st * U + u);
+      if (l < src.lines) {
+        const bool half = FMT == 1 && src.odd && l == src.lines - 1;
+        const uint32_t at = half && (lane & 4) ? src.lane - 64 : src.lane;
+        A.l[u][0] = __builtin_amdgcn_raw_buffer_load_b128(codes, at, src.first + l * 128, 2 /* nt */);
+        A.l[u][1] = __builtin_amdgcn_raw_buffer_load_b128(codes, at, src.second + l * 128, 2);
+        if (FMT == 1) {
+          A.s[u][0] = __builtin_amdgcn_raw_buffer_load_b32(scales, src.slane, l * 8, 0);
+          A.s[u][1] = __builtin_amdgcn_raw_buffer_load_b32(scales, src.slane, l * 8 + (half ? 0 : 4), 0);
+        }
+        if (FMT == 2) A.s[u][0] = __builtin_amdgcn_raw_buffer_load_b32(scales, src.slane, l * 4, 0);
+      }
+    }
   };
 
-  const int r16 = lane & 15, kq = lane >> 4;
   const int src0 = (((r16 & 7) << 3) | kq) * 4;
   const int src1 = (((r16 & 7) << 3) | (4 + kq)) * 4;
   const bool lo = r16 < 8;
-
-  struct Stage {
-    u32x4 l[U][RG][2];
-    uint32_t s[U][FMT == 1 ? RG : 1][2];
-  };
-  auto lines_of = [&](int k) __attribute__((always_inline)) { return (k + LK - 1) / LK; };
-  // Stage st: lines w + kWaves (st U + u) of the block's rows.  (MXFP4: where K
-  // ends in half a line, its second half reads the first one's bytes again,
-  // and x is 0 there.)
-  auto load = [&](Stage& A, const Item& it, const Matrix& x, int st) __attribute__((always_inline)) {
-    const int lines = lines_of(x.K);
-    const uint32_t rb = FMT == 0 ? x.K * 2 : FMT == 1 ? x.K / 2 : x.K;
+  f32x4 acc;
+  // Adds stage st to acc; x0: the lane's place in LDS of the first value of its
+  // column's row in line `l0`.
+  auto compute = [&](const Stage& A, int st, int lines, const char* x0, int l0)
+                     __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int l = w + kWaves * (st * U + u);
-      if (l >= lines) break;
-      const bool half = FMT == 1 && l * LK + LK > x.K;
-      const uint32_t at = l * 128 + (half ? lane & 3 : lane & 7) * 16;
-#pragma unroll
-      for (int g = 0; g < RG; ++g) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          A.l[u][g][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
-              x.w + (size_t)((uint32_t)row_of(it, x, g, 8 * h + (lane >> 3)) * rb + at)));
-        if (FMT == 1) {
-          const uint32_t* sp = reinterpret_cast<const uint32_t*>(x.s) +
-                               (uint32_t)row_of(it, x, g, r16) * (uint32_t)(x.K / 128) + 2 * l;
-          A.s[u][g][0] = sp[0];
-          A.s[u][g][1] = sp[half ? 0 : 1];
-        }
-      }
-      if (FMT == 2)  // (a block's groups lie in one block of scales)
-        A.s[u][0][0] = reinterpret_cast<const uint32_t*>(
-            x.s)[(uint32_t)(row_of(it, x, 0, 4 * kq) / 128) * (uint32_t)(x.K / 128) + l];
-    }
-  };
-
-  f32x4 acc[RG];
-  // Adds stage st to acc.  x0: the lane's place in LDS of the first value of the
-  // tokens' rows there (line l0 on), PN parts `plane` bytes apart; `on` is false
-  // for lanes whose token is not among them (multi: only then there are some).
-  auto compute = [&](auto pn, const Stage& A, int K_, int st, int l0, const char* x0, int plane,
-                     bool multi, bool on) __attribute__((always_inline)) {
-    constexpr int PN = decltype(pn)::value;
-    const int lines = lines_of(K_);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int l = w + kWaves * (st * U + u);
-      if (l >= lines) break;
-      u32x4 c[RG][2];
-#pragma unroll
-      for (int g = 0; g < RG; ++g)
+      const int l = wk + WK * (st * U + u);
+      if (l < lines) {
+        u32x4 c[2];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const int a = (int)A.l[u][g][0][d], b = (int)A.l[u][g][1][d];
+          const int a = (int)A.l[u][0][d], b = (int)A.l[u][1][d];
           const int a0 = __builtin_amdgcn_ds_bpermute(src0, a);
           const int b0 = __builtin_amdgcn_ds_bpermute(src0, b);
           const int a1 = __builtin_amdgcn_ds_bpermute(src1, a);
           const int b1 = __builtin_amdgcn_ds_bpermute(src1, b);
-          c[g][0][d] = lo ? a0 : b0;
-          c[g][1][d] = lo ? a1 : b1;
+          c[0][d] = lo ? a0 : b0;
+          c[1][d] = lo ? a1 : b1;
         }
-      f32x4 blk[RG];
+        const char* const xl = x0 + (l - l0) * (LK * 2);
+        f32x4 sum = FMT == 2 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc;
 #pragma unroll
-      for (int g = 0; g < RG; ++g) blk[g] = FMT == 2 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[g];
-      const char* xl = x0 + (l - l0) * LK * 2;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < NF; ++i) {
-          bf16x8 xf[PN];
-#pragma unroll
-          for (int q = 0; q < PN; ++q) {
-            xf[q] = *reinterpret_cast<const bf16x8*>(xl + q * plane + h * 64 * NF + i * 16);
-            if (multi && !on) xf[q] = zero8();
-          }
-#pragma unroll
-          for (int g = 0; g < RG; ++g) {
+          for (int i = 0; i < NF; ++i) {
             bf16x8 wf;
             if (FMT == 0) {
-              wf = __builtin_bit_cast(bf16x8, c[g][h]);
+              wf = __builtin_bit_cast(bf16x8, c[h]);
             } else if (FMT == 1) {
-              wf = mx_decode8(c[g][h][i], mx_scale((A.s[u][g][h] >> (8 * kq)) & 255u));
+              wf = mx_decode8(c[h][i], mx_scale((A.s[u][h] >> (8 * kq)) & 255u));
             } else {
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
+              for (int d = 0; d < 2; ++d) {
                 const auto v0 =
-                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[g][h][2 * i + j], 1.f, false);
+                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, false);
                 const auto v1 =
-                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[g][h][2 * i + j], 1.f, true);
-                wf[4 * j] = v0[0], wf[4 * j + 1] = v0[1];
-                wf[4 * j + 2] = v1[0], wf[4 * j + 3] = v1[1];
+                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, true);
+                wf[4 * d] = v0[0], wf[4 * d + 1] = v0[1];
+                wf[4 * d + 2] = v1[0], wf[4 * d + 3] = v1[1];
               }
             }
-#pragma unroll
-            for (int q = 0; q < PN; ++q) blk[g] = mfma_bf16(wf, xf[q], blk[g]);
+            sum = mfma_bf16(wf, *reinterpret_cast<const bf16x8*>(xl + h * 64 * NF + i * 16), sum);
           }
-        }
-#pragma unroll
-      for (int g = 0; g < RG; ++g)
-        acc[g] = FMT == 2 ? acc[g] + blk[g] * __uint_as_float(A.s[u][0][0]) : blk[g];
-    }
-  };
-
-  // Rows r0 .. r0 + n - 1 of the item's tokens (x, or hidden rows), values k0 ..
-  // k0 + kn - 1, into LDS as parts of bf16; zeros from K on.
-  auto put_rows = [&](const Item& it, int K_, int r0, int n, int k0, int kn, int pitch, int plane,
-                      int parts) __attribute__((always_inline)) {
-    for (int r = 0; r < n; ++r) {
-      const int pair = it.u < 0 ? r0 + r : slist[sstart[it.u] + r0 + r];
-      const int t = it.u < 0 ? pair : pair / K;
-      const float* hrow = it.u < 0 ? p.hs + (size_t)pair * S : p.h + (size_t)pair * F;
-      for (int k = tid * 4; k < kn; k += kThreads * 4) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (k0 + k < K_) {
-          if (it.down) v = load4(hrow + k0 + k);
-          else if (m.x_bf16) v = load4(static_cast<const uint16_t*>(m.x) + t * m.x_stride + k0 + k);
-          else v = load4(static_cast<const float*>(m.x) + t * m.x_stride + k0 + k);
-        }
-        char* const to = smem + r * pitch + k * 2;
-        for (int q = 0; q < parts; ++q) {
-          const u16x4 b = pack4_bf16(v);
-          *reinterpret_cast<u16x4*>(to + q * plane) = b;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] -= bf16_to_f32(b[i]);
-        }
+        acc = FMT == 2 ? acc + sum * __uint_as_float(A.s[u][0]) : sum;
       }
     }
   };
 
-  f32x4* const red = reinterpret_cast<f32x4*>(smem + kXBytes);  // [kWaves][RG][64]
+  // The item's tokens' rows (x, or hidden rows), values k0 .. k0 + kn - 1, into
+  // LDS as `parts` bf16 numbers each; zeros from K on.
+  auto put_rows = [&](const Item& it, int r0, int rows, int k0, int kn, int pitch, int parts)
+                      __attribute__((always_inline)) {
+    const bool sh = it.u < nsh;
+    constexpr int N = 5;
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r) {
+      const int pair = uniform(sh ? r0 + r : slist[r0 + r]);
+      const size_t row = it.down || sh ? pair : pair / K;
+      const float* const hp = pick(sh, p.hs, p.h) + row * it.K;
+      const size_t xo = row * m.x_stride;
+      char* const to = smem + r * parts * pitch;
+#pragma unroll 1
+      for (int k = tid * 4; k < kn; k += N * kThreads * 4) {
+        f32x4 v[N];
+        // (past the row's end: its last values again, which are not put)
+        const auto at = [&](int j) { return (uint32_t)min(k0 + k + j * kThreads * 4, it.K - 4); };
+        if (it.down) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[j] = get4_shared(hp + at(j));
+        } else if (m.x_bf16) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[j] = load4(static_cast<const uint16_t*>(m.x) + xo + at(j));
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[j] = load4(static_cast<const float*>(m.x) + xo + at(j));
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int kj = k + j * kThreads * 4;
+          if (k0 + kj >= it.K) v[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (kj < kn) {
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+              if (q < parts) {
+                const u16x4 b = pack4_bf16(v[j]);
+                *reinterpret_cast<u16x4*>(to + q * pitch + kj * 2) = b;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) v[j][n] -= bf16_to_f32(b[n]);
+              }
+            }
+          }
+        }
+      }
+    }
+  };
+  // Until the flags of an entry's hidden rows are all set (bounded, about ten
+  // seconds: should one ever be lost, the result is wrong, but the kernel ends).
+  auto flags_of = [&](int u) __attribute__((always_inline)) {
+    return pick(u < nsh, u * ns, nsup + (u - nsh) * nf) * WR;
+  };
+  auto wait_hidden = [&](int u) __attribute__((always_inline)) {
+    const int n = pick(u < nsh, ns, nf) * WR;
+    const int32_t* const flags = p.up_done + flags_of(u);
+#pragma unroll 1
+    for (int tries = 0; tries < (1 << 22); ++tries) {
+      int ok = 1;
+      for (int i = tid; i < n; i += kThreads)
+        ok &= __hip_atomic_load(flags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (__syncthreads_and(ok)) break;
+    }
+  };
+
   Stage A, B;
   Item it = item_of(cur);
-  Matrix x = it.valid ? matrix_of(it) : Matrix{};
-  if (it.valid) load(A, it, x, 0);
-  while (it.valid) {
-    int pending = 0;
+  if (cur < total) {
+    enter(it);
+    load(A, 0);
+  }
+  int staged = -1;  // whose rows are in LDS, all of them
+  int parity = 0;
+#pragma unroll 1
+  while (cur < total) {
     if (tid == 0)
-      pending = __hip_atomic_fetch_add(p.next, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const Item nit = item_of(next);
-    const Matrix nx = nit.valid ? matrix_of(nit) : Matrix{};
-    const int r0 = it.u < 0 ? 0 : uniform(sstart[it.u]);
-    const int rows = it.u < 0 ? T : uniform(sstart[it.u + 1]) - r0;
-    const int parts = !it.down && m.x_bf16 ? 1 : 3;
-    const int lines = lines_of(x.K);
-    const int stages = (lines + LANES - 1) / LANES;
-    // stages whose rows fit LDS at a time; where not even one does, a stage's
-    // rows take turns (the products of the others' columns are with zeros)
-    const int per = LANES * LK * 2;
-    int chunk = (kXBytes / (rows * parts) - 16) / per;
-    int turn = rows;
-    if (chunk < 1) {
-      chunk = 1;
-      turn = kXBytes / (parts * (per + 16));
-    }
-    chunk = min(chunk, stages);
-    const bool multi = turn < rows;
-    const int pitch = min(chunk * LANES, lines) * LK * 2 + 16, plane = turn * pitch;
-#pragma unroll
-    for (int g = 0; g < RG; ++g) acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+      pending = __hip_atomic_fetch_add(p.queues + (phase * kQueues + queue) * kSpread, 1,
+                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const bool sh = it.u < nsh;
+    const int r0 = uniform(sstart[it.u]), rows = uniform(srows[it.u]);
+    const int parts = !it.down && m.x_bf16 ? 1 : (m.y_bf16 ? 2 : 3);
+    const int cols = rows * parts;
+    const int lines = src.lines, subs = (lines + WK - 1) / WK, stages = (subs + U - 1) / U;
+    // pairs of stages whose rows fit LDS at a time (at least one)
+    constexpr int per = 2 * U * WK * LK * 2;
+    const int chunk = min((p.xbytes / cols - 16) / per, (stages + 1) / 2);
+    const int pitch = min(chunk * per, lines * LK * 2) + 16;
+    // one token's x is the same for every expert
+    const bool all = 2 * chunk >= stages;
+    const int whose = it.down ? it.u + 1 : (T == 1 ? 0 : -2 - it.u);
+    const bool keep = all && whose == staged;
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    const char* const xat = smem + (r16 < cols ? r16 : 0) * pitch + kq * NF * 16;
+    Item nit = it;
 
-    auto step = [&](const Stage& Cur, Stage& Nxt, int st) __attribute__((always_inline)) {
-      const int in = st % chunk;
-      for (int b = 0; b < rows; b += turn) {
-        const int n = min(turn, rows - b);
-        if (in == 0) {
-          if (st == 0 && b == 0 && it.down) {
-            // the expert's hidden rows, all of them
-            if (tid == 0) {
-              // (bounded, about ten seconds: should a counter ever be wrong, the
-              // result is, too, but the kernel ends)
-              const int want = RG * (it.u < 0 ? ns : nf);
-              for (int n = 0; n < (1 << 23); ++n) {
-                if (__hip_atomic_load(p.up_done + it.u + 1, __ATOMIC_RELAXED,
-                                      __HIP_MEMORY_SCOPE_AGENT) >= want)
-                  break;
-                __builtin_amdgcn_s_sleep(1);
-              }
-            }
-            __syncthreads();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-          } else {
-            __syncthreads();  // what is there has been read
-          }
-          const int k0 = st * LANES * LK;
-          put_rows(it, x.K, b, n, k0, min(chunk * LANES * LK, lines * LK - k0), pitch, plane,
-                   parts);
-          __syncthreads();
-        }
-        if (b == 0) {
-          if (st + 1 < stages) load(Nxt, it, x, st + 1);
-          else if (st == stages - 1 && (stages & 1) == 0 && nit.valid) load(Nxt, nit, nx, 0);
-        }
-        const bool on = r16 >= b && r16 < b + n;
-        const char* const x0 = smem + (on ? r16 - b : 0) * pitch + kq * NF * 16;
-        const int l0 = (st - in) * LANES;
-        if (parts == 1)
-          compute(std::integral_constant<int, 1>{}, Cur, x.K, st, l0, x0, plane, multi, on);
-        else
-          compute(std::integral_constant<int, 3>{}, Cur, x.K, st, l0, x0, plane, multi, on);
-      }
-    };
+    int in = 0, l0 = 0;  // pairs of stages in this chunk, its first line
+#pragma unroll 1
     for (int st = 0; st < stages; st += 2) {
-      step(A, B, st);
-      if (st + 1 < stages) step(B, A, st + 1);
+      if (in == 0 && !keep) {
+        if (it.down && st == 0) wait_hidden(it.u);
+        else if (st > 0) __syncthreads();  // what is there has been read
+        l0 = st * U * WK;
+        put_rows(it, r0, rows, l0 * LK, min(chunk * (per / 2), (lines - l0) * LK), pitch, parts);
+        __syncthreads();
+      }
+      in = in + 1 == chunk ? 0 : in + 1;
+      if (st + 1 < stages) load(B, st + 1);
+      compute(A, st, lines, xat, l0);
+      int ahead = st + 2;
+      if (ahead >= stages && next < total) {
+        nit = item_of(next);
+        enter(nit);
+        ahead = 0;
+      }
+      if (ahead < stages || next < total) load(A, ahead);
+      if (st + 1 < stages) compute(B, st + 1, lines, xat, l0);
     }
-    // (an odd number of stages: A was the last one read)
-    if ((stages & 1) && nit.valid) load(A, nit, nx, 0);
+    staged = all ? whose : -1;
 
-#pragma unroll
-    for (int g = 0; g < RG; ++g) red[(w * RG + g) * 64 + lane] = acc[g];
-    if (tid == 0) stick = pending;
+    // the waves' sums (two places in turn: the last item's may still be read)
+    f32x4* const red = reinterpret_cast<f32x4*>(smem + p.xbytes) + parity * kThreads;
+    red[tid] = acc;
+    if (w == 0) {
+      const int d = draw(uniform(pending));
+      if (lane == 0) stick[parity] = d;
+    }
     __syncthreads();
-    if (w < RG) {
-      const int g = w;
-      f32x4 v = red[g * 64 + lane];
+    const int after = uniform(stick[parity]);
+    parity ^= 1;
+    if (wk == 0) {
+      // lane (r, q): columns 4 q .. + 3 of token row r
+      const int r = lane >> 2, q = lane & 3;
+      const bool live = r < rows;
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int i = 0; i < parts; ++i) {
 #pragma unroll
-      for (int i = 1; i < kWaves; ++i) v += red[(i * RG + g) * 64 + lane];
-      const bool live = r16 < rows;
-      const int pair = it.u < 0 ? r16 : (live ? slist[r0 + r16] : 0);
+        for (int j = 0; j < WK; ++j)
+          v += red[(w + j) * 64 + q * 16 + (live ? r * parts + i : 0)];
+      }
+      const int pair = live ? (sh ? r0 + r : slist[r0 + r]) : 0;
+      const int group = it.blk * WR + wr;
       if (!it.down) {
-        float* const hrow = it.u < 0 ? p.hs + (size_t)pair * S : p.h + (size_t)pair * F;
+        float* const hrow = pick(sh, p.hs, p.h) + (size_t)pair * pick(sh, S, F);
         f32x4 o;
-        int col;
         if (gated) {
-          f32x4 b;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            b[i] = __shfl_xor(v[i], 32, 64);
-            o[i] = v[i] / (1.f + expf(-v[i])) * b[i];
-          }
-          col = it.blk * fr + 8 * g + 4 * kq;
+          for (int i = 0; i < 4; ++i)
+            o[i] = v[i] / (1.f + expf(-v[i])) * __shfl_xor(v[i], 2, 64);
+          if (live && q < 2) put4_shared(hrow + group * 8 + 4 * q, o);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[i] = relu_sq(v[i]);
-          col = it.blk * fr + 16 * g + 4 * kq;
+          if (live) put4_shared(hrow + group * 16 + 4 * q, o);
         }
-        if (live && (!gated || kq < 2)) *reinterpret_cast<f32x4*>(hrow + col) = o;
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+        stores_done();
         if (lane == 0)
-          __hip_atomic_fetch_add(p.up_done + it.u + 1, 1, __ATOMIC_RELAXED,
-                                 __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(p.up_done + flags_of(it.u) + group, 1, __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
       } else {
-        const int block = it.blk * RG + g, n0 = block * 16;
-        float* const orow = p.o + (size_t)(it.u < 0 ? P + pair : pair) * D + n0;
+        const int n0 = group * 16;
         if (live)
-          *reinterpret_cast<f32x4*>(orow + 4 * kq) = v * (it.u < 0 ? 1.f : sw[pair]);
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+          put4_shared(p.o + (size_t)(sh ? P + pair : pair) * D + n0 + 4 * q,
+                      v * (sh ? 1.f : sw[pair]));
+        stores_done();
         int before = 0;
         if (lane == 0)
-          before = __hip_atomic_fetch_add(p.down_done + block, 1, __ATOMIC_RELAXED,
+          before = __hip_atomic_fetch_add(p.down_done + group * kSpread, 1, __ATOMIC_RELAXED,
                                           __HIP_MEMORY_SCOPE_AGENT);
         if (uniform(before) == nexp - 1) {
-          // all pairs' rows of these columns are there: add them, k ascending
-          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-          for (int t = kq; t < T; t += 4) {
-            const float* at = p.o + n0 + r16;
+          // all pairs' rows of these columns are there: a lane adds every fourth
+          // of a token's, then the four sums are added
+#pragma unroll 1
+          for (int t = 0; t < T; ++t) {
+            const float* const at = p.o + n0 + r16;
             float s = 0.f;
-            for (int k = 0; k < K; ++k) s += at[(size_t)(t * K + k) * D];
-            if (S > 0) s += at[(size_t)(P + t) * D];
+#pragma unroll 1
+            for (int k0 = kq; k0 < K; k0 += 32) {
+              float a[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                a[i] = get1_shared(at + (size_t)(t * K + min(k0 + 4 * i, K - 1)) * D);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) s += k0 + 4 * i < K ? a[i] : 0.f;
+            }
+            if (S > 0 && kq == 3) s += get1_shared(at + (size_t)(P + t) * D);
+            s += __shfl_xor(s, 16, 64);
+            s += __shfl_xor(s, 32, 64);
             const size_t to = (size_t)t * D + n0 + r16;
-            if (m.y_bf16) static_cast<uint16_t*>(m.y)[to] = f32_to_bf16(s);
-            else static_cast<float*>(m.y)[to] = s;
+            if (kq == 0) {
+              if (m.y_bf16) static_cast<uint16_t*>(m.y)[to] = f32_to_bf16(s);
+              else static_cast<float*>(m.y)[to] = s;
+            }
           }
         }
       }
     }
     cur = next;
-    next = uniform(stick);
+    next = after;
     it = nit;
-    x = nx;
-    __syncthreads();
   }
 }
 
 namespace {
 
+template <class F>
+void with_format(int format, F f) {
+  if (format == 0) f(std::integral_constant<int, 0>{});
+  else if (format == 1) f(std::integral_constant<int, 1>{});
+  else f(std::integral_constant<int, 2>{});
+}
+
 struct Layout {
   size_t sync, logits, h, hs, o, total;
-  int nsync;
+  int nsync, up_done, down_done;  // ints: counters and flags, and where they begin
 };
 Layout layout(const MoeTokens& m) {
   Layout l{};
@@ -555,18 +679,19 @@ Layout layout(const MoeTokens& m) {
     return at;
   };
   const size_t pairs = (size_t)m.T * m.r.K;
-  l.nsync = 64 + m.r.E + 1 + m.D / 16;
+  const size_t used = pairs < (size_t)m.r.E ? pairs : m.r.E;
+  l.down_done = 2 * kQueues * kSpread;
+  l.up_done = l.down_done + m.D / 16 * kSpread;
+  // a flag for each 8 (gated) or 16 hidden columns of an entry (of five rows or
+  // more, and one more an expert)
+  const size_t entries = used + pairs / 5, shared = m.S ? 1 + m.T / 5 : 0;
+  l.nsync = l.up_done + (int)((entries * m.F + shared * m.S) / (m.gated ? 8 : 16));
   l.sync = take((size_t)l.nsync * 4);
   l.logits = take((size_t)m.T * m.r.E * 4);
   l.h = take(pairs * m.F * 4);
   l.hs = take((size_t)m.T * m.S * 4);
   l.o = take((pairs + (m.S ? m.T : 0)) * m.D * 4);
   return l;
-}
-
-template <int FMT, int NJ>
-void launch(const MoeParams& p, int grid, hipStream_t s) {
-  moe_tokens_kernel<FMT, NJ><<<grid, kThreads, 0, s>>>(p);
 }
 
 }  // namespace
@@ -577,37 +702,55 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const Layout l = layout(m);
   char* const ws = static_cast<char*>(workspace);
   int32_t* const sync = reinterpret_cast<int32_t*>(ws + l.sync);
+  const int P = m.T * m.r.K, E = m.r.E;
+  // LDS: the tokens' rows and the waves' sums, in whose room the tokens are
+  // routed before; then the lists
+  const bool here = m.T <= kRouteHere && E <= 512;
+  const int nj = !here ? 0 : (E <= 128 ? 2 : 8);
+  const int route = kRouteHere * (256 + nj * 512) + 8 * E + 4 * P;
+  const int turn = 16 / (m.y_bf16 ? 2 : 3);
+  const int cols = (m.T < turn ? m.T : turn) * (m.y_bf16 ? 2 : 3);
+  const int red = 2 * kThreads * 16, lists = 12 * P + 160;
+  // four work-groups a CU where the rows allow it: 40 KB each
+  const int least = cols * (2048 + 16), left = 40 * 1024 - red - lists;
+  const int xbytes = (left > least ? left : least) / 16 * 16;
+  const int work = xbytes + red;
   MoeParams p{m,
               reinterpret_cast<float*>(ws + l.logits),
               reinterpret_cast<float*>(ws + l.h),
               reinterpret_cast<float*>(ws + l.hs),
               reinterpret_cast<float*>(ws + l.o),
               sync,
-              sync + 64,
-              sync + 64 + m.r.E + 1};
+              sync + l.up_done,
+              sync + l.down_done,
+              turn,
+              xbytes,
+              ((route > work ? route : work) + 15) / 16 * 16};
+  const int lds = p.misc + lists;
   auto logits = [&](auto g, auto x) {
     using GT = decltype(g);
     using XT = decltype(x);
-    moe_logits_kernel<GT, XT><<<m.r.E, 256, 0, s>>>(
-        static_cast<const XT*>(m.x), m.x_stride, static_cast<const GT*>(m.gate), m.T, m.r.E, m.D,
+    moe_logits_kernel<GT, XT><<<E, 256, 0, s>>>(
+        static_cast<const XT*>(m.x), m.x_stride, static_cast<const GT*>(m.gate), m.T, E, m.D,
         p.logits, sync, l.nsync);
   };
   if (m.gate_bf16 && m.x_bf16) logits(uint16_t{}, uint16_t{});
   else if (m.gate_bf16) logits(uint16_t{}, float{});
   else if (m.x_bf16) logits(float{}, uint16_t{});
   else logits(float{}, float{});
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int grid = 512;
-  auto go = [&](auto fmt) {
+  if (!here) {
+    e = route_logits(m.r, p.logits, false, m.bias, m.idx, m.weights, s);
+    if (e != hipSuccess) return e;
+  }
+  constexpr int grid = 1024;
+  with_format(m.format, [&](auto fmt) {
     constexpr int FMT = decltype(fmt)::value;
-    if (m.r.E <= 128) launch<FMT, 2>(p, grid, s);
-    else if (m.r.E <= 512) launch<FMT, 8>(p, grid, s);
-    else launch<FMT, 16>(p, grid, s);
-  };
-  if (m.format == 0) go(std::integral_constant<int, 0>{});
-  else if (m.format == 1) go(std::integral_constant<int, 1>{});
-  else go(std::integral_constant<int, 2>{});
+    if (nj == 0) moe_tokens_kernel<FMT, 0><<<grid, kThreads, lds, s>>>(p);
+    else if (nj == 2) moe_tokens_kernel<FMT, 2><<<grid, kThreads, lds, s>>>(p);
+    else moe_tokens_kernel<FMT, 8><<<grid, kThreads, lds, s>>>(p);
+  });
   return hipGetLastError();
 }
 
