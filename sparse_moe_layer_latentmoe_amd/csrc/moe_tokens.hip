@@ -23,8 +23,8 @@
 // by the wave that finishes a block of columns last, in a fixed order: the same
 // bits every time.
 //
-// Weights are the MFMA's A operand, read from HBM as whole lines into registers
-// two stages ahead (across items), brought into its layout by ds_bpermute and
+// Weights are the MFMA's A operand, read from HBM as whole lines into registers,
+// kAhead lines ahead (on into the next block), brought into its layout by ds_bpermute and
 // decoded exactly to bf16 (8-bit: the block's scale on its sum).  The tokens'
 // operand is bf16, too: a value that is no bf16 number (fp32 x, the hidden rows)
 // is the sum of two such parts (y in bf16: 16 bits, its error far below y's
@@ -51,7 +51,7 @@ namespace {
 constexpr int kWaves = 4, kThreads = kWaves * 64;
 constexpr int kQueues = 16, kSpread = 64;  // counters, ints apart
 constexpr int kRouteHere = 4;              // tokens that every work-group routes
-constexpr int kLines = 2;                  // lines a wave loads at a time (a stage)
+constexpr int kAhead = 3;                  // lines that a wave loads ahead
 
 // Formats: k values in a line of 128 bytes, fragments of 8 values in 16 bytes,
 // waves that share a row group of 16 (each takes every WK-th line).  Items are 16
@@ -181,9 +181,9 @@ struct Source {
   int lines, odd;        // of the item; the last is half a line
 };
 
-struct Stage {
-  u32x4 l[kLines][2];
-  uint32_t s[kLines][2];
+struct Line {
+  u32x4 l[2];  // of the first and the last eight rows
+  uint32_t s[2];
 };
 
 constexpr int kShared = 0xFFFF;  // an entry of the shared expert
@@ -194,7 +194,7 @@ constexpr int kShared = 0xFFFF;  // an entry of the shared expert
 template <int FMT, int NJ>
 __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   using C = Fmt<FMT>;
-  constexpr int LK = C::LK, NF = C::NF, WK = C::WK, WR = kWaves / WK, U = kLines;
+  constexpr int LK = C::LK, NF = C::NF, WK = C::WK, WR = kWaves / WK, NL = kAhead + 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
 
   const MoeTokens& m = p.m;
@@ -208,10 +208,10 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   // ---- routing and the list of used experts, in every work-group ----
   int pending = 0;
   if (tid == 0)
-    pending = __hip_atomic_fetch_add(p.queues + queue * kSpread, 2, __ATOMIC_RELAXED,
+    pending = __hip_atomic_fetch_add(p.queues + queue * kSpread, 1, __ATOMIC_RELAXED,
                                      __HIP_MEMORY_SCOPE_AGENT);
-  int* const stick = reinterpret_cast<int*>(smem + p.misc);     // [2] drawn items
-  int* const scount = stick + 2;                                // [kWaves]
+  int* const stick = reinterpret_cast<int*>(smem + p.misc);     // [2][2] drawn runs
+  int* const scount = stick + 4;                                // [kWaves]
   float* const sw = reinterpret_cast<float*>(scount + kWaves);  // [P] pairs' weights
   uint16_t* const slist = reinterpret_cast<uint16_t*>(sw + P);  // [P] pairs by expert
   // entries: expert, first of its pairs in the list, their number
@@ -297,21 +297,41 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   const int nf = F / fr, ns = S / fr, nd = D / (16 * WR), nsup = nsh * ns;
   const int nup = nsup + (nexp - nsh) * nf, ndown = nexp * nd, total = nup + ndown;
 
-  // Wave 0: the item of draw t of the queue, or from a queue that is not empty.
-  auto items_of = [&](int ph, int q) { return (pick(ph != 0, ndown, nup) - q + kQueues - 1) / kQueues; };
-  auto draw = [&](int t) __attribute__((always_inline)) {
+  // Runs of blocks: the first gridDim.x of a projection are long and cover three
+  // quarters of it, the others are short.
+  auto long_run = [&](int ph) __attribute__((always_inline)) {
+    return min(max(pick(ph != 0, ndown, nup) * 3 / 4 / (int)gridDim.x, 1), 64);
+  };
+  auto run_at = [&](int ph, int n) __attribute__((always_inline)) {  // first block of run n
+    const int g = (int)gridDim.x, len = long_run(ph), over = max(n - g, 0);
+    return min(n, g) * len + over * ((len + 3) / 4);
+  };
+  // Wave 0: the run of draw t of the queue, or from a queue that is not empty.
+  auto draw = [&](int t, int* to) __attribute__((always_inline)) {
     for (;;) {
-      if (t < items_of(phase, queue)) return (phase ? nup : 0) + t * kQueues + queue;
+      const int end = pick(phase != 0, ndown, nup), base = pick(phase != 0, nup, 0);
+      const int n = t * kQueues + queue, from = run_at(phase, min(n, end));
+      if (from < end) {
+        if (lane == 0) {
+          to[0] = base + from;
+          to[1] = base + min(run_at(phase, n + 1), end);
+        }
+        return;
+      }
       uint64_t some;
       for (;;) {
         const int q = lane & (kQueues - 1);
         const int at = __hip_atomic_load(p.queues + (phase * kQueues + q) * kSpread,
                                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        some = __ballot(lane < kQueues && at < items_of(phase, q));
+        const int end = pick(phase != 0, ndown, nup);
+        some = __ballot(lane < kQueues && run_at(phase, min(at * kQueues + q, end)) < end);
         if (some || phase == 1) break;
         phase = 1;
       }
-      if (!some) return total;
+      if (!some) {
+        if (lane == 0) to[0] = to[1] = total;
+        return;
+      }
       // the next one after the own
       const uint64_t later = some & (~0ull << queue);
       queue = __builtin_ctzll(later ? later : some);
@@ -322,20 +342,9 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
       t = uniform(got);
     }
   };
-  if (w == 0) {
-    // two draws were made at once (an item past the queue's: neither counts)
-    int t = uniform(pending);
-    const bool both = t < items_of(0, queue);
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      const int a = draw(t);
-      if (lane == 0) stick[i] = a;
-      t = both ? t + 1 : 1 << 30;
-    }
-  }
+  if (w == 0) draw(uniform(pending), stick);
   __syncthreads();  // (the lists, too; the room before them is free)
-  int cur = uniform(stick[0]), next = uniform(stick[1]);
-  __syncthreads();
+  int cur = uniform(stick[0]), end = uniform(stick[1]);  // the run
 
   auto item_of = [&](int i) __attribute__((always_inline)) {
     Item it;
@@ -381,26 +390,27 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     src.lines = lines_of(it.K);
     src.odd = FMT == 1 && it.K % LK != 0;
   };
-  // Stage st: lines wk + WK (st U + u) of the wave's rows.  (MXFP4: where K ends
-  // in half a line, its second half reads the first one's bytes and scales again,
-  // and x is 0 there.)
-  auto load = [&](Stage& A, int st) __attribute__((always_inline)) {
+  // Line j of the wave's: wk + WK j of its rows.  (MXFP4: where K ends in half a
+  // line, its second half reads the first one's bytes and scales again, and x is
+  // 0 there.)  The loads are always issued, out of the buffers' bounds where there
+  // is no such line (nothing is fetched then): behind a branch, the compiler
+  // would have to wait for all loads in flight wherever it waits for one.
+  auto load = [&](Line& A, int j, bool some) __attribute__((always_inline)) {
+    const int l = wk + WK * j;
+    const bool on = some && l < src.lines;
     const __amdgpu_buffer_rsrc_t codes = buffer_rsrc(src.codes);
-    const __amdgpu_buffer_rsrc_t scales = buffer_rsrc(src.scales);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int l = wk + WK * (st * U + u);
-      if (l < src.lines) {
-        const bool half = FMT == 1 && src.odd && l == src.lines - 1;
-        const uint32_t at = half && (lane & 4) ? src.lane - 64 : src.lane;
-        A.l[u][0] = __builtin_amdgcn_raw_buffer_load_b128(codes, at, src.first + l * 128, 2 /* nt */);
-        A.l[u][1] = __builtin_amdgcn_raw_buffer_load_b128(codes, at, src.second + l * 128, 2);
-        if (FMT == 1) {
-          A.s[u][0] = __builtin_amdgcn_raw_buffer_load_b32(scales, src.slane, l * 8, 0);
-          A.s[u][1] = __builtin_amdgcn_raw_buffer_load_b32(scales, src.slane, l * 8 + (half ? 0 : 4), 0);
-        }
-        if (FMT == 2) A.s[u][0] = __builtin_amdgcn_raw_buffer_load_b32(scales, src.slane, l * 4, 0);
-      }
+    const bool half = FMT == 1 && src.odd && l == src.lines - 1;
+    const uint32_t at = on ? (half && (lane & 4) ? src.lane - 64 : src.lane) : 0x80000000u;
+    const int to = pick(on, l, 0) * 128;
+    A.l[0] = __builtin_amdgcn_raw_buffer_load_b128(codes, at, src.first + to, 2 /* nt */);
+    A.l[1] = __builtin_amdgcn_raw_buffer_load_b128(codes, at, src.second + to, 2);
+    if (FMT != 0) {
+      const __amdgpu_buffer_rsrc_t scales = buffer_rsrc(src.scales);
+      const uint32_t sat = on ? src.slane : 0x80000000u;
+      const int st = pick(on, l, 0) * (FMT == 1 ? 8 : 4);
+      A.s[0] = __builtin_amdgcn_raw_buffer_load_b32(scales, sat, st, 0);
+      if (FMT == 1)
+        A.s[1] = __builtin_amdgcn_raw_buffer_load_b32(scales, sat, st + (half ? 0 : 4), 0);
     }
   };
 
@@ -408,51 +418,46 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   const int src1 = (((r16 & 7) << 3) | (4 + kq)) * 4;
   const bool lo = r16 < 8;
   f32x4 acc;
-  // Adds stage st to acc; x0: the lane's place in LDS of the first value of its
+  // Adds line j to acc; x0: the lane's place in LDS of the first value of its
   // column's row in line `l0`.
-  auto compute = [&](const Stage& A, int st, int lines, const char* x0, int l0)
+  auto compute = [&](const Line& A, int j, int lines, const char* x0, int l0)
                      __attribute__((always_inline)) {
+    const int l = wk + WK * j;
+    if (l < lines) {
+      u32x4 c[2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int l = wk + WK * (st * U + u);
-      if (l < lines) {
-        u32x4 c[2];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const int a = (int)A.l[u][0][d], b = (int)A.l[u][1][d];
-          const int a0 = __builtin_amdgcn_ds_bpermute(src0, a);
-          const int b0 = __builtin_amdgcn_ds_bpermute(src0, b);
-          const int a1 = __builtin_amdgcn_ds_bpermute(src1, a);
-          const int b1 = __builtin_amdgcn_ds_bpermute(src1, b);
-          c[0][d] = lo ? a0 : b0;
-          c[1][d] = lo ? a1 : b1;
-        }
-        const char* const xl = x0 + (l - l0) * (LK * 2);
-        f32x4 sum = FMT == 2 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < NF; ++i) {
-            bf16x8 wf;
-            if (FMT == 0) {
-              wf = __builtin_bit_cast(bf16x8, c[h]);
-            } else if (FMT == 1) {
-              wf = mx_decode8(c[h][i], mx_scale((A.s[u][h] >> (8 * kq)) & 255u));
-            } else {
-#pragma unroll
-              for (int d = 0; d < 2; ++d) {
-                const auto v0 =
-                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, false);
-                const auto v1 =
-                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, true);
-                wf[4 * d] = v0[0], wf[4 * d + 1] = v0[1];
-                wf[4 * d + 2] = v1[0], wf[4 * d + 3] = v1[1];
-              }
-            }
-            sum = mfma_bf16(wf, *reinterpret_cast<const bf16x8*>(xl + h * 64 * NF + i * 16), sum);
-          }
-        acc = FMT == 2 ? acc + sum * __uint_as_float(A.s[u][0]) : sum;
+      for (int d = 0; d < 4; ++d) {
+        const int a = (int)A.l[0][d], b = (int)A.l[1][d];
+        const int a0 = __builtin_amdgcn_ds_bpermute(src0, a);
+        const int b0 = __builtin_amdgcn_ds_bpermute(src0, b);
+        const int a1 = __builtin_amdgcn_ds_bpermute(src1, a);
+        const int b1 = __builtin_amdgcn_ds_bpermute(src1, b);
+        c[0][d] = lo ? a0 : b0;
+        c[1][d] = lo ? a1 : b1;
       }
+      const char* const xl = x0 + (l - l0) * (LK * 2);
+      f32x4 sum = FMT == 2 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          bf16x8 wf;
+          if (FMT == 0) {
+            wf = __builtin_bit_cast(bf16x8, c[h]);
+          } else if (FMT == 1) {
+            wf = mx_decode8(c[h][i], mx_scale((A.s[h] >> (8 * kq)) & 255u));
+          } else {
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, false);
+              const auto v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, true);
+              wf[4 * d] = v0[0], wf[4 * d + 1] = v0[1];
+              wf[4 * d + 2] = v1[0], wf[4 * d + 3] = v1[1];
+            }
+          }
+          sum = mfma_bf16(wf, *reinterpret_cast<const bf16x8*>(xl + h * 64 * NF + i * 16), sum);
+        }
+      acc = FMT == 2 ? acc + sum * __uint_as_float(A.s[0]) : sum;
     }
   };
 
@@ -520,70 +525,82 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     }
   };
 
-  Stage A, B;
+  Line buf[NL];
   Item it = item_of(cur);
   if (cur < total) {
     enter(it);
-    load(A, 0);
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) load(buf[q], q, true);
   }
-  int staged = -1;  // whose rows are in LDS, all of them
-  int parity = 0;
+  int run = cur;             // the first of the run's blocks
+  int next = -1, nend = -1;  // the run after it; -1: not drawn, total: none
+  int staged = -1;           // whose rows are in LDS, all of them
+  int waited = -1;           // whose hidden rows are known to be written
+  int parity = 1;  // (the first run's place is still being read)
 #pragma unroll 1
   while (cur < total) {
-    if (tid == 0)
+    // A run is drawn (its number is here by the end of a block) when fewer than two
+    // blocks after this one are known, so that the next one's weights are always
+    // on the way; no earlier, for the long ones to be shared out evenly.
+    const bool last = cur + 1 == end;
+    const bool draws = next < 0 ? cur + 2 >= end : last && nend - next == 1;
+    if (draws && tid == 0)
       pending = __hip_atomic_fetch_add(p.queues + (phase * kQueues + queue) * kSpread, 1,
                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int coming = last ? next : cur + 1;  // the block after this one
+    const bool known = coming >= 0 && coming < total;
     const bool sh = it.u < nsh;
     const int r0 = uniform(sstart[it.u]), rows = uniform(srows[it.u]);
     const int parts = !it.down && m.x_bf16 ? 1 : (m.y_bf16 ? 2 : 3);
     const int cols = rows * parts;
-    const int lines = src.lines, subs = (lines + WK - 1) / WK, stages = (subs + U - 1) / U;
-    // pairs of stages whose rows fit LDS at a time (at least one)
-    constexpr int per = 2 * U * WK * LK * 2;
-    const int chunk = min((p.xbytes / cols - 16) / per, (stages + 1) / 2);
+    // turns of NL lines a wave, and how many of them have their rows in LDS at a
+    // time (at least one)
+    constexpr int per = NL * WK * LK * 2;
+    const int lines = src.lines, turns = (lines + NL * WK - 1) / (NL * WK);
+    const int chunk = min((p.xbytes / cols - 16) / per, turns);
     const int pitch = min(chunk * per, lines * LK * 2) + 16;
     // one token's x is the same for every expert
-    const bool all = 2 * chunk >= stages;
+    const bool all = chunk == turns;
     const int whose = it.down ? it.u + 1 : (T == 1 ? 0 : -2 - it.u);
     const bool keep = all && whose == staged;
     acc = f32x4{0.f, 0.f, 0.f, 0.f};
     const char* const xat = smem + (r16 < cols ? r16 : 0) * pitch + kq * NF * 16;
     Item nit = it;
 
-    int in = 0, l0 = 0;  // pairs of stages in this chunk, its first line
+    int in = 0, l0 = 0;  // turns in this chunk, its first line
 #pragma unroll 1
-    for (int st = 0; st < stages; st += 2) {
+    for (int j = 0; j < turns; ++j) {
       if (in == 0 && !keep) {
-        if (it.down && st == 0) wait_hidden(it.u);
-        else if (st > 0) __syncthreads();  // what is there has been read
-        l0 = st * U * WK;
+        if (it.down && it.u != waited) wait_hidden(it.u);
+        else if (j > 0) __syncthreads();  // what is there has been read
+        waited = pick(it.down != 0, it.u, waited);
+        l0 = j * NL * WK;
         put_rows(it, r0, rows, l0 * LK, min(chunk * (per / 2), (lines - l0) * LK), pitch, parts);
         __syncthreads();
       }
       in = in + 1 == chunk ? 0 : in + 1;
-      if (st + 1 < stages) load(B, st + 1);
-      compute(A, st, lines, xat, l0);
-      int ahead = st + 2;
-      if (ahead >= stages && next < total) {
-        nit = item_of(next);
-        enter(nit);
-        ahead = 0;
+      const bool ends = j + 1 == turns;
+#pragma unroll
+      for (int q = 0; q < NL; ++q) {
+        // kAhead lines ahead, in the last turn the next block's
+        if (q == 1 && ends && known) {
+          nit = item_of(coming);
+          enter(nit);
+        }
+        const bool over = q > 0 && ends;
+        load(buf[(q + kAhead) % NL], pick(over, q - 1, j * NL + q + kAhead), !over || known);
+        compute(buf[q], j * NL + q, lines, xat, l0);
       }
-      if (ahead < stages || next < total) load(A, ahead);
-      if (st + 1 < stages) compute(B, st + 1, lines, xat, l0);
     }
     staged = all ? whose : -1;
 
     // the waves' sums (two places in turn: the last item's may still be read)
     f32x4* const red = reinterpret_cast<f32x4*>(smem + p.xbytes) + parity * kThreads;
-    red[tid] = acc;
-    if (w == 0) {
-      const int d = draw(uniform(pending));
-      if (lane == 0) stick[parity] = d;
-    }
-    __syncthreads();
-    const int after = uniform(stick[parity]);
+    int* const drawn = stick + 2 * parity;
     parity ^= 1;
+    red[tid] = acc;
+    if (draws && w == 0) draw(uniform(pending), drawn);
+    __syncthreads();
     if (wk == 0) {
       // lane (r, q): columns 4 q .. + 3 of token row r
       const int r = lane >> 2, q = lane & 3;
@@ -610,51 +627,71 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
           for (int i = 0; i < 4; ++i) o[i] = relu_sq(v[i]);
           if (live) put4_shared(hrow + group * 16 + 4 * q, o);
         }
+      } else if (live) {
+        put4_shared(p.o + (size_t)(sh ? P + pair : pair) * D + group * 16 + 4 * q,
+                    v * (sh ? 1.f : sw[pair]));
+      }
+      if (last) {
+        // the run is written: a lane tells of each of its blocks
         stores_done();
-        if (lane == 0)
-          __hip_atomic_store(p.up_done + flags_of(it.u) + group, 1, __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-      } else {
-        const int n0 = group * 16;
-        if (live)
-          put4_shared(p.o + (size_t)(sh ? P + pair : pair) * D + n0 + 4 * q,
-                      v * (sh ? 1.f : sw[pair]));
-        stores_done();
-        int before = 0;
-        if (lane == 0)
-          before = __hip_atomic_fetch_add(p.down_done + group * kSpread, 1, __ATOMIC_RELAXED,
-                                          __HIP_MEMORY_SCOPE_AGENT);
-        if (uniform(before) == nexp - 1) {
-          // all pairs' rows of these columns are there: a lane adds every fourth
-          // of a token's, then the four sums are added
+        const int i = run + lane;
+        if (!it.down) {
+          if (i < end)
+            __hip_atomic_store(p.up_done + i * WR + wr, 1, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+        } else {
+          int before = 0;
+          if (i < end)
+            before = __hip_atomic_fetch_add(p.down_done + ((i - nup) % nd * WR + wr) * kSpread, 1,
+                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          // Where all pairs' rows of a block's columns are there, they are added: a
+          // lane every fourth of a token's, then the four sums.
+          for (uint64_t done = __ballot(i < end && before == nexp - 1); done; done &= done - 1) {
+            const int n0 = ((run + __builtin_ctzll(done) - nup) % nd * WR + wr) * 16;
 #pragma unroll 1
-          for (int t = 0; t < T; ++t) {
-            const float* const at = p.o + n0 + r16;
-            float s = 0.f;
+            for (int t = 0; t < T; ++t) {
+              const float* const at = p.o + n0 + r16;
+              float s = 0.f;
 #pragma unroll 1
-            for (int k0 = kq; k0 < K; k0 += 32) {
-              float a[8];
+              for (int k0 = kq; k0 < K; k0 += 32) {
+                float a[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                a[i] = get1_shared(at + (size_t)(t * K + min(k0 + 4 * i, K - 1)) * D);
+                for (int i = 0; i < 8; ++i)
+                  a[i] = get1_shared(at + (size_t)(t * K + min(k0 + 4 * i, K - 1)) * D);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) s += k0 + 4 * i < K ? a[i] : 0.f;
-            }
-            if (S > 0 && kq == 3) s += get1_shared(at + (size_t)(P + t) * D);
-            s += __shfl_xor(s, 16, 64);
-            s += __shfl_xor(s, 32, 64);
-            const size_t to = (size_t)t * D + n0 + r16;
-            if (kq == 0) {
-              if (m.y_bf16) static_cast<uint16_t*>(m.y)[to] = f32_to_bf16(s);
-              else static_cast<float*>(m.y)[to] = s;
+                for (int i = 0; i < 8; ++i) s += k0 + 4 * i < K ? a[i] : 0.f;
+              }
+              if (S > 0 && kq == 3) s += get1_shared(at + (size_t)(P + t) * D);
+              s += __shfl_xor(s, 16, 64);
+              s += __shfl_xor(s, 32, 64);
+              const size_t to = (size_t)t * D + n0 + r16;
+              if (kq == 0) {
+                if (m.y_bf16) static_cast<uint16_t*>(m.y)[to] = f32_to_bf16(s);
+                else static_cast<float*>(m.y)[to] = s;
+              }
             }
           }
         }
       }
     }
-    cur = next;
-    next = after;
+    const int db = draws ? uniform(drawn[0]) : -1, de = draws ? uniform(drawn[1]) : -1;
+    if (!last) {
+      cur += 1;
+      if (draws) next = db, nend = de;
+    } else {
+      const bool had = next >= 0;
+      cur = run = pick(had, next, db);
+      end = pick(had, nend, de);
+      next = pick(had, db, -1);
+      nend = pick(had, de, -1);
+    }
     it = nit;
+    if (!known && cur < total) {
+      it = item_of(cur);
+      enter(it);
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) load(buf[q], q, true);
+    }
   }
 }
 
@@ -710,7 +747,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const int route = kRouteHere * (256 + nj * 512) + 8 * E + 4 * P;
   const int turn = 16 / (m.y_bf16 ? 2 : 3);
   const int cols = (m.T < turn ? m.T : turn) * (m.y_bf16 ? 2 : 3);
-  const int red = 2 * kThreads * 16, lists = 12 * P + 160;
+  const int red = 2 * kThreads * 16, lists = 12 * P + 192;
   // four work-groups a CU where the rows allow it: 40 KB each
   const int least = cols * (2048 + 16), left = 40 * 1024 - red - lists;
   const int xbytes = (left > least ? left : least) / 16 * 16;
