@@ -24,8 +24,8 @@
 // bits every time.
 //
 // Weights are the MFMA's A operand, read from HBM as whole lines into registers,
-// kAhead lines ahead (on into the next block), brought into its layout by ds_bpermute and
-// decoded exactly to bf16 (8-bit: the block's scale on its sum).  The tokens'
+// kAhead lines ahead (on into the next block), brought into its layout through LDS
+// and decoded exactly to bf16 (8-bit: the block's scale on its sum).  The tokens'
 // operand is bf16, too: a value that is no bf16 number (fp32 x, the hidden rows)
 // is the sum of two such parts (y in bf16: 16 bits, its error far below y's
 // rounding) or three (24 bits), each a column of its own of the operand, of which
@@ -84,7 +84,8 @@ struct MoeParams {
   float *logits, *h, *hs, *o;
   int32_t *queues, *up_done, *down_done;
   int turn;    // rows of an expert taken at a time
-  int xbytes;  // LDS for the tokens' rows
+  int xbytes;  // LDS for the tokens' rows (then the waves' sums)
+  int turn_at; // where in LDS lines change their layout
   int misc;    // where in LDS what is not of the loop begins
 };
 
@@ -414,51 +415,50 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     }
   };
 
-  const int src0 = (((r16 & 7) << 3) | kq) * 4;
-  const int src1 = (((r16 & 7) << 3) | (4 + kq)) * 4;
-  const bool lo = r16 < 8;
-  f32x4 acc;
+  // A line's way into the instruction's layout, through 2 KB of LDS of the wave's
+  // own: lane l writes piece l % 8 of row l / 8 (and of row 8 + l / 8), lane (r, q)
+  // reads pieces q and 4 + q of row r, places exchanged so that neither meets a
+  // bank twice.
+  char* const turn_in = smem + p.turn_at + w * 2048 + (lane >> 3) * 128 +
+                        (((lane & 7) ^ (lane >> 3)) << 4);
+  char* const turn_in2 = smem + p.turn_at + w * 2048 + 1024 + (lane >> 3) * 128 +
+                         (((lane & 7) ^ (lane >> 3) ^ 1) << 4);
+  const char* const turn_row =
+      smem + p.turn_at + w * 2048 + (r16 >> 3) * 1024 + (r16 & 7) * 128;
+  const char* const turn_out = turn_row + ((kq ^ (r16 & 7) ^ (r16 >> 3)) << 4);
+  const char* const turn_out2 = turn_row + (((4 + kq) ^ (r16 & 7) ^ (r16 >> 3)) << 4);
   // Adds line j to acc; x0: the lane's place in LDS of the first value of its
-  // column's row in line `l0`.
-  auto compute = [&](const Line& A, int j, int lines, const char* x0, int l0)
+  // column's row in line `l0`.  (A line past the last is zeros times the last's x.)
+  auto compute = [&](const Line& A, f32x4& acc, int j, int lines, const char* x0, int l0)
                      __attribute__((always_inline)) {
-    const int l = wk + WK * j;
-    if (l < lines) {
-      u32x4 c[2];
+    u32x4 c[2];
+    *reinterpret_cast<u32x4*>(turn_in) = A.l[0];
+    *reinterpret_cast<u32x4*>(turn_in2) = A.l[1];
+    c[0] = *reinterpret_cast<const u32x4*>(turn_out);
+    c[1] = *reinterpret_cast<const u32x4*>(turn_out2);
+    const char* const xl = x0 + (min(wk + WK * j, lines - 1) - l0) * (LK * 2);
+    f32x4 sum = FMT == 2 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc;
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const int a = (int)A.l[0][d], b = (int)A.l[1][d];
-        const int a0 = __builtin_amdgcn_ds_bpermute(src0, a);
-        const int b0 = __builtin_amdgcn_ds_bpermute(src0, b);
-        const int a1 = __builtin_amdgcn_ds_bpermute(src1, a);
-        const int b1 = __builtin_amdgcn_ds_bpermute(src1, b);
-        c[0][d] = lo ? a0 : b0;
-        c[1][d] = lo ? a1 : b1;
-      }
-      const char* const xl = x0 + (l - l0) * (LK * 2);
-      f32x4 sum = FMT == 2 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < NF; ++i) {
+        bf16x8 wf;
+        if (FMT == 0) {
+          wf = __builtin_bit_cast(bf16x8, c[h]);
+        } else if (FMT == 1) {
+          wf = mx_decode8(c[h][i], mx_scale((A.s[h] >> (8 * kq)) & 255u));
+        } else {
 #pragma unroll
-        for (int i = 0; i < NF; ++i) {
-          bf16x8 wf;
-          if (FMT == 0) {
-            wf = __builtin_bit_cast(bf16x8, c[h]);
-          } else if (FMT == 1) {
-            wf = mx_decode8(c[h][i], mx_scale((A.s[h] >> (8 * kq)) & 255u));
-          } else {
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-              const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, false);
-              const auto v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, true);
-              wf[4 * d] = v0[0], wf[4 * d + 1] = v0[1];
-              wf[4 * d + 2] = v1[0], wf[4 * d + 3] = v1[1];
-            }
+          for (int d = 0; d < 2; ++d) {
+            const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, false);
+            const auto v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h][2 * i + d], 1.f, true);
+            wf[4 * d] = v0[0], wf[4 * d + 1] = v0[1];
+            wf[4 * d + 2] = v1[0], wf[4 * d + 3] = v1[1];
           }
-          sum = mfma_bf16(wf, *reinterpret_cast<const bf16x8*>(xl + h * 64 * NF + i * 16), sum);
         }
-      acc = FMT == 2 ? acc + sum * __uint_as_float(A.s[0]) : sum;
-    }
+        sum = mfma_bf16(wf, *reinterpret_cast<const bf16x8*>(xl + h * 64 * NF + i * 16), sum);
+      }
+    acc = FMT == 2 ? acc + sum * __uint_as_float(A.s[0]) : sum;
   };
 
   // The item's tokens' rows (x, or hidden rows), values k0 .. k0 + kn - 1, into
@@ -563,7 +563,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     const bool all = chunk == turns;
     const int whose = it.down ? it.u + 1 : (T == 1 ? 0 : -2 - it.u);
     const bool keep = all && whose == staged;
-    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[2] = {};  // of every other line
     const char* const xat = smem + (r16 < cols ? r16 : 0) * pitch + kq * NF * 16;
     Item nit = it;
 
@@ -589,7 +589,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
         }
         const bool over = q > 0 && ends;
         load(buf[(q + kAhead) % NL], pick(over, q - 1, j * NL + q + kAhead), !over || known);
-        compute(buf[q], j * NL + q, lines, xat, l0);
+        compute(buf[q], acc[q & 1], j * NL + q, lines, xat, l0);
       }
     }
     staged = all ? whose : -1;
@@ -598,7 +598,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     f32x4* const red = reinterpret_cast<f32x4*>(smem + p.xbytes) + parity * kThreads;
     int* const drawn = stick + 2 * parity;
     parity ^= 1;
-    red[tid] = acc;
+    red[tid] = acc[0] + acc[1];
     if (draws && w == 0) draw(uniform(pending), drawn);
     __syncthreads();
     if (wk == 0) {
@@ -748,10 +748,10 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const int turn = 16 / (m.y_bf16 ? 2 : 3);
   const int cols = (m.T < turn ? m.T : turn) * (m.y_bf16 ? 2 : 3);
   const int red = 2 * kThreads * 16, lists = 12 * P + 192;
-  // four work-groups a CU where the rows allow it: 40 KB each
-  const int least = cols * (2048 + 16), left = 40 * 1024 - red - lists;
+  // three work-groups a CU where the rows allow it: 53 KB each
+  const int least = cols * (2048 + 16), left = 52 * 1024 - red - lists - kWaves * 2048;
   const int xbytes = (left > least ? left : least) / 16 * 16;
-  const int work = xbytes + red;
+  const int turned = kWaves * 2048, work = xbytes + red + turned;
   MoeParams p{m,
               reinterpret_cast<float*>(ws + l.logits),
               reinterpret_cast<float*>(ws + l.h),
@@ -762,6 +762,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
               sync + l.down_done,
               turn,
               xbytes,
+              xbytes + red,
               ((route > work ? route : work) + 15) / 16 * 16};
   const int lds = p.misc + lists;
   auto logits = [&](auto g, auto x) {
@@ -781,7 +782,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
     e = route_logits(m.r, p.logits, false, m.bias, m.idx, m.weights, s);
     if (e != hipSuccess) return e;
   }
-  constexpr int grid = 1024;
+  constexpr int grid = 768;
   with_format(m.format, [&](auto fmt) {
     constexpr int FMT = decltype(fmt)::value;
     if (nj == 0) moe_tokens_kernel<FMT, 0><<<grid, kThreads, lds, s>>>(p);
