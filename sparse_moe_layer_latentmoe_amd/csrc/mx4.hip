@@ -340,6 +340,341 @@ __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(Mx4Gemm p, const Ti
   }
 }
 
+// Many tokens: MFMA tiles of BM token rows x BN weight rows fed through LDS by
+// direct global -> LDS copies.  A step is a line of k (128 bytes of a row, 256
+// values) in two halves of the tile's weight rows; each wave owns 32 TM token
+// rows and 32 TH weight rows of each half, and holds the fragments it multiplies
+// in registers: a 32x32x64 MFMA takes 16 bytes of a row and lane, lane (r, h) (r =
+// lane % 32, h = lane / 32) of step s the block 4 h + s of row r, whose scale is
+// byte s of word h of the line's two.  A fragment's registers are read anew from
+// LDS, for the next half (one set of them where there are two groups, two where
+// there is one), right after their last use, so no LDS read is waited for at
+// the top of a step.  During step k, LDS holds what is read in it (weight half 1 of
+// k, half 0 of k + 1, token rows of k + 1), and copies run into the places of what
+// step k - 1 read: token rows of k + 2 and, with a ring of WD lines of weights,
+// half 1 of line k + WD - 1 and half 0 of k + WD.  One barrier a step; the copy
+// instructions are spread over the MFMAs.
+//
+// Scales come four lines at a time (32 bytes of a row), a quarter of the tile's
+// rows with each step.
+//
+// Split over k (dense, few tiles): work-group (x, y) computes tile x over the
+// y-th part of the lines and writes fp32 partial sums to part y of `y`.
+template <bool GROUPED, int NW, int BM, int BN, int WM, int WD, class OUT>
+__global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile* tiles,
+                                                           const int* ntiles) {
+  constexpr int BH = BN / 2, WN = NW / WM;
+  constexpr int TM = BM / WM / 32, TH = BH / WN / 32, SETS = TH == 1 ? 2 : 1;
+  constexpr int RPI = kFp8CopyRows, ROWB = 128;
+  constexpr int NIA = BM / RPI / NW, NIH = BH / RPI / NW;  // copies a wave and unit
+  constexpr int ABUF = BM * ROWB, HBUF = BH * ROWB;
+  constexpr int SROWS = BM + BN;                  // rows of scales
+  constexpr int NIS = SROWS / RPI;                // copies of four lines' scales
+  constexpr int NSW = (NIS + 4 * NW - 1) / (4 * NW);  // a wave's with each step
+  static_assert(TM * 32 * WM == BM && TH * 32 * WN == BH, "whole groups");
+  static_assert(NIA * RPI * NW == BM && NIH * RPI * NW == BH, "rows per unit");
+  // One LDS array: with several, the compiler tells them apart and then waits
+  // for all copies in flight before every LDS read.
+  constexpr int W00 = 2 * ABUF, S00 = W00 + 2 * WD * HBUF, LDS = S00 + 2 * SROWS * 32;
+  static_assert(LDS <= 160 * 1024, "LDS");
+  __shared__ __attribute__((aligned(1024))) char smem[LDS];
+
+  int tm, nb;
+  const int nblocks = (p.N + BN - 1) / BN;
+  if (!work_item_uniform<GROUPED>(nblocks, p.M, BM, tiles, ntiles, tm, nb)) return;
+  int e = 0, m0, mcount;
+  if (GROUPED) {
+    e = uniform(tiles[tm].expert);
+    m0 = uniform(tiles[tm].row0);
+    mcount = uniform(tiles[tm].nrows);
+  } else {
+    m0 = tm * BM;
+    mcount = min(BM, p.M - m0);
+  }
+  const int n0 = nb * BN;
+  const int lane = threadIdx.x & 63;
+  const int w = uniform(threadIdx.x >> 6);
+  const int wm = w / WN, wn = w % WN;
+  const int RB = p.K / 2, SW = p.K / 128;  // bytes and scale words of a row
+  const int LT = (SW + 1) / 2;             // lines of a whole row
+  int k0 = 0, KL = LT;                     // this work-group's: k0 .. k0 + KL - 1
+  if (!GROUPED && p.splits > 1) {
+    k0 = blockIdx.y * LT / p.splits;
+    KL = (blockIdx.y + 1) * LT / p.splits - k0;
+    p.y = static_cast<float*>(p.y) + (size_t)blockIdx.y * p.M * p.N;
+  }
+  // the last line is half a line (and this work-group's)
+  const int half_line = SW % 2 && k0 + KL == LT ? KL - 1 : -1;
+
+  // Copy sources: instruction j of wave w fills rows RPI (w + NW j) .. + 7 of its
+  // buffer, written already swizzled (16-byte chunk c of row r in place c ^ (r / 2)
+  // % 8).  Token rows past the tile's count, rows whose index is outside x and the
+  // second half of a half line are past the buffer's bound and read as 0.  Weight
+  // rows past N read the matrix's last rows again (their columns are not stored).
+  constexpr uint32_t kNone = 0x80000000u;
+  const int lr = lane >> 3;
+  const int sw = ((4 * (w & 1)) + (lr >> 1)) & 7;
+  static_assert(NW % 2 == 0, "the swizzle of a wave's rows");
+  const uint32_t chunk = (uint32_t)(((lane & 7) ^ sw) * 16);
+  const bool gather = p.rows != nullptr;
+  const __amdgpu_buffer_rsrc_t ra =
+      buffer_rsrc((gather ? p.x : p.x + (size_t)m0 * RB) + k0 * ROWB);
+  const size_t w0 = ((size_t)e * p.N + n0) * RB + k0 * ROWB;
+  const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(p.w + w0);
+  auto x_row = [&](int i, bool& ok) -> uint32_t {
+    ok = i < mcount;
+    if (!ok) return 0;
+    return gather ? (uint32_t)mx4_x_row(p, m0 + i, ok) : (uint32_t)i;
+  };
+  uint32_t ao[NIA], bo = fp8_weight_lane(lane, chunk, (uint32_t)RB);
+#pragma unroll
+  for (int j = 0; j < NIA; ++j) {
+    bool ok;
+    const uint32_t row = x_row(RPI * (w + NW * j) + lr, ok);
+    ao[j] = ok ? row * (uint32_t)RB + chunk : kNone;
+    asm volatile("" : "+v"(ao[j]));  // one register: not half of a 64-bit product
+  }
+  asm volatile("" : "+v"(bo));
+  const bool upper = chunk >= 64;  // of a half line, what is not there
+  auto copy_x = [&](int k, int j) __attribute__((always_inline)) {
+    const uint32_t at = k == half_line && upper ? kNone : ao[j];
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        ra, (lds_void*)(smem + (k & 1) * ABUF + (w + NW * j) * RPI * ROWB), 16, at, k * ROWB, 0, 0);
+  };
+  // weight half h of line k, to ring offset r
+  auto copy_w = [&](int k, int h, int r, int j) __attribute__((always_inline)) {
+    const uint32_t at = k == half_line && upper ? kNone : bo;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rb, (lds_void*)(smem + W00 + r + h * HBUF + (w + NW * j) * RPI * ROWB), 16, at,
+        fp8_weight_scalar(h * BH + (w + NW * j) * RPI, p.N - n0, k, RB), 0, 0);
+  };
+  // Scales of lines 4 g .. 4 g + 3: rows 0 .. BM - 1 are the tokens', then the
+  // weights'.  Instruction i fills rows 8 i .. + 7, lane l row 8 i + l / 8, place
+  // l % 8, which holds word (l % 8) ^ 2 (i % 4) of the eight (so that 32 rows' reads of
+  // a line meet no bank twice).  Words past K and rows that are not there read as 0.
+  const __amdgpu_buffer_rsrc_t rxs = buffer_rsrc(gather ? p.xs : p.xs + (size_t)m0 * SW * 4);
+  const __amdgpu_buffer_rsrc_t rws = buffer_rsrc(p.ws + ((size_t)e * p.N + n0) * SW * 4);
+  uint32_t so[4][NSW];  // the row's offset
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int u = 0; u < NSW; ++u) {
+      const int id = (j * NW + w) * NSW + u, row = RPI * (id < NIS ? id : id - NIS) + lr;
+      bool ok;
+      uint32_t at;
+      if (row < BM) {
+        at = x_row(row, ok) * (uint32_t)SW * 4u;
+      } else {
+        ok = n0 + row - BM < p.N;
+        at = (uint32_t)(row - BM) * (uint32_t)SW * 4u;
+      }
+      so[j][u] = ok ? at : kNone;
+      asm volatile("" : "+v"(so[j][u]));
+    }
+  // copies u of part j of group g (lines counted from k0, words from the row's start)
+  auto copy_s = [&](int g, int j, int u, uint32_t off) __attribute__((always_inline)) {
+    int id = (j * NW + w) * NSW + u;
+    id = id < NIS ? id : id - NIS;
+    const uint32_t word = (uint32_t)(2 * k0 + 8 * g) + (uint32_t)((lane & 7) ^ ((id & 3) << 1));
+    const uint32_t at = off == kNone || word >= (uint32_t)SW ? kNone : off + word * 4u;
+    char* const to = smem + S00 + ((g & 1) * SROWS + RPI * id) * 32;
+    if (RPI * id < BM) __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (lds_void*)to, 4, at, 0, 0, 0);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rws, (lds_void*)to, 4, at, 0, 0, 0);
+  };
+  // what the first MFMAs need, then what step 0 reads, then what it need not
+  // wait for
+  constexpr int R = 2 * HBUF;  // a line's place in the ring of weights
+#pragma unroll
+  for (int j = 0; j < NIA; ++j) copy_x(0, j);
+#pragma unroll
+  for (int j = 0; j < NIH; ++j) copy_w(0, 0, 0, j);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int u = 0; u < NSW; ++u) copy_s(0, j, u, so[j][u]);
+#pragma unroll
+  for (int j = 0; j < NIH; ++j) copy_w(0, 1, 0, j);
+  if (KL > 1) {
+#pragma unroll
+    for (int j = 0; j < NIH; ++j) copy_w(1, 0, R, j);
+#pragma unroll
+    for (int j = 0; j < NIA; ++j) copy_x(1, j);
+#pragma unroll
+    for (int u = 0; u < NSW; ++u) copy_s(1, 0, u, so[0][u]);
+    if constexpr (WD == 3) {
+#pragma unroll
+      for (int j = 0; j < NIH; ++j) copy_w(1, 1, R, j);
+      if (KL > 2) {
+#pragma unroll
+        for (int j = 0; j < NIH; ++j) copy_w(2, 0, 2 * R, j);
+      }
+    }
+  }
+
+  const int r32 = lane & 31, kh = lane >> 5;
+  uint32_t lo[4];  // a lane's place of block 4 h + s in a 32-row group
+#pragma unroll
+  for (int s = 0; s < 4; ++s) lo[s] = r32 * ROWB + (((4 * kh + s) ^ ((r32 >> 1) & 7)) << 4);
+  const uint32_t aw = (uint32_t)(wm * (BM / WM)) * ROWB;
+  const uint32_t bw = (uint32_t)(W00 + wn * (BH / WN) * ROWB);
+  f32x16 acc[2 * TH][TM];
+#pragma unroll
+  for (int a = 0; a < 2 * TH; ++a)
+#pragma unroll
+    for (int b = 0; b < TM; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+
+  struct Frag {
+    i32x4 v[4];
+  };
+  // fragments: token group t of line k, weight group g at ring offset r
+  auto read_x = [&](int k, int t) __attribute__((always_inline)) {
+    Frag f;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      f.v[s] = *reinterpret_cast<const i32x4*>(smem + (k & 1) * ABUF + aw + t * 32 * ROWB + lo[s]);
+    return f;
+  };
+  auto read_w = [&](int r, int g) __attribute__((always_inline)) {
+    Frag f;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      f.v[s] = *reinterpret_cast<const i32x4*>(smem + bw + r + g * 32 * ROWB + lo[s]);
+    return f;
+  };
+  // the word of scales of row `row` (a multiple of 32 and the lane's) for line k
+  const uint32_t sl = (uint32_t)(S00 + r32 * 32 + kh * 4), sx = (r32 >> 3) & 3;
+  auto read_s = [&](int k, int row) __attribute__((always_inline)) {
+    return *reinterpret_cast<const int*>(smem + sl + ((k >> 2) & 1) * (SROWS * 32) + row * 32 +
+                                         (((k & 3) ^ sx) << 3));
+  };
+  Frag xf[TM], wf[SETS][TH];
+  int xs[TM], ws[2 * TH];
+
+  int r0 = 0;  // ring offset of line k
+  // Step k.  COPY: 2 copies everything (k + WD < KL), 1 all but the weights of
+  // line k + WD (the last step with copies), 0 nothing.
+  auto step = [&](auto copy_c, int k) __attribute__((always_inline)) {
+    constexpr int COPY = decltype(copy_c)::value;
+    const int r1 = r0 + R == WD * R ? 0 : r0 + R;
+    const int r2 = r1 + R == WD * R ? 0 : r1 + R;  // r0 when WD = 2
+    // what this step reads has landed (with WD = 3 the weight copies of the
+    // last step may be in flight), and this wave's LDS reads of the last step
+    // are done; then the same for every wave
+    if (WD == 3 && COPY) wait_vmcnt<2 * NIH>();
+    else wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    stage_barrier_hard();
+    // part j of group g of the scales comes with step 4 g - 5 + j, so that group g,
+    // first read in step 4 g - 1, is whole then, and what it replaces, group g - 2,
+    // was last read in step 4 g - 6
+    constexpr bool XC = COPY == 2 || (COPY == 1 && WD == 3);  // line k + 2 exists
+    constexpr int NX = XC ? NIA + NSW : 0;
+    constexpr int NC = NX + (COPY == 2 ? 2 * NIH : (COPY == 1 ? NIH : 0));
+    constexpr int X0 = WD == 2 ? NC - NX : 0, W0 = WD == 2 ? 0 : NX;
+    uint32_t sof[NSW];
+#pragma unroll
+    for (int u = 0; u < NSW; ++u) {
+      const int j = (k + 1) & 3;
+      const uint32_t a = j & 1 ? so[1][u] : so[0][u], b = j & 1 ? so[3][u] : so[2][u];
+      sof[u] = j & 2 ? b : a;
+    }
+    auto copy = [&](int c) __attribute__((always_inline)) {
+      if (c >= X0 && c < X0 + NX - NSW) copy_x(k + 2, c - X0);
+      else if (c >= X0 && c < X0 + NX)
+        copy_s((k + 5) >> 2, (k + 1) & 3, c - X0 - NIA, sof[(c - X0 - NIA) % NSW]);
+      else if (c < W0 + NIH) copy_w(k + WD - 1, 1, WD == 2 ? r1 : r2, c - W0);
+      else copy_w(k + WD, 0, r0, c - W0 - NIH);
+    };
+    constexpr int NP = TM * TH * 4;  // MFMAs of a half
+    constexpr int EVERY = NC <= NP ? 2 : 1;
+    static_assert(NC <= 2 * NP, "copies");
+    int xn[TM], wnx[2 * TH];
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
+      const int h = i / NP, g = i % NP / (4 * TM), t = i % (4 * TM) / 4, s = i % 4;
+      const int a = h * TH + g;
+      if (SETS == 2 && i % NP == 0) wf[1 - h][0] = read_w(h == 0 ? r0 + HBUF : r1, 0);
+      const i32x8 av = low(wf[SETS == 2 ? h : 0][g].v[s]), bv = low(xf[t].v[s]);
+#define LMOE_MFMA(S) \
+  __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, acc[a][t], 4, 4, S, ws[a], S, xs[t])
+      acc[a][t] = s == 0 ? LMOE_MFMA(0) : s == 1 ? LMOE_MFMA(1) : s == 2 ? LMOE_MFMA(2) : LMOE_MFMA(3);
+#undef LMOE_MFMA
+      if (SETS == 1 && t == TM - 1 && s == 3) wf[0][g] = read_w(h == 0 ? r0 + HBUF : r1, g);
+      if (h == 1 && g == TH - 1 && s == 3) {
+        xf[t] = read_x(k + 1, t);
+        xn[t] = read_s(k + 1, wm * (BM / WM) + t * 32);
+      }
+      if (h == 1 && i - NP < 2 * TH) {
+        const int b = i - NP;
+        wnx[b] = read_s(k + 1, BM + (b / TH) * BH + wn * (BH / WN) + (b % TH) * 32);
+      }
+      if (i % EVERY == 0 && i / EVERY < NC) copy(i / EVERY);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int t = 0; t < TM; ++t) xs[t] = xn[t];
+#pragma unroll
+    for (int b = 0; b < 2 * TH; ++b) ws[b] = wnx[b];
+    r0 = r1;
+  };
+  if (KL > 2) wait_vmcnt<(WD == 3 ? 4 : 2) * NIH + NIA + NSW>();
+  else wait_vmcnt<0>();
+  stage_barrier_hard();
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+    xf[t] = read_x(0, t);
+    xs[t] = read_s(0, wm * (BM / WM) + t * 32);
+  }
+#pragma unroll
+  for (int g = 0; g < TH; ++g) wf[0][g] = read_w(0, g);
+#pragma unroll
+  for (int b = 0; b < 2 * TH; ++b)
+    ws[b] = read_s(0, BM + (b / TH) * BH + wn * (BH / WN) + (b % TH) * 32);
+  int k = 0;
+  for (; k + WD < KL; ++k) step(std::integral_constant<int, 2>{}, k);
+  if (k + WD - 1 < KL) step(std::integral_constant<int, 1>{}, k++);
+  for (; k < KL; ++k) step(std::integral_constant<int, 0>{}, k);
+  // the last step read ahead (values that are not used): let the reads end
+  // before the buffers are written below
+  wait_lgkmcnt0();
+  stage_barrier_hard();
+
+  // Lane (r, h) holds, in registers 4 v .. + 3 of a group, columns 8 v + 4 h .. + 3 of
+  // token r.  They leave through LDS, in the wave's own region, as whole pieces of
+  // rows of 32 columns (16-byte chunk c of row r in place c ^ r % chunks).
+  constexpr int EL = std::is_same<OUT, float>::value ? 4 : 2;
+  constexpr int RBO = 32 * EL, CH = RBO / 16, RPS = 64 / CH;  // row bytes, chunks; rows a store
+  static_assert(NW * 32 * RBO <= 2 * ABUF + 2 * WD * HBUF, "staging room");
+  char* const reg = smem + w * 32 * RBO;
+#pragma unroll
+  for (int a = 0; a < 2 * TH; ++a)
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const f32x4 q = {acc[a][t][4 * v], acc[a][t][4 * v + 1], acc[a][t][4 * v + 2],
+                         acc[a][t][4 * v + 3]};
+        const int c = EL == 4 ? 2 * v + kh : v;
+        char* const to = reg + r32 * RBO + ((c ^ (r32 & (CH - 1))) << 4);
+        if constexpr (EL == 4) *reinterpret_cast<f32x4*>(to) = q;
+        else *reinterpret_cast<u16x4*>(to + kh * 8) = pack4_bf16(q);
+      }
+      const int n = n0 + (a / TH) * BH + wn * (BH / WN) + (a % TH) * 32;
+      const int c = lane & (CH - 1);
+#pragma unroll
+      for (int j = 0; j < 32 / RPS; ++j) {
+        const int row = j * RPS + lane / CH, i = wm * (BM / WM) + t * 32 + row;
+        const u32x4 q =
+            *reinterpret_cast<const u32x4*>(reg + row * RBO + ((c ^ (row & (CH - 1))) << 4));
+        if (i < mcount && n + c * (16 / EL) < p.N)
+          *reinterpret_cast<u32x4*>(static_cast<OUT*>(p.y) + (size_t)(m0 + i) * p.N + n +
+                                    c * (16 / EL)) = q;
+      }
+    }
+}
+
 // ---- launchers ---------------------------------------------------------------------
 
 namespace {
@@ -357,28 +692,79 @@ bool wide(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % 
 // A launch has fewer than 2^32 threads.
 bool too_many(long grid, int threads) { return grid >= (1L << 32) / threads; }
 
+// How a product runs.
 struct Plan {
   bool stream;  // weight streaming, else LDS-tiled
   int bm;       // token rows of a tile
   int splits;   // of k (dense tiles)
 };
 
+// Grouped: rows per group on average decide.
+Plan grouped_plan(int rows, int groups) {
+  if (rows <= 4L * groups) return {true, kStreamTileM, 1};
+  const double r = (double)rows / groups;
+  const int bm[3] = {64, 128, 192};
+  const double cost[3] = {1.0, 1.25, 1.675};
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 3; ++i) {
+    const double n = r / bm[i] + 0.4;
+    const double c = (n > 1 ? n : 1.0) * cost[i];
+    if (i == 0 || c < least) best = i, least = c;
+  }
+  return {false, bm[best], 1};
+}
+
+// Dense: up to 16 rows stream the weights.  Above that the tile shape and the
+// split of k with the least estimated time.
+struct DenseTile {
+  int bm, bn;
+};
+constexpr DenseTile kDenseTiles[3] = {{256, 256}, {128, 256}, {64, 128}};
+double tile_us(const DenseTile& t, long n) {
+  if (t.bm == 64) return n * (0.34 / 256) > 0.36 ? n * (0.34 / 256) : 0.36;
+  return (double)((n + 255) / 256) * (t.bm == 256 ? 1.65 : 0.96);
+}
+Plan dense_plan(int M, int N, int K) {
+  if (M <= 16) return {true, kStreamTileM, 1};
+  const int lines = (K + 255) / 256;
+  Plan best{};
+  double least = 0;
+  for (const DenseTile& t : kDenseTiles) {
+    for (int s = 1; s <= 8; s *= 2) {
+      if (s > 1 && lines / s < 4) continue;  // a part is at least four lines
+      const long n = (long)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn) * s;
+      double us = tile_us(t, n) * ((lines + s - 1) / s) + 3.4;
+      if (s > 1) us += 4.0 + (double)s * M * N * 8 / 4e6;
+      if (best.bm == 0 || us < least) best = {false, t.bm, s}, least = us;
+    }
+  }
+  return best;
+}
+
 Plan make_plan(int M, int N, int K, int groups) {
-  (void)M, (void)N, (void)K, (void)groups;
-  return {true, kStreamTileM, 1};
+  return groups ? grouped_plan(M, groups) : dense_plan(M, N, K);
 }
 
 int grouped_tiles(int rows, int groups, int tile_m) {
   return (rows < groups ? rows : groups) + rows / tile_m + 1;
 }
 
+long xcd_grid(long work) { return kXcds * ((work + kXcds - 1) / kXcds); }
+
 // Work-groups and threads of a product's launch.
 constexpr int kGroupedWaves = 4, kGroupedRG = 4, kDenseWaves = 8, kDenseRG = 1;
 long grid_of(const Plan& plan, int M, int N, int groups, int* threads) {
-  const int rg = groups ? kGroupedRG : kDenseRG;
-  *threads = 64 * (groups ? kGroupedWaves : kDenseWaves);
   const long tiles = groups ? grouped_tiles(M, groups, plan.bm) : (M + plan.bm - 1) / plan.bm;
-  return tiles * ((N + 16 * rg - 1) / (16 * rg));
+  if (plan.stream) {
+    const int rg = groups ? kGroupedRG : kDenseRG;
+    *threads = 64 * (groups ? kGroupedWaves : kDenseWaves);
+    return tiles * ((N + 16 * rg - 1) / (16 * rg));
+  }
+  const bool small = !groups && plan.bm == 64;
+  *threads = small ? 256 : 512;
+  const int bn = small ? 128 : 256;
+  return xcd_grid(tiles * ((N + bn - 1) / bn));
 }
 
 template <class OUT>
@@ -387,12 +773,29 @@ hipError_t launch(const Mx4Gemm& p, const Plan& plan, const Tile* tiles, const i
   int threads;
   const long grid = grid_of(plan, p.M, p.N, p.groups, &threads);
   if (too_many(grid, threads)) return hipErrorInvalidConfiguration;
-  if (p.groups)
-    mx4_stream_kernel<true, kGroupedWaves, kGroupedRG, 1, OUT><<<grid, threads, 0, s>>>(p, tiles,
-                                                                                       ntiles);
-  else
-    mx4_stream_kernel<false, kDenseWaves, kDenseRG, 2, OUT><<<grid, threads, 0, s>>>(p, nullptr,
-                                                                                    nullptr);
+  const dim3 g(grid, p.splits);
+  if (plan.stream) {
+    if (p.groups)
+      mx4_stream_kernel<true, kGroupedWaves, kGroupedRG, 1, OUT><<<g, threads, 0, s>>>(p, tiles,
+                                                                                      ntiles);
+    else
+      mx4_stream_kernel<false, kDenseWaves, kDenseRG, 2, OUT><<<g, threads, 0, s>>>(p, nullptr,
+                                                                                   nullptr);
+  } else if (p.groups) {
+    if (plan.bm == 64)
+      mx4_pipe_kernel<true, 8, 64, 256, 2, 3, OUT><<<g, threads, 0, s>>>(p, tiles, ntiles);
+    else if (plan.bm == 128)
+      mx4_pipe_kernel<true, 8, 128, 256, 2, 3, OUT><<<g, threads, 0, s>>>(p, tiles, ntiles);
+    else
+      mx4_pipe_kernel<true, 8, 192, 256, 2, 2, OUT><<<g, threads, 0, s>>>(p, tiles, ntiles);
+  } else {
+    if (plan.bm == 64)
+      mx4_pipe_kernel<false, 4, 64, 128, 2, 3, OUT><<<g, threads, 0, s>>>(p, nullptr, nullptr);
+    else if (plan.bm == 128)
+      mx4_pipe_kernel<false, 8, 128, 256, 2, 3, OUT><<<g, threads, 0, s>>>(p, nullptr, nullptr);
+    else
+      mx4_pipe_kernel<false, 8, 256, 256, 4, 2, OUT><<<g, threads, 0, s>>>(p, nullptr, nullptr);
+  }
   return hipGetLastError();
 }
 
@@ -449,6 +852,14 @@ hipError_t mx4_matmul(Mx4Gemm p, const int32_t* offsets, bool out_bf16, void* ws
     if (e != hipSuccess) return e;
     tiles = t;
     ntiles = n;
+  }
+  p.splits = plan.splits;
+  if (plan.splits > 1) {
+    void* const y = p.y;
+    p.y = ws;
+    const hipError_t e = launch<float>(p, plan, nullptr, nullptr, s);
+    if (e != hipSuccess) return e;
+    return add_parts(static_cast<const float*>(ws), plan.splits, (long)p.M * p.N, y, out_bf16, s);
   }
   return out_bf16 ? launch<uint16_t>(p, plan, tiles, ntiles, s)
                   : launch<float>(p, plan, tiles, ntiles, s);
