@@ -368,9 +368,10 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
   constexpr int RPI = kFp8CopyRows, ROWB = 128;
   constexpr int NIA = BM / RPI / NW, NIH = BH / RPI / NW;  // copies a wave and unit
   constexpr int ABUF = BM * ROWB, HBUF = BH * ROWB;
-  constexpr int SROWS = BM + BN;                  // rows of scales
-  constexpr int NIS = SROWS / RPI;                // copies of four lines' scales
-  constexpr int NSW = (NIS + 4 * NW - 1) / (4 * NW);  // a wave's with each step
+  constexpr int SROWS = BM + BN;       // rows of scales
+  constexpr int NST = BM / 32, NSB = BN / 32;  // copies of a quarter of four lines' scales
+  constexpr int NSW = 2;               // a wave's with each step (some twice)
+  static_assert(NST <= NW && NSB <= NW, "one of each a wave");
   static_assert(TM * 32 * WM == BM && TH * 32 * WN == BH, "whole groups");
   static_assert(NIA * RPI * NW == BM && NIH * RPI * NW == BH, "rows per unit");
   // One LDS array: with several, the compiler tells them apart and then waits
@@ -449,37 +450,41 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
         fp8_weight_scalar(h * BH + (w + NW * j) * RPI, p.N - n0, k, RB), 0, 0);
   };
   // Scales of lines 4 g .. 4 g + 3: rows 0 .. BM - 1 are the tokens', then the
-  // weights'.  Instruction i fills rows 8 i .. + 7, lane l row 8 i + l / 8, place
-  // l % 8, which holds word (l % 8) ^ 2 (i % 4) of the eight (so that 32 rows' reads of
-  // a line meet no bank twice).  Words past K and rows that are not there read as 0.
+  // weights'.  A copy fills 8 rows, lane l row l / 8, place l % 8, which holds word
+  // (l % 8) ^ 2 (i % 4) of the eight, i the row / 8 (so that 32 rows' reads of a line
+  // meet no bank twice).  With quarter j a wave copies the (w % NST)-th of the quarter
+  // of the tokens' rows and the (w % NSB)-th of the weights'.  Words past K and rows
+  // that are not there read as 0.
   const __amdgpu_buffer_rsrc_t rxs = buffer_rsrc(gather ? p.xs : p.xs + (size_t)m0 * SW * 4);
   const __amdgpu_buffer_rsrc_t rws = buffer_rsrc(p.ws + ((size_t)e * p.N + n0) * SW * 4);
-  uint32_t so[4][NSW];  // the row's offset
+  const int wt = w % NST, wb = w % NSB;
+  uint32_t so[4];  // the token row's offset
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int u = 0; u < NSW; ++u) {
-      const int id = (j * NW + w) * NSW + u, row = RPI * (id < NIS ? id : id - NIS) + lr;
-      bool ok;
-      uint32_t at;
-      if (row < BM) {
-        at = x_row(row, ok) * (uint32_t)SW * 4u;
-      } else {
-        ok = n0 + row - BM < p.N;
-        at = (uint32_t)(row - BM) * (uint32_t)SW * 4u;
-      }
-      so[j][u] = ok ? at : kNone;
-      asm volatile("" : "+v"(so[j][u]));
-    }
-  // copies u of part j of group g (lines counted from k0, words from the row's start)
-  auto copy_s = [&](int g, int j, int u, uint32_t off) __attribute__((always_inline)) {
-    int id = (j * NW + w) * NSW + u;
-    id = id < NIS ? id : id - NIS;
-    const uint32_t word = (uint32_t)(2 * k0 + 8 * g) + (uint32_t)((lane & 7) ^ ((id & 3) << 1));
-    const uint32_t at = off == kNone || word >= (uint32_t)SW ? kNone : off + word * 4u;
-    char* const to = smem + S00 + ((g & 1) * SROWS + RPI * id) * 32;
-    if (RPI * id < BM) __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (lds_void*)to, 4, at, 0, 0, 0);
-    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rws, (lds_void*)to, 4, at, 0, 0, 0);
+  for (int j = 0; j < 4; ++j) {
+    bool ok;
+    const uint32_t row = x_row(RPI * (j * NST + wt) + lr, ok);
+    so[j] = ok ? row * (uint32_t)SW * 4u : kNone;
+    asm volatile("" : "+v"(so[j]));
+  }
+  // (words from the row's start; lines are counted from k0)
+  auto word_of = [&](int g, int id) __attribute__((always_inline)) {
+    return (uint32_t)(2 * k0 + 8 * g) + (uint32_t)((lane & 7) ^ ((id & 3) << 1));
+  };
+  auto copy_st = [&](int g, int j, uint32_t off) __attribute__((always_inline)) {
+    const int id = j * NST + wt;
+    // (past the bound: kNone and whatever is added to it)
+    const uint32_t word = word_of(g, id), sum = off + word * 4u;
+    const uint32_t at = word < (uint32_t)SW ? sum : kNone;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rxs, (lds_void*)(smem + S00 + ((g & 1) * SROWS + RPI * id) * 32), 4, at, 0, 0, 0);
+  };
+  auto copy_sw = [&](int g, int j) __attribute__((always_inline)) {
+    const int id = j * NSB + wb, row = RPI * id + lr;
+    const uint32_t word = word_of(g, id);
+    const uint32_t sum = ((uint32_t)row * (uint32_t)SW + word) * 4u;
+    const uint32_t at = (n0 + row < p.N) & (word < (uint32_t)SW) ? sum : kNone;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rws, (lds_void*)(smem + S00 + ((g & 1) * SROWS + BM + RPI * id) * 32), 4, at, 0, 0, 0);
   };
   // what the first MFMAs need, then what step 0 reads, then what it need not
   // wait for
@@ -489,9 +494,10 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
 #pragma unroll
   for (int j = 0; j < NIH; ++j) copy_w(0, 0, 0, j);
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int u = 0; u < NSW; ++u) copy_s(0, j, u, so[j][u]);
+  for (int j = 0; j < 4; ++j) {
+    copy_st(0, j, so[j]);
+    copy_sw(0, j);
+  }
 #pragma unroll
   for (int j = 0; j < NIH; ++j) copy_w(0, 1, 0, j);
   if (KL > 1) {
@@ -499,8 +505,8 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
     for (int j = 0; j < NIH; ++j) copy_w(1, 0, R, j);
 #pragma unroll
     for (int j = 0; j < NIA; ++j) copy_x(1, j);
-#pragma unroll
-    for (int u = 0; u < NSW; ++u) copy_s(1, 0, u, so[0][u]);
+    copy_st(1, 0, so[0]);
+    copy_sw(1, 0);
     if constexpr (WD == 3) {
 #pragma unroll
       for (int j = 0; j < NIH; ++j) copy_w(1, 1, R, j);
@@ -529,18 +535,22 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
     i32x4 v[4];
   };
   // fragments: token group t of line k, weight group g at ring offset r
+  auto read_x1 = [&](int k, int t, int s) __attribute__((always_inline)) {
+    return *reinterpret_cast<const i32x4*>(smem + (k & 1) * ABUF + aw + t * 32 * ROWB + lo[s]);
+  };
+  auto read_w1 = [&](int r, int g, int s) __attribute__((always_inline)) {
+    return *reinterpret_cast<const i32x4*>(smem + bw + r + g * 32 * ROWB + lo[s]);
+  };
   auto read_x = [&](int k, int t) __attribute__((always_inline)) {
     Frag f;
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      f.v[s] = *reinterpret_cast<const i32x4*>(smem + (k & 1) * ABUF + aw + t * 32 * ROWB + lo[s]);
+    for (int s = 0; s < 4; ++s) f.v[s] = read_x1(k, t, s);
     return f;
   };
   auto read_w = [&](int r, int g) __attribute__((always_inline)) {
     Frag f;
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      f.v[s] = *reinterpret_cast<const i32x4*>(smem + bw + r + g * 32 * ROWB + lo[s]);
+    for (int s = 0; s < 4; ++s) f.v[s] = read_w1(r, g, s);
     return f;
   };
   // the word of scales of row `row` (a multiple of 32 and the lane's) for line k
@@ -573,27 +583,26 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
     constexpr int NX = XC ? NIA + NSW : 0;
     constexpr int NC = NX + (COPY == 2 ? 2 * NIH : (COPY == 1 ? NIH : 0));
     constexpr int X0 = WD == 2 ? NC - NX : 0, W0 = WD == 2 ? 0 : NX;
-    uint32_t sof[NSW];
-#pragma unroll
-    for (int u = 0; u < NSW; ++u) {
-      const int j = (k + 1) & 3;
-      const uint32_t a = j & 1 ? so[1][u] : so[0][u], b = j & 1 ? so[3][u] : so[2][u];
-      sof[u] = j & 2 ? b : a;
+    const int part = (k + 1) & 3;
+    uint32_t sof = 0;
+    if (XC) {
+      const uint32_t a = part & 1 ? so[1] : so[0], b = part & 1 ? so[3] : so[2];
+      sof = part & 2 ? b : a;
     }
     auto copy = [&](int c) __attribute__((always_inline)) {
-      if (c >= X0 && c < X0 + NX - NSW) copy_x(k + 2, c - X0);
-      else if (c >= X0 && c < X0 + NX)
-        copy_s((k + 5) >> 2, (k + 1) & 3, c - X0 - NIA, sof[(c - X0 - NIA) % NSW]);
+      if (c >= X0 && c < X0 + NIA && XC) copy_x(k + 2, c - X0);
+      else if (XC && c == X0 + NIA) copy_st((k + 5) >> 2, part, sof);
+      else if (XC && c == X0 + NIA + 1) copy_sw((k + 5) >> 2, part);
       else if (c < W0 + NIH) copy_w(k + WD - 1, 1, WD == 2 ? r1 : r2, c - W0);
       else copy_w(k + WD, 0, r0, c - W0 - NIH);
     };
     constexpr int NP = TM * TH * 4;  // MFMAs of a half
     constexpr int EVERY = NC <= NP ? 2 : 1;
     static_assert(NC <= 2 * NP, "copies");
-    int xn[TM], wnx[2 * TH];
 #pragma unroll
     for (int i = 0; i < 2 * NP; ++i) {
-      const int h = i / NP, g = i % NP / (4 * TM), t = i % (4 * TM) / 4, s = i % 4;
+      // (neighbouring products go to different sums)
+      const int h = i / NP, g = i % NP / (4 * TM), s = i % (4 * TM) / TM, t = i % TM;
       const int a = h * TH + g;
       if (SETS == 2 && i % NP == 0) wf[1 - h][0] = read_w(h == 0 ? r0 + HBUF : r1, 0);
       const i32x8 av = low(wf[SETS == 2 ? h : 0][g].v[s]), bv = low(xf[t].v[s]);
@@ -601,22 +610,17 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
   __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, acc[a][t], 4, 4, S, ws[a], S, xs[t])
       acc[a][t] = s == 0 ? LMOE_MFMA(0) : s == 1 ? LMOE_MFMA(1) : s == 2 ? LMOE_MFMA(2) : LMOE_MFMA(3);
 #undef LMOE_MFMA
-      if (SETS == 1 && t == TM - 1 && s == 3) wf[0][g] = read_w(h == 0 ? r0 + HBUF : r1, g);
-      if (h == 1 && g == TH - 1 && s == 3) {
-        xf[t] = read_x(k + 1, t);
-        xn[t] = read_s(k + 1, wm * (BM / WM) + t * 32);
+      // keeps the product here
+      asm volatile("" : "+v"(acc[a][t]));
+      if (SETS == 1 && t == TM - 1) wf[0][g].v[s] = read_w1(h == 0 ? r0 + HBUF : r1, g, s);
+      if (h == 1 && g == TH - 1) {
+        xf[t].v[s] = read_x1(k + 1, t, s);
+        if (s == 3) xs[t] = read_s(k + 1, wm * (BM / WM) + t * 32);
       }
-      if (h == 1 && i - NP < 2 * TH) {
-        const int b = i - NP;
-        wnx[b] = read_s(k + 1, BM + (b / TH) * BH + wn * (BH / WN) + (b % TH) * 32);
-      }
+      if (t == TM - 1 && s == 3) ws[a] = read_s(k + 1, BM + h * BH + wn * (BH / WN) + g * 32);
       if (i % EVERY == 0 && i / EVERY < NC) copy(i / EVERY);
       __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int t = 0; t < TM; ++t) xs[t] = xn[t];
-#pragma unroll
-    for (int b = 0; b < 2 * TH; ++b) ws[b] = wnx[b];
     r0 = r1;
   };
   if (KL > 2) wait_vmcnt<(WD == 3 ? 4 : 2) * NIH + NIA + NSW>();
