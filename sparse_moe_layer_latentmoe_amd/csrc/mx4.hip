@@ -222,20 +222,13 @@ __device__ __forceinline__ i32x4 mx4_permute(const i32x4& a, const i32x4& b, int
 // of 128 bytes of each row (256 k, eight blocks): lane (r, q) (r = lane % 16,
 // q = lane / 16) takes blocks q and 4 + q of row r, whose scales are byte q of
 // the line's two scale words.
-template <bool GROUPED, int NW, int RG, int U, class OUT>
-__global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(Mx4Gemm p, const Tile* tiles,
-                                                             const int* ntiles) {
+template <int NW, int RG, int U, class OUT>
+__global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(Mx4Gemm p) {
   __shared__ f32x4 red[NW][RG][64];
   const int nblocks = (p.N + 16 * RG - 1) / (16 * RG);
   const int nb = blockIdx.x % nblocks;
   const int tm = blockIdx.x / nblocks;
-  int e = 0, m0 = tm * 16, mcount = min(16, p.M - m0);
-  if (GROUPED) {
-    if (tm >= *ntiles) return;
-    e = uniform(tiles[tm].expert);
-    m0 = uniform(tiles[tm].row0);
-    mcount = uniform(tiles[tm].nrows);
-  }
+  const int m0 = tm * 16, mcount = min(16, p.M - m0);
   const int n0 = nb * (16 * RG);
   const int lane = threadIdx.x & 63;
   const int w = uniform(threadIdx.x >> 6);
@@ -250,7 +243,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(Mx4Gemm p, const Ti
 #pragma unroll
   for (int g = 0; g < RG; ++g) {
     // 16-row groups past N read the last one (N is a multiple of 16)
-    const size_t n = (size_t)e * p.N + min(n0 + g * 16, p.N - 16);
+    const size_t n = min(n0 + g * 16, p.N - 16);
     wa[g] = p.w + (n + lrow) * RB;
     wsp[g] = reinterpret_cast<const uint32_t*>(p.ws) + (n + r16) * SW;
   }
@@ -337,6 +330,144 @@ __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(Mx4Gemm p, const Ti
     for (int v = 1; v < NW; ++v) sm += red[v][g][lane];
     const int n = n0 + g * 16;
     if (r16 < mcount && n < p.N) mx4_store4<OUT>(p, m0 + r16, n + kq * 4, sm);
+  }
+}
+
+// Few tokens a group: as above, but each of the NW waves takes 16 RG weight rows of
+// its own over the whole of k, and everything comes through LDS by direct copies
+// one line (256 values) ahead: a wave's codes (8 rows x 128 bytes a copy, with the
+// non-temporal hint) into its own two slots, the 16 token rows' by the first two
+// waves.  Scales come two lines at a time, 16 bytes of a row, into registers.  One
+// barrier a line.  LDS rows are XOR-swizzled: row r keeps its 16-byte chunk c at c ^
+// (r % 8), rows 8 to 15 of sixteen at c ^ (r % 8) ^ 1.  Work items (tile, row block) are
+// taken XCD-major.
+template <int NW, int RG, class OUT>
+__global__ __launch_bounds__(NW * 64) void mx4_lines_kernel(Mx4Gemm p, const Tile* tiles,
+                                                            const int* ntiles) {
+  constexpr int ROWS = NW * 16 * RG, CSLOT = 16 * RG * 128, TSLOT = 16 * 128;
+  __shared__ __attribute__((aligned(1024))) char smem[NW * 2 * CSLOT + 2 * TSLOT];
+  const int nblocks = (p.N + ROWS - 1) / ROWS;
+  const int nwork = uniform(*ntiles) * nblocks;
+  const int b = blockIdx.x;
+  if (b >= nwork) return;
+  const int per = nwork / kXcds;
+  const int item = b < per * kXcds ? (b % kXcds) * per + b / kXcds : b;
+  const int nb = item % nblocks, tix = item / nblocks;
+  const int e = uniform(tiles[tix].expert), m0 = uniform(tiles[tix].row0);
+  const int mcount = uniform(tiles[tix].nrows);
+  const int lane = threadIdx.x & 63;
+  const int w = uniform(threadIdx.x >> 6);
+  const int r16 = lane & 15, kq = lane >> 4;
+  const int RB = p.K / 2, SW = p.K / 128, LT = (SW + 1) / 2;
+  const int n0 = nb * ROWS + w * 16 * RG;
+  constexpr uint32_t kNone = 0x80000000u;
+
+  // 16-row groups past N read the last one (their columns are not stored)
+  const __amdgpu_buffer_rsrc_t rc = buffer_rsrc(p.w + (size_t)e * p.N * RB);
+  const uint32_t piece = (lane & 7) ^ (lane >> 3);
+  const uint32_t clane = (uint32_t)(lane >> 3) * (uint32_t)RB + piece * 16;
+  char* const cslots = smem + w * 2 * CSLOT;
+  const size_t srow = (size_t)e * p.N * SW * 4;
+  const __amdgpu_buffer_rsrc_t rs =
+      buffer_rsrc(p.ws + srow, (size_t)p.groups * p.N * SW * 4 - srow);
+  uint32_t soff[RG];
+#pragma unroll
+  for (int g = 0; g < RG; ++g)
+    soff[g] = (uint32_t)(min(n0 + g * 16, p.N - 16) + r16) * (uint32_t)SW * 4u;
+
+  // tokens: rows past the tile's count and indices outside x read as 0
+  const bool gather = p.rows != nullptr;
+  const uint8_t* const xbase = gather ? p.x : p.x + (size_t)m0 * RB;
+  const size_t xs0 = gather ? 0 : (size_t)m0 * SW * 4;
+  const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(xbase);
+  const __amdgpu_buffer_rsrc_t rxs = buffer_rsrc(p.xs + xs0, (size_t)p.x_rows * SW * 4 - xs0);
+  auto x_row = [&](int i, bool& ok) -> uint32_t {
+    ok = i < mcount;
+    if (!ok) return 0;
+    return gather ? (uint32_t)mx4_x_row(p, m0 + i, ok) : (uint32_t)i;
+  };
+  char* const tslots = smem + NW * 2 * CSLOT;
+  uint32_t toff = kNone, xsoff = kNone;
+  {
+    bool ok;
+    uint32_t row = x_row(8 * w + (lane >> 3), ok);
+    if (w < 2 && ok) toff = row * (uint32_t)RB + (w ? piece ^ 1u : piece) * 16;
+    row = x_row(r16, ok);
+    if (ok) xsoff = row * (uint32_t)SW * 4u;
+  }
+  auto issue = [&](int l) __attribute__((always_inline)) {
+    // the second half of a half line reads as 0
+    const bool half = 2 * l + 2 > SW;
+    char* const cs = cslots + (l & 1) * CSLOT;
+    const uint32_t a = half && (piece & 4) ? kNone : clane;
+    const uint32_t c = half && (piece & 4) ? kNone : clane ^ 16u;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      const int row = min(n0 + g * 16, p.N - 16);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (lds_void*)(cs + g * 2048), 16, a,
+                                               row * RB + l * 128, 0, 2 /* nt */);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (lds_void*)(cs + g * 2048 + 1024), 16, c,
+                                               (row + 8) * RB + l * 128, 0, 2);
+    }
+    if (w < 2) {
+      const bool none = half && ((w ? piece ^ 1u : piece) & 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rx, (lds_void*)(tslots + (l & 1) * TSLOT + w * 1024), 16, none ? kNone : toff, l * 128, 0,
+          0);
+    }
+  };
+  u32x4 scur[RG], snext[RG], xcur, xnext;
+  auto scales = [&](int l) __attribute__((always_inline)) {
+#pragma unroll
+    for (int g = 0; g < RG; ++g)
+      snext[g] = __builtin_amdgcn_raw_buffer_load_b128(rs, soff[g] + l * 8, 0, 0);
+    xnext = __builtin_amdgcn_raw_buffer_load_b128(rxs, xsoff + l * 8, 0, 0);
+  };
+  f32x4 acc[RG];
+#pragma unroll
+  for (int g = 0; g < RG; ++g) acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  scales(0);
+  issue(0);
+  const int at = (r16 >> 3) * 1024 + (r16 & 7) * 128, sz = (r16 & 7) ^ (r16 >> 3);
+  const int a0 = at + ((kq ^ sz) << 4), a1 = at + (((4 + kq) ^ sz) << 4);
+  for (int l = 0; l < LT; ++l) {
+    // this line's copies (every wave's) have landed, and every wave is done with
+    // the slots that the next line's overwrite
+    wait_vmcnt<0>();
+    stage_barrier_hard();
+    if ((l & 1) == 0) {
+#pragma unroll
+      for (int g = 0; g < RG; ++g) scur[g] = snext[g];
+      xcur = xnext;
+    }
+    if (l + 1 < LT) {
+      issue(l + 1);
+      if (l & 1) scales(l + 1);
+    }
+    const char* const cs = cslots + (l & 1) * CSLOT;
+    const char* const ts = tslots + (l & 1) * TSLOT;
+    const i32x4 x0 = *reinterpret_cast<const i32x4*>(ts + a0);
+    const i32x4 x1 = *reinterpret_cast<const i32x4*>(ts + a1);
+    const uint32_t xw0 = l & 1 ? xcur[2] : xcur[0], xw1 = l & 1 ? xcur[3] : xcur[1];
+    // (a half line's second word is another row's: its values are 0, 1 will do)
+    const bool half = 2 * l + 2 > SW;
+    const int t0 = (int)(xw0 >> (8 * kq)), t1 = half ? 127 : (int)(xw1 >> (8 * kq));
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      const i32x4 c0 = *reinterpret_cast<const i32x4*>(cs + g * 2048 + a0);
+      const i32x4 c1 = *reinterpret_cast<const i32x4*>(cs + g * 2048 + a1);
+      const uint32_t w0 = l & 1 ? scur[g][2] : scur[g][0], w1 = l & 1 ? scur[g][3] : scur[g][1];
+      acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          low(c0), low(x0), acc[g], 4, 4, 0, (int)(w0 >> (8 * kq)), 0, t0);
+      acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          low(c1), low(x1), acc[g], 4, 4, 0, half ? 127 : (int)(w1 >> (8 * kq)), 0, t1);
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < RG; ++g) {
+    const int n = n0 + g * 16;
+    if (r16 < mcount && n < p.N) mx4_store4<OUT>(p, m0 + r16, n + kq * 4, acc[g]);
   }
 }
 
@@ -757,13 +888,13 @@ int grouped_tiles(int rows, int groups, int tile_m) {
 long xcd_grid(long work) { return kXcds * ((work + kXcds - 1) / kXcds); }
 
 // Work-groups and threads of a product's launch.
-constexpr int kGroupedWaves = 4, kGroupedRG = 4, kDenseWaves = 8, kDenseRG = 1;
+constexpr int kGroupedWaves = 4, kGroupedRG = 2, kDenseWaves = 8, kDenseRG = 1;
 long grid_of(const Plan& plan, int M, int N, int groups, int* threads) {
   const long tiles = groups ? grouped_tiles(M, groups, plan.bm) : (M + plan.bm - 1) / plan.bm;
   if (plan.stream) {
-    const int rg = groups ? kGroupedRG : kDenseRG;
+    const int rows = groups ? 16 * kGroupedWaves * kGroupedRG : 16 * kDenseRG;
     *threads = 64 * (groups ? kGroupedWaves : kDenseWaves);
-    return tiles * ((N + 16 * rg - 1) / (16 * rg));
+    return tiles * ((N + rows - 1) / rows);
   }
   const bool small = !groups && plan.bm == 64;
   *threads = small ? 256 : 512;
@@ -780,11 +911,9 @@ hipError_t launch(const Mx4Gemm& p, const Plan& plan, const Tile* tiles, const i
   const dim3 g(grid, p.splits);
   if (plan.stream) {
     if (p.groups)
-      mx4_stream_kernel<true, kGroupedWaves, kGroupedRG, 1, OUT><<<g, threads, 0, s>>>(p, tiles,
-                                                                                      ntiles);
+      mx4_lines_kernel<kGroupedWaves, kGroupedRG, OUT><<<g, threads, 0, s>>>(p, tiles, ntiles);
     else
-      mx4_stream_kernel<false, kDenseWaves, kDenseRG, 2, OUT><<<g, threads, 0, s>>>(p, nullptr,
-                                                                                   nullptr);
+      mx4_stream_kernel<kDenseWaves, kDenseRG, 2, OUT><<<g, threads, 0, s>>>(p);
   } else if (p.groups) {
     if (plan.bm == 64)
       mx4_pipe_kernel<true, 8, 64, 256, 2, 3, OUT><<<g, threads, 0, s>>>(p, tiles, ntiles);
