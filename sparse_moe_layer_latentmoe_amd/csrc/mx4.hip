@@ -178,6 +178,11 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint32_t* __r
 
 namespace {
 
+template <class V>
+__device__ __forceinline__ V pick(bool c, V a, V b) {
+  return c ? a : b;
+}
+
 // A lane's 16 bytes as the instructions' operand (they take the low half).
 __device__ __forceinline__ i32x8 low(i32x4 a) {
   return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -486,8 +491,8 @@ __global__ __launch_bounds__(NW * 64) void mx4_lines_kernel(Mx4Gemm p, const Til
 // half 1 of line k + WD - 1 and half 0 of k + WD.  One barrier a step; the copy
 // instructions are spread over the MFMAs.
 //
-// Scales come four lines at a time (32 bytes of a row), a quarter of the tile's
-// rows with each step.
+// Scales come two lines at a time (16 bytes of a row), half of the tile's rows with
+// each step.
 //
 // Split over k (dense, few tiles): work-group (x, y) computes tile x over the
 // y-th part of the lines and writes fp32 partial sums to part y of `y`.
@@ -500,14 +505,14 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
   constexpr int NIA = BM / RPI / NW, NIH = BH / RPI / NW;  // copies a wave and unit
   constexpr int ABUF = BM * ROWB, HBUF = BH * ROWB;
   constexpr int SROWS = BM + BN;       // rows of scales
-  constexpr int NST = BM / 32, NSB = BN / 32;  // copies of a quarter of four lines' scales
+  constexpr int NST = BM / 32, NSB = BN / 32;  // copies of half of two lines' scales
   constexpr int NSW = 2;               // a wave's with each step (some twice)
   static_assert(NST <= NW && NSB <= NW, "one of each a wave");
   static_assert(TM * 32 * WM == BM && TH * 32 * WN == BH, "whole groups");
   static_assert(NIA * RPI * NW == BM && NIH * RPI * NW == BH, "rows per unit");
   // One LDS array: with several, the compiler tells them apart and then waits
   // for all copies in flight before every LDS read.
-  constexpr int W00 = 2 * ABUF, S00 = W00 + 2 * WD * HBUF, LDS = S00 + 2 * SROWS * 32;
+  constexpr int W00 = 2 * ABUF, S00 = W00 + 2 * WD * HBUF, LDS = S00 + 2 * SROWS * 16;
   static_assert(LDS <= 160 * 1024, "LDS");
   __shared__ __attribute__((aligned(1024))) char smem[LDS];
 
@@ -580,26 +585,26 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
         rb, (lds_void*)(smem + W00 + r + h * HBUF + (w + NW * j) * RPI * ROWB), 16, at,
         fp8_weight_scalar(h * BH + (w + NW * j) * RPI, p.N - n0, k, RB), 0, 0);
   };
-  // Scales of lines 4 g .. 4 g + 3: rows 0 .. BM - 1 are the tokens', then the
-  // weights'.  A copy fills 8 rows, lane l row l / 8, place l % 8, which holds word
-  // (l % 8) ^ 2 (i % 4) of the eight, i the row / 8 (so that 32 rows' reads of a line
-  // meet no bank twice).  With quarter j a wave copies the (w % NST)-th of the quarter
-  // of the tokens' rows and the (w % NSB)-th of the weights'.  Words past K and rows
+  // Scales of lines 2 g and 2 g + 1: rows 0 .. BM - 1 are the tokens', then the
+  // weights'.  A copy fills 16 rows, lane l row l / 4, place l % 4, which holds word
+  // (l % 4) ^ 2 (i % 2) of the four, i the row / 16 (so that 32 rows' reads of a line
+  // meet no bank twice).  With half j a wave copies the (w % NST)-th of that half of
+  // the tokens' rows and the (w % NSB)-th of the weights'.  Words past K and rows
   // that are not there read as 0.
   const __amdgpu_buffer_rsrc_t rxs = buffer_rsrc(gather ? p.xs : p.xs + (size_t)m0 * SW * 4);
   const __amdgpu_buffer_rsrc_t rws = buffer_rsrc(p.ws + ((size_t)e * p.N + n0) * SW * 4);
   const int wt = w % NST, wb = w % NSB;
-  uint32_t so[4];  // the token row's offset
+  uint32_t so[2];  // the token row's offset
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 2; ++j) {
     bool ok;
-    const uint32_t row = x_row(RPI * (j * NST + wt) + lr, ok);
+    const uint32_t row = x_row(16 * (j * NST + wt) + (lane >> 2), ok);
     so[j] = ok ? row * (uint32_t)SW * 4u : kNone;
     asm volatile("" : "+v"(so[j]));
   }
   // (words from the row's start; lines are counted from k0)
   auto word_of = [&](int g, int id) __attribute__((always_inline)) {
-    return (uint32_t)(2 * k0 + 8 * g) + (uint32_t)((lane & 7) ^ ((id & 3) << 1));
+    return (uint32_t)(2 * k0 + 4 * g) + (uint32_t)((lane & 3) ^ ((id & 1) << 1));
   };
   auto copy_st = [&](int g, int j, uint32_t off) __attribute__((always_inline)) {
     const int id = j * NST + wt;
@@ -607,15 +612,15 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
     const uint32_t word = word_of(g, id), sum = off + word * 4u;
     const uint32_t at = word < (uint32_t)SW ? sum : kNone;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rxs, (lds_void*)(smem + S00 + ((g & 1) * SROWS + RPI * id) * 32), 4, at, 0, 0, 0);
+        rxs, (lds_void*)(smem + S00 + ((g & 1) * SROWS + 16 * id) * 16), 4, at, 0, 0, 0);
   };
   auto copy_sw = [&](int g, int j) __attribute__((always_inline)) {
-    const int id = j * NSB + wb, row = RPI * id + lr;
+    const int id = j * NSB + wb, row = 16 * id + (lane >> 2);
     const uint32_t word = word_of(g, id);
     const uint32_t sum = ((uint32_t)row * (uint32_t)SW + word) * 4u;
     const uint32_t at = (n0 + row < p.N) & (word < (uint32_t)SW) ? sum : kNone;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rws, (lds_void*)(smem + S00 + ((g & 1) * SROWS + BM + RPI * id) * 32), 4, at, 0, 0, 0);
+        rws, (lds_void*)(smem + S00 + ((g & 1) * SROWS + BM + 16 * id) * 16), 4, at, 0, 0, 0);
   };
   // what the first MFMAs need, then what step 0 reads, then what it need not
   // wait for
@@ -625,7 +630,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
 #pragma unroll
   for (int j = 0; j < NIH; ++j) copy_w(0, 0, 0, j);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 2; ++j) {
     copy_st(0, j, so[j]);
     copy_sw(0, j);
   }
@@ -685,10 +690,10 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
     return f;
   };
   // the word of scales of row `row` (a multiple of 32 and the lane's) for line k
-  const uint32_t sl = (uint32_t)(S00 + r32 * 32 + kh * 4), sx = (r32 >> 3) & 3;
+  const uint32_t sl = (uint32_t)(S00 + r32 * 16 + kh * 4), sx = r32 >> 4;
   auto read_s = [&](int k, int row) __attribute__((always_inline)) {
-    return *reinterpret_cast<const int*>(smem + sl + ((k >> 2) & 1) * (SROWS * 32) + row * 32 +
-                                         (((k & 3) ^ sx) << 3));
+    return *reinterpret_cast<const int*>(smem + sl + ((k >> 1) & 1) * (SROWS * 16) + row * 16 +
+                                         (((k & 1) ^ sx) << 3));
   };
   Frag xf[TM], wf[SETS][TH];
   int xs[TM], ws[2 * TH];
@@ -707,23 +712,19 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
     else wait_vmcnt<0>();
     wait_lgkmcnt0();
     stage_barrier_hard();
-    // part j of group g of the scales comes with step 4 g - 5 + j, so that group g,
-    // first read in step 4 g - 1, is whole then, and what it replaces, group g - 2,
-    // was last read in step 4 g - 6
+    // half j of group g of the scales comes with step 2 g - 3 + j, so that group g,
+    // first read in step 2 g - 1, is whole then, and what it replaces, group g - 2,
+    // was last read in step 2 g - 4
     constexpr bool XC = COPY == 2 || (COPY == 1 && WD == 3);  // line k + 2 exists
     constexpr int NX = XC ? NIA + NSW : 0;
     constexpr int NC = NX + (COPY == 2 ? 2 * NIH : (COPY == 1 ? NIH : 0));
     constexpr int X0 = WD == 2 ? NC - NX : 0, W0 = WD == 2 ? 0 : NX;
-    const int part = (k + 1) & 3;
-    uint32_t sof = 0;
-    if (XC) {
-      const uint32_t a = part & 1 ? so[1] : so[0], b = part & 1 ? so[3] : so[2];
-      sof = part & 2 ? b : a;
-    }
+    const int part = (k + 1) & 1;
+    const uint32_t sof = pick(part != 0, so[1], so[0]);
     auto copy = [&](int c) __attribute__((always_inline)) {
       if (c >= X0 && c < X0 + NIA && XC) copy_x(k + 2, c - X0);
-      else if (XC && c == X0 + NIA) copy_st((k + 5) >> 2, part, sof);
-      else if (XC && c == X0 + NIA + 1) copy_sw((k + 5) >> 2, part);
+      else if (XC && c == X0 + NIA) copy_st((k + 3) >> 1, part, sof);
+      else if (XC && c == X0 + NIA + 1) copy_sw((k + 3) >> 1, part);
       else if (c < W0 + NIH) copy_w(k + WD - 1, 1, WD == 2 ? r1 : r2, c - W0);
       else copy_w(k + WD, 0, r0, c - W0 - NIH);
     };
@@ -920,7 +921,7 @@ hipError_t launch(const Mx4Gemm& p, const Plan& plan, const Tile* tiles, const i
     else if (plan.bm == 128)
       mx4_pipe_kernel<true, 8, 128, 256, 2, 3, OUT><<<g, threads, 0, s>>>(p, tiles, ntiles);
     else
-      mx4_pipe_kernel<true, 8, 192, 256, 2, 2, OUT><<<g, threads, 0, s>>>(p, tiles, ntiles);
+      mx4_pipe_kernel<true, 8, 192, 256, 2, 3, OUT><<<g, threads, 0, s>>>(p, tiles, ntiles);
   } else {
     if (plan.bm == 64)
       mx4_pipe_kernel<false, 4, 64, 128, 2, 3, OUT><<<g, threads, 0, s>>>(p, nullptr, nullptr);
