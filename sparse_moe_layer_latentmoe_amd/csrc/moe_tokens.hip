@@ -48,14 +48,14 @@ namespace lmoe {
 
 namespace {
 
-constexpr int kWaves = 4, kThreads = kWaves * 64;
+constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kQueues = 16, kSpread = 64;  // counters, ints apart
 constexpr int kRouteHere = 4;              // tokens that every work-group routes
 constexpr int kAhead = 3;                  // lines that a wave loads ahead
 
 // Formats: k values in a line of 128 bytes, fragments of 8 values in 16 bytes,
 // waves that share a row group of 16 (each takes every WK-th line).  Items are 16
-// kWaves / WK rows: 64 KB at K = 2048 in each format; a line of each wave is 256
+// kWaves / WK rows: 128 KB at K = 2048 in each format; a line of each wave is 256
 // values of x.
 template <int FMT>
 struct Fmt;
@@ -748,8 +748,12 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const int turn = 16 / (m.y_bf16 ? 2 : 3);
   const int cols = (m.T < turn ? m.T : turn) * (m.y_bf16 ? 2 : 3);
   const int red = 2 * kThreads * 16, lists = 12 * P + 192;
-  // three work-groups a CU where the rows allow it: 53 KB each
-  const int least = cols * (2048 + 16), left = 52 * 1024 - red - lists - kWaves * 2048;
+  // One work-group a CU (they route all tokens and stage the same rows, each for
+  // itself), or two of them where the routing is done and there is more to read: T = 1
+  // bf16 161 us against 163 (512 experts top-22, 2048 x 5120), MXFP4 76 against 90;
+  // T = 6 FP8 378 against 349, T = 13 MXFP4 (128 experts top-8) 74 against 68.
+  const int room = (here ? 156 : 79) * 1024;
+  const int least = cols * (2048 + 16), left = room - red - lists - kWaves * 2048;
   const int xbytes = (left > least ? left : least) / 16 * 16;
   const int turned = kWaves * 2048, work = xbytes + red + turned;
   MoeParams p{m,
@@ -782,7 +786,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
     e = route_logits(m.r, p.logits, false, m.bias, m.idx, m.weights, s);
     if (e != hipSuccess) return e;
   }
-  constexpr int grid = 768;
+  const int grid = here ? 256 : 512;
   with_format(m.format, [&](auto fmt) {
     constexpr int FMT = decltype(fmt)::value;
     if (nj == 0) moe_tokens_kernel<FMT, 0><<<grid, kThreads, lds, s>>>(p);

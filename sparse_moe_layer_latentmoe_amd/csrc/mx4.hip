@@ -858,8 +858,8 @@ struct DenseTile {
 };
 constexpr DenseTile kDenseTiles[3] = {{256, 256}, {128, 256}, {64, 128}};
 double tile_us(const DenseTile& t, long n) {
-  if (t.bm == 64) return n * (0.34 / 256) > 0.36 ? n * (0.34 / 256) : 0.36;
-  return (double)((n + 255) / 256) * (t.bm == 256 ? 1.65 : 0.96);
+  if (t.bm == 64) return n * (0.6 / 256) > 0.8 ? n * (0.6 / 256) : 0.8;
+  return (double)((n + 255) / 256) * (t.bm == 256 ? 1.7 : 1.0);
 }
 Plan dense_plan(int M, int N, int K) {
   if (M <= 16) return {true, kStreamTileM, 1};
@@ -870,7 +870,7 @@ Plan dense_plan(int M, int N, int K) {
     for (int s = 1; s <= 8; s *= 2) {
       if (s > 1 && lines / s < 4) continue;  // a part is at least four lines
       const long n = (long)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn) * s;
-      double us = tile_us(t, n) * ((lines + s - 1) / s) + 3.4;
+      double us = tile_us(t, n) * ((lines + s - 1) / s) + 8.0;
       if (s > 1) us += 4.0 + (double)s * M * N * 8 / 4e6;
       if (best.bm == 0 || us < least) best = {false, t.bm, s}, least = us;
     }
