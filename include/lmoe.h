@@ -432,7 +432,7 @@ lmoe_status lmoe_fp8_matmul(const lmoe_fp8_matmul_args *a, void *workspace,
  * elements apart), any cols >= 1.  Codes [rows, 16 ceil(cols / 32)], 4-byte
  * aligned, those past cols 0; scales [rows, ceil(cols / 32)].  Same rounding,
  * so the same bits as lmoe_quantize_mxfp4 where that takes x.  Inputs must be
- * finite.  Fewer than 2^30 blocks. */
+ * finite.  Up to 2^30 - 64 blocks, cols up to 2^30. */
 lmoe_status lmoe_quantize_mxfp4_rows(const void *x, int32_t x_type, int64_t rows, int32_t cols,
                                      int64_t x_stride, uint8_t *codes, uint8_t *scales,
                                      void *stream);
@@ -474,7 +474,7 @@ size_t lmoe_mxfp4_matmul_workspace_size(const lmoe_mxfp4_matmul_args *a);
 lmoe_status lmoe_mxfp4_matmul(const lmoe_mxfp4_matmul_args *a, void *workspace,
                               size_t workspace_bytes, void *stream);
 
-/* A whole sparse layer for a few tokens, in two kernels:
+/* A whole sparse layer for a few tokens:
  *   l = x gate^T;  (I, w) = routing of l as by lmoe_route_logits
  *   y = sum_k w_k act(x up[I_k]^T) down[I_k]^T  (+ act(x shared_up^T)
  *       shared_down^T)
@@ -484,7 +484,9 @@ lmoe_status lmoe_mxfp4_matmul(const lmoe_mxfp4_matmul_args *a, void *workspace,
  * not quantised.  Logits are 64-bit sums rounded once to fp32; products and
  * sums are fp32 (the hidden rows are kept in fp32), w_k is applied to an
  * expert's fp32 output, and y rounds once.  Each used expert's weights are
- * read once.  Inputs must be finite. */
+ * read from memory once, whatever the number of its tokens.  The same call gives
+ * the same bits.  Inputs should be finite: what is not stays in its token's row
+ * of y (an infinite value may become NaN there). */
 typedef enum { LMOE_ACT_RELU2 = 0, LMOE_ACT_SWIGLU = 1 } lmoe_activation;
 typedef struct {
   lmoe_router router;
@@ -507,7 +509,7 @@ typedef struct {
   int32_t activation;                /* lmoe_activation */
   int32_t T;                         /* 0..16 */
   int32_t D, F, S;  /* S may be 0; multiples of 64 (bf16) or 128, up to 32768; a
-                       matrix must be below 2^32 bytes */
+                       matrix must be below 2^31 - 16 bytes */
 } lmoe_moe_tokens_args;
 
 /* Bytes of workspace of lmoe_moe_tokens (logits, hidden and output rows,

@@ -52,6 +52,7 @@ constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kQueues = 16, kSpread = 64;  // counters, ints apart
 constexpr int kRouteHere = 4;              // tokens that every work-group routes
 constexpr int kAhead = 3;                  // lines that a wave loads ahead
+constexpr float kBf16Max = 0x1.FEp127f;
 
 // Formats: k values in a line of 128 bytes, fragments of 8 values in 16 bytes,
 // waves that share a row group of 16 (each takes every WK-th line).  Items are 16
@@ -237,7 +238,10 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   }
   __syncthreads();
   for (int i = tid; i < P; i += kThreads) {
-    atomicOr(&smask[sidx[i]], 1u << (i / K));
+    // (whatever a bias that is no number made of it: an expert)
+    const int e = (int)min((uint32_t)sidx[i], (uint32_t)E - 1u);
+    sidx[i] = e;
+    atomicOr(&smask[e], 1u << (i / K));
     if (NJ > 0 && blockIdx.x == 0) {
       m.idx[i] = sidx[i];
       m.weights[i] = sw[i];
@@ -497,7 +501,14 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
               if (q < parts) {
-                const u16x4 b = pack4_bf16(v[j]);
+                // what is rounded to infinity, or is infinite, is the last part's
+                f32x4 c = v[j];
+                if (q + 1 < parts) {
+#pragma unroll
+                  for (int n = 0; n < 4; ++n)
+                    c[n] = __builtin_amdgcn_fmed3f(c[n], -kBf16Max, kBf16Max);
+                }
+                const u16x4 b = pack4_bf16(c);
                 *reinterpret_cast<u16x4*>(to + q * pitch + kj * 2) = b;
 #pragma unroll
                 for (int n = 0; n < 4; ++n) v[j][n] -= bf16_to_f32(b[n]);
@@ -624,7 +635,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
           if (live && q < 2) put4_shared(hrow + group * 8 + 4 * q, o);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = relu_sq(v[i]);
+          for (int i = 0; i < 4; ++i) o[i] = v[i] < 0.f ? 0.f : v[i] * v[i];
           if (live) put4_shared(hrow + group * 16 + 4 * q, o);
         }
       } else if (live) {

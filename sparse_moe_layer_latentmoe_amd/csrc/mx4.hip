@@ -367,18 +367,20 @@ __global__ __launch_bounds__(NW * 64) void mx4_lines_kernel(Mx4Gemm p, const Til
   const int n0 = nb * ROWS + w * 16 * RG;
   constexpr uint32_t kNone = 0x80000000u;
 
-  // 16-row groups past N read the last one (their columns are not stored)
-  const __amdgpu_buffer_rsrc_t rc = buffer_rsrc(p.w + (size_t)e * p.N * RB);
+  // Offsets are from the wave's first row (a matrix may be larger than a buffer).
+  // 16-row groups past N read the last one (their columns are not stored).
+  const int base = min(n0, p.N - 16);
+  const __amdgpu_buffer_rsrc_t rc = buffer_rsrc(p.w + ((size_t)e * p.N + base) * RB);
   const uint32_t piece = (lane & 7) ^ (lane >> 3);
   const uint32_t clane = (uint32_t)(lane >> 3) * (uint32_t)RB + piece * 16;
   char* const cslots = smem + w * 2 * CSLOT;
-  const size_t srow = (size_t)e * p.N * SW * 4;
+  const size_t srow = ((size_t)e * p.N + base) * SW * 4;
   const __amdgpu_buffer_rsrc_t rs =
       buffer_rsrc(p.ws + srow, (size_t)p.groups * p.N * SW * 4 - srow);
   uint32_t soff[RG];
 #pragma unroll
   for (int g = 0; g < RG; ++g)
-    soff[g] = (uint32_t)(min(n0 + g * 16, p.N - 16) + r16) * (uint32_t)SW * 4u;
+    soff[g] = (uint32_t)(min(n0 + g * 16, p.N - 16) - base + r16) * (uint32_t)SW * 4u;
 
   // tokens: rows past the tile's count and indices outside x read as 0
   const bool gather = p.rows != nullptr;
@@ -408,7 +410,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_lines_kernel(Mx4Gemm p, const Til
     const uint32_t c = half && (piece & 4) ? kNone : clane ^ 16u;
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
-      const int row = min(n0 + g * 16, p.N - 16);
+      const int row = min(n0 + g * 16, p.N - 16) - base;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (lds_void*)(cs + g * 2048), 16, a,
                                                row * RB + l * 128, 0, 2 /* nt */);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (lds_void*)(cs + g * 2048 + 1024), 16, c,

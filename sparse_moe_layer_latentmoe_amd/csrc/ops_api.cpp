@@ -147,6 +147,8 @@ lmoe_status check_quantize(const void* x, int32_t type, int64_t rows, int64_t co
 
 // Largest element count of an array whose work-groups a launch can number.
 constexpr int64_t kMaxElements = int64_t{1} << 40;
+// Blocks of 32 that a launch can number: four threads each, fewer than 2^32.
+constexpr int64_t kMaxBlocks = (int64_t{1} << 30) - 64;
 
 // Host-side checks that do not need the workspace.
 lmoe_status check_fp8(const lmoe_fp8_matmul_args* a) {
@@ -214,6 +216,7 @@ bool mxfp4_disjoint(const lmoe_mxfp4_matmul_args& a, const void* workspace, size
 }
 
 constexpr int32_t kFewTokens = 16, kFewWidth = 32768;
+constexpr int64_t kMaxBuffer = 0x7FFFFFF0;  // bytes that a buffer descriptor covers
 
 // Codes and scales of [rows, cols] in an expert format.
 int64_t code_bytes(int32_t format, int64_t rows, int64_t cols) {
@@ -246,8 +249,7 @@ lmoe_status check_few_sizes(const lmoe_moe_tokens_args* a) {
     if (n % step || n > kFewWidth) return LMOE_ERR_UNSUPPORTED;
   const int64_t two = a->activation == LMOE_ACT_SWIGLU ? 2 : 1;
   for (int32_t n : {a->F, a->S})
-    if (code_bytes(a->expert_format, two * n, a->D) >= (int64_t{1} << 32))
-      return LMOE_ERR_UNSUPPORTED;
+    if (code_bytes(a->expert_format, two * n, a->D) >= kMaxBuffer) return LMOE_ERR_UNSUPPORTED;
   return LMOE_OK;
 }
 
@@ -505,8 +507,7 @@ lmoe_status lmoe_quantize_mxfp4_rows(const void* x, int32_t x_type, int64_t rows
   if (rows > kMaxElements / cols || x_stride > (int64_t{1} << 31)) return LMOE_ERR_UNSUPPORTED;
   if (rows == 0) return LMOE_OK;
   const int64_t nb = (static_cast<int64_t>(cols) + 31) / 32, el = type_size(x_type);
-  // a launch has fewer than 2^32 threads: four to a block
-  if (rows * nb >= (int64_t{1} << 30)) return LMOE_ERR_UNSUPPORTED;
+  if (rows * nb > kMaxBlocks || cols > (1 << 30)) return LMOE_ERR_UNSUPPORTED;
   if (!x || !codes || !scales || !aligned(x, el) || !aligned(codes, 4))
     return LMOE_ERR_INVALID_ARG;
   if (!disjoint({{x, strided(rows, x_stride, cols, el)}},
@@ -522,7 +523,7 @@ lmoe_status lmoe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, i
   if (rows > kMaxElements / cols) return LMOE_ERR_UNSUPPORTED;
   if (rows == 0) return LMOE_OK;
   const int64_t nb = (static_cast<int64_t>(cols) + 31) / 32, el = type_size(y_type);
-  if (rows * nb >= (int64_t{1} << 30)) return LMOE_ERR_UNSUPPORTED;
+  if (rows * nb > kMaxBlocks || cols > (1 << 30)) return LMOE_ERR_UNSUPPORTED;
   if (!codes || !scales || !y || !aligned(codes, 4) || !aligned(y, el))
     return LMOE_ERR_INVALID_ARG;
   if (!disjoint({{codes, rows * nb * 16}, {scales, rows * nb}}, {{y, rows * cols * el}}))

@@ -237,3 +237,49 @@ def test_agrees_with_routing_and_grouped_products():
                        out_dtype=F)
     z = torch.zeros(T, D, device=DEV).index_add_(0, order // K, o * w.flatten()[order][:, None])
     assert float((z - y).norm() / y.norm()) < 2.0 ** -4
+
+
+@pytest.mark.parametrize("out", [F, B])
+def test_rows_that_are_not_finite_stay_alone(out):
+    for T in (4, 11):                     # routed in the kernel and before it
+        layer = Layer(40, 5, 256, 128, S=128, seed=3)
+        x = rand(T, 256, seed=4)
+        want = layer(x, out)
+        x[1] = float("nan")
+        x[3, 7] = float("inf")
+        got = layer(x, out)
+        keep = [t for t in range(T) if t not in (1, 3)]
+        # a token's own sums are the same whoever shares its experts
+        assert all(torch.equal(a[keep], b[keep]) for a, b in zip(got, want))
+        assert bool(got[0][1].isnan().all()) and not bool(got[0][3].isfinite().any())
+        i = got[1]
+        assert bool((i >= 0).all()) and bool((i < 40).all()) and bool((i[:, 1:] > i[:, :-1]).all())
+
+
+def test_values_next_to_the_largest():
+    """x that rounds to infinity in bf16: its parts do not."""
+    layer = Layer(8, 2, 128, 64, seed=3, swiglu=True, bias=False)
+    big = torch.finfo(F).max
+    layer.up = (layer.up[0] * 0, None, layer.up[2] * 0)
+    layer.up[0][:, :64, 0] = layer.up[0][:, 64:, 1] = 2.0 ** -120
+    layer.up[2][:, :64, 0] = layer.up[2][:, 64:, 1] = 2.0 ** -120
+    x = torch.zeros(5, 128, device=DEV)
+    x[:, 0], x[:, 1] = big, -big
+    layer.gate = layer.gate * 2.0 ** -60
+    layer.check(x, out=F)
+    layer.check(x, out=B)
+
+
+def test_a_bias_that_is_not_finite_stays_in_bounds():
+    layer = Layer(200, 6, 128, 64, seed=3)
+    x = rand(13, 128, seed=4)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        layer.bias = rand(200, seed=1)
+        layer.bias[::3] = bad
+        for T in (1, 4, 13):
+            y, idx, w = layer(x[:T])
+            assert bool((idx >= 0).all()) and bool((idx < 200).all())
+    layer.bias = torch.full((200,), float("nan"), device=DEV)
+    for T in (1, 4, 13):
+        layer(x[:T])
+    torch.cuda.synchronize()

@@ -286,3 +286,23 @@ def test_experts_in_four_bits_end_to_end():
     # K products rounded and added in fp32 on top of the product's own bound
     ok = ((H // 64 + 8) * 2.0 ** -22 + (K + 2) * 2.0 ** -24) * my
     assert np.all(np.abs(y.double().cpu().numpy() - wy) <= ok)
+
+
+def test_matrices_larger_than_a_buffer_of_32_bits():
+    """Three groups of 2^31 + bytes of codes each (4.3 GB, 8.6 GB and more away), few
+    and many rows a group: the last columns against the same rows alone."""
+    N, K, G = 65536 + 48, 65536, 3
+    xc, xs = pkg.quantize_mxfp4_rows(rand(300, K, seed=1, dtype=B))
+    wc = torch.zeros(G, N, K // 2, dtype=torch.uint8, device=DEV)
+    ws = torch.full((G, N, K // 32), 120, dtype=torch.uint8, device=DEV)
+    part, scales = pkg.quantize_mxfp4_rows(rand(64, K, seed=2, dtype=B))
+    wc[:, -64:], ws[:, -64:] = part, scales
+    xd, wd = (pkg.dequantize_mxfp4(*q, out_dtype=F).double() for q in ((xc, xs), (part, scales)))
+    want, mag = xd @ wd.t(), xd.abs() @ wd.abs().t()
+    ok = (K // 64 + 8) * 2.0 ** -22 * (1 + 2.0 ** -8) * mag + 2.0 ** -8 * want.abs()
+    for counts in ([2, 1, 3], [60, 100, 40]):
+        M = sum(counts)
+        off = torch.tensor(offsets_of(counts), dtype=torch.int32, device=DEV)
+        y = pkg.mxfp4_matmul(xc[:M], xs[:M], wc, ws, off)
+        assert not bool(y[:, :-64].any())
+        assert bool(((y[:, -64:].double() - want[:M]).abs() <= ok[:M]).all())
