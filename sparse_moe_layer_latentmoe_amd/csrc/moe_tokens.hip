@@ -209,9 +209,11 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
 
   // ---- routing and the list of used experts, in every work-group ----
   int pending = 0;
-  if (tid == 0)
-    pending = __hip_atomic_fetch_add(p.queues + queue * kSpread, 1, __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_AGENT);
+  if (tid == 0) {
+    int at = queue * kSpread;
+    asm volatile("" : "+v"(at));  // (of one known address, the result is waited for here)
+    pending = __hip_atomic_fetch_add(p.queues + at, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
   int* const stick = reinterpret_cast<int*>(smem + p.misc);     // [2][2] drawn runs
   int* const scount = stick + 4;                                // [kWaves]
   float* const sw = reinterpret_cast<float*>(scount + kWaves);  // [P] pairs' weights

@@ -161,9 +161,16 @@ __device__ __forceinline__ void route_token(const LT* lp, const float* bias, con
 
   float l[NJ], s[NJ], b[NJ];
   uint32_t key[NJ];
+  // All loads at once (past E: the last expert's again).  Behind a condition each
+  // would be waited for before the next is issued.
 #pragma unroll
-  for (int j = 0; j < NJ; ++j)
-    l[j] = j * 64 + lane < E ? clean_logit(route_load(lp + j * 64 + lane)) : -INFINITY;
+  for (int j = 0; j < NJ; ++j) {
+    const int e = min(j * 64 + lane, E - 1);
+    l[j] = route_load(lp + e);
+    b[j] = bias ? bias[e] : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) l[j] = j * 64 + lane < E ? clean_logit(l[j]) : -INFINITY;
   float m = 0.f, inv = 1.f;
   if (p.softmax) {
     m = l[0];
@@ -196,7 +203,7 @@ __device__ __forceinline__ void route_token(const LT* lp, const float* bias, con
   for (int j = 0; j < NJ; ++j) {
     const int e = j * 64 + lane;
     const bool on = l[j] > -INFINITY;
-    b[j] = on ? (bias ? s[j] + bias[e] : s[j]) : -INFINITY;
+    b[j] = on ? (bias ? s[j] + b[j] : s[j]) : -INFINITY;
     key[j] = e < E ? (on ? key32(bias ? b[j] : l[j]) : kKeyMinusInf) : 0u;
   }
 
