@@ -52,6 +52,7 @@ constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kQueues = 16, kSpread = 64;  // counters, ints apart
 constexpr int kRouteHere = 4;              // tokens that every work-group routes
 constexpr int kAhead = 3;                  // lines that a wave loads ahead
+constexpr int kLogitTokens = 4;            // tokens of a work-group of the first kernel
 constexpr float kBf16Max = 0x1.FEp127f;
 
 // Formats: k values in a line of 128 bytes, fragments of 8 values in 16 bytes,
@@ -79,6 +80,8 @@ template <class V>
 __device__ __forceinline__ V pick(bool c, V a, V b) {
   return c ? a : b;
 }
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 struct MoeParams {
   MoeTokens m;
@@ -128,42 +131,40 @@ __device__ __forceinline__ void stores_done() {
 
 }  // namespace
 
-// Logits: a work-group an expert, products and sums in 64 bits.
+// Logits: a work-group an expert and four tokens, products and sums in 64 bits.
 template <class GT, class XT>
 __global__ __launch_bounds__(256) void moe_logits_kernel(const XT* __restrict__ x, long x_stride,
                                                          const GT* __restrict__ gate, int T, int E,
                                                          int D, float* __restrict__ logits,
                                                          int32_t* __restrict__ sync, int nsync) {
-  constexpr int TB = 8;
+  constexpr int TB = kLogitTokens;
   __shared__ double part[4][TB];
-  const int e = blockIdx.x, tid = threadIdx.x;
-  for (int i = e * 256 + tid; i < nsync; i += E * 256) sync[i] = 0;
-  for (int t0 = 0; t0 < T; t0 += TB) {
-    double acc[TB];
+  const int e = blockIdx.x, tid = threadIdx.x, t0 = blockIdx.y * TB;
+  if (t0 == 0)
+    for (int i = e * 256 + tid; i < nsync; i += E * 256) sync[i] = 0;
+  double acc[TB];
 #pragma unroll
-    for (int u = 0; u < TB; ++u) acc[u] = 0.0;
-    for (int k = tid * 4; k < D; k += 1024) {
-      const f32x4 g = load4(gate + (size_t)e * D + k);
-#pragma unroll
-      for (int u = 0; u < TB; ++u) {
-        if (t0 + u >= T) break;
-        const f32x4 v = load4(x + (t0 + u) * x_stride + k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[u] = fma((double)g[i], (double)v[i], acc[u]);
-      }
-    }
+  for (int u = 0; u < TB; ++u) acc[u] = 0.0;
+  for (int k = tid * 4; k < D; k += 1024) {
+    const f32x4 g = load4(gate + (size_t)e * D + k);
 #pragma unroll
     for (int u = 0; u < TB; ++u) {
       if (t0 + u >= T) break;
-      const double s = wave_sum(acc[u]);
-      if ((tid & 63) == 0) part[tid >> 6][u] = s;
+      const f32x4 v = load4(x + (t0 + u) * x_stride + k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[u] = fma((double)g[i], (double)v[i], acc[u]);
     }
-    __syncthreads();
-    if (tid < TB && t0 + tid < T)
-      logits[(size_t)(t0 + tid) * E + e] =
-          (float)(part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid]);
-    __syncthreads();
   }
+#pragma unroll
+  for (int u = 0; u < TB; ++u) {
+    if (t0 + u >= T) break;
+    const double s = wave_sum(acc[u]);
+    if ((tid & 63) == 0) part[tid >> 6][u] = s;
+  }
+  __syncthreads();
+  if (tid < TB && t0 + tid < T)
+    logits[(size_t)(t0 + tid) * E + e] =
+        (float)(part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid]);
 }
 
 namespace {
@@ -468,56 +469,60 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   };
 
   // The item's tokens' rows (x, or hidden rows), values k0 .. k0 + kn - 1, into
-  // LDS as `parts` bf16 numbers each; zeros from K on.
+  // LDS as `parts` bf16 numbers each; zeros from K on.  A wave takes 256 values of a
+  // row at a time and has N such pieces, of whichever rows, in flight (one row
+  // after the other would wait for memory once a row).
   auto put_rows = [&](const Item& it, int r0, int rows, int k0, int kn, int pitch, int parts)
                       __attribute__((always_inline)) {
-    const bool sh = it.u < nsh;
+    const bool sh = it.u < nsh, down = it.down;
     constexpr int N = 5;
+    const uint32_t pieces = (kn + 255) >> 8, all = rows * pieces;  // at most 2^11
+    const uint32_t per_row = 0xFFFFFFFFu / pieces + 1;             // (0 of one piece)
+    auto row_of = [&](uint32_t c) __attribute__((always_inline)) {
+      return pieces == 1 ? c : __umulhi(c, per_row);
+    };
 #pragma unroll 1
-    for (int r = 0; r < rows; ++r) {
-      const int pair = uniform(sh ? r0 + r : slist[r0 + r]);
-      const size_t row = it.down || sh ? pair : pair / K;
-      const float* const hp = pick(sh, p.hs, p.h) + row * it.K;
-      const size_t xo = row * m.x_stride;
-      char* const to = smem + r * parts * pitch;
+    for (uint32_t c0 = w; c0 < all; c0 += N * kWaves) {
+      f32x4 v[N];
+      const float* hp[N];
+      size_t xo[N];
+      uint32_t at[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        // (past the last: the last again, which is not put)
+        const uint32_t c = min(c0 + j * kWaves, all - 1), r = row_of(c);
+        const int pair = uniform(sh ? r0 + (int)r : (int)slist[r0 + r]);
+        hp[j] = pick(sh, p.hs, p.h) + (size_t)pair * it.K;
+        xo[j] = (size_t)(sh ? pair : pair / K) * m.x_stride;
+        at[j] = min(k0 + (int)(c - r * pieces) * 256 + lane * 4, it.K - 4);
+      }
+      if (down) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = get4_shared(hp[j] + at[j]);
+      } else if (m.x_bf16) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = load4(static_cast<const uint16_t*>(m.x) + xo[j] + at[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = load4(static_cast<const float*>(m.x) + xo[j] + at[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t c = c0 + j * kWaves, r = row_of(c);
+        const int k = (int)(c - r * pieces) * 256 + lane * 4;
+        if (c >= all || k >= kn) continue;
+        char* to = smem + r * parts * pitch + k * 2;
+        f32x4 u = k0 + k < it.K ? v[j] : f32x4{0.f, 0.f, 0.f, 0.f};
+        // what is rounded to infinity, or is infinite, is the last part's
 #pragma unroll 1
-      for (int k = tid * 4; k < kn; k += N * kThreads * 4) {
-        f32x4 v[N];
-        // (past the row's end: its last values again, which are not put)
-        const auto at = [&](int j) { return (uint32_t)min(k0 + k + j * kThreads * 4, it.K - 4); };
-        if (it.down) {
+        for (int q = 1; q < parts; ++q, to += pitch) {
 #pragma unroll
-          for (int j = 0; j < N; ++j) v[j] = get4_shared(hp + at(j));
-        } else if (m.x_bf16) {
-#pragma unroll
-          for (int j = 0; j < N; ++j) v[j] = load4(static_cast<const uint16_t*>(m.x) + xo + at(j));
-        } else {
-#pragma unroll
-          for (int j = 0; j < N; ++j) v[j] = load4(static_cast<const float*>(m.x) + xo + at(j));
+          for (int n = 0; n < 4; ++n) v[j][n] = __builtin_amdgcn_fmed3f(u[n], -kBf16Max, kBf16Max);
+          const bf16x4 b = __builtin_convertvector(v[j], bf16x4);
+          *reinterpret_cast<bf16x4*>(to) = b;
+          u -= __builtin_convertvector(b, f32x4);
         }
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int kj = k + j * kThreads * 4;
-          if (k0 + kj >= it.K) v[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if (kj < kn) {
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-              if (q < parts) {
-                // what is rounded to infinity, or is infinite, is the last part's
-                f32x4 c = v[j];
-                if (q + 1 < parts) {
-#pragma unroll
-                  for (int n = 0; n < 4; ++n)
-                    c[n] = __builtin_amdgcn_fmed3f(c[n], -kBf16Max, kBf16Max);
-                }
-                const u16x4 b = pack4_bf16(c);
-                *reinterpret_cast<u16x4*>(to + q * pitch + kj * 2) = b;
-#pragma unroll
-                for (int n = 0; n < 4; ++n) v[j][n] -= bf16_to_f32(b[n]);
-              }
-            }
-          }
-        }
+        *reinterpret_cast<bf16x4*>(to) = __builtin_convertvector(u, bf16x4);
       }
     }
   };
@@ -785,7 +790,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   auto logits = [&](auto g, auto x) {
     using GT = decltype(g);
     using XT = decltype(x);
-    moe_logits_kernel<GT, XT><<<E, 256, 0, s>>>(
+    moe_logits_kernel<GT, XT><<<dim3(E, (m.T + kLogitTokens - 1) / kLogitTokens), 256, 0, s>>>(
         static_cast<const XT*>(m.x), m.x_stride, static_cast<const GT*>(m.gate), m.T, E, m.D,
         p.logits, sync, l.nsync);
   };
