@@ -620,7 +620,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_pipe_kernel(Mx4Gemm p, const Tile
     const int id = j * NSB + wb, row = 16 * id + (lane >> 2);
     const uint32_t word = word_of(g, id);
     const uint32_t sum = ((uint32_t)row * (uint32_t)SW + word) * 4u;
-    const uint32_t at = (n0 + row < p.N) & (word < (uint32_t)SW) ? sum : kNone;
+    const uint32_t at = ((n0 + row < p.N) & (word < (uint32_t)SW)) ? sum : kNone;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rws, (lds_void*)(smem + S00 + ((g & 1) * SROWS + BM + 16 * id) * 16), 4, at, 0, 0, 0);
   };
