@@ -853,18 +853,25 @@ Plan grouped_plan(int rows, int groups) {
   return {false, bm[best], 1};
 }
 
-// Dense: up to 16 rows stream the weights.  Above that the tile shape and the
-// split of k with the least estimated time.
+// Dense: the tile shape and the split of k with the least estimated time, or, up to
+// 16 rows, the stream where that is less.  Estimates are lines of measurements (N x K
+// weights in MB, a call of M rows): the stream 42 MB 12.1 us at M = 1, 16.5 at 8, 20.2
+// at 16; 134 MB (16384 x 16384) 30.1, 40.9, 50.0 (each work-group reads all tokens for 16
+// weight rows); 8 MB 7.6 to 8.6.  The tiles at any M up to 64: 42 MB 16.2, 134 MB 27.4,
+// 8 MB 10.7 to 11.8 (k split in most, and added up by a second kernel).
 struct DenseTile {
   int bm, bn;
 };
 constexpr DenseTile kDenseTiles[3] = {{256, 256}, {128, 256}, {64, 128}};
+// A line of n tiles (all at once, as far as there are CUs).
 double tile_us(const DenseTile& t, long n) {
   if (t.bm == 64) return n * (0.6 / 256) > 0.8 ? n * (0.6 / 256) : 0.8;
   return (double)((n + 255) / 256) * (t.bm == 256 ? 1.7 : 1.0);
 }
+double stream_us(int M, int N, int K) {
+  return 7.5 + 0.5e-6 * N * K * (0.196 + 0.011 * (M - 1));
+}
 Plan dense_plan(int M, int N, int K) {
-  if (M <= 16) return {true, kStreamTileM, 1};
   const int lines = (K + 255) / 256;
   Plan best{};
   double least = 0;
@@ -877,6 +884,7 @@ Plan dense_plan(int M, int N, int K) {
       if (best.bm == 0 || us < least) best = {false, t.bm, s}, least = us;
     }
   }
+  if (M <= 16 && stream_us(M, N, K) < least) best = {true, kStreamTileM, 1};
   return best;
 }
 
