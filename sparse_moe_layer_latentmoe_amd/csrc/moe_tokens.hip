@@ -50,7 +50,6 @@ namespace {
 
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kQueues = 16, kSpread = 64;  // counters, ints apart
-constexpr int kRouteHere = 4;              // tokens that every work-group routes
 constexpr int kAhead = 3;                  // lines that a wave loads ahead
 constexpr int kLogitTokens = 4;            // tokens of a work-group of the first kernel
 constexpr float kBf16Max = 0x1.FEp127f;
@@ -223,16 +222,19 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   uint16_t* const sexp = slist + P;
   uint16_t* const sstart = sexp + P + 16;
   uint16_t* const srows = sstart + P + 16;
-  constexpr int ROUTE = kRouteHere * (256 + NJ * 512);
+  constexpr int ROUTE = kWaves * (256 + NJ * 512);
   uint32_t* const smask = reinterpret_cast<uint32_t*>(smem + ROUTE);  // [E] tokens
   uint32_t* const sfirst = smask + E;                                 // [E]
   int32_t* const sidx = reinterpret_cast<int32_t*>(sfirst + E);       // [P]
   for (int i = tid; i < E; i += kThreads) smask[i] = 0;
   if constexpr (NJ > 0) {
-    if (w < T)
-      route_token<float, NJ>(p.logits + (size_t)w * E, m.bias, m.r, lane,
+    for (int t = w; t < T; t += kWaves) {
+      route_token<float, NJ>(p.logits + (size_t)t * E, m.bias, m.r, lane,
                              reinterpret_cast<float*>(smem + w * 256),
-                             smem + kRouteHere * 256 + w * NJ * 512, sidx + w * K, sw + w * K);
+                             smem + kWaves * 256 + w * NJ * 512, sidx + t * K, sw + t * K);
+      if (NJ > 2) break;  // (up to four tokens)
+      wave_lds_fence();
+    }
   } else {
     for (int i = tid; i < P; i += kThreads) {
       sidx[i] = m.idx[i];
@@ -663,27 +665,29 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
             before = __hip_atomic_fetch_add(p.down_done + ((i - nup) % nd * WR + wr) * kSpread, 1,
                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
           // Where all pairs' rows of a block's columns are there, they are added: a
-          // lane every fourth of a token's, then the four sums.
+          // lane a column of one of four tokens, or every second or fourth row of it
+          // where there are two tokens or one.
+          const int G = T == 1 ? 4 : T == 2 ? 2 : 1, part = kq & (G - 1);
           for (uint64_t done = __ballot(i < end && before == nexp - 1); done; done &= done - 1) {
             const int n0 = ((run + __builtin_ctzll(done) - nup) % nd * WR + wr) * 16;
+            const float* const at = p.o + n0 + r16;
 #pragma unroll 1
-            for (int t = 0; t < T; ++t) {
-              const float* const at = p.o + n0 + r16;
-              float s = 0.f;
+            for (int t0 = 0; t0 < T; t0 += 4 / G) {
+              const int t = t0 + (G == 1 ? kq : G == 2 ? kq >> 1 : 0), tr = min(t, T - 1);
+              float s = S > 0 && part == 0 ? get1_shared(at + (size_t)(P + tr) * D) : 0.f;
 #pragma unroll 1
-              for (int k0 = kq; k0 < K; k0 += 32) {
+              for (int k0 = part; k0 - part < K; k0 += 8 * G) {
                 float a[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  a[i] = get1_shared(at + (size_t)(t * K + min(k0 + 4 * i, K - 1)) * D);
+                  a[i] = get1_shared(at + (size_t)(tr * K + min(k0 + G * i, K - 1)) * D);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s += k0 + 4 * i < K ? a[i] : 0.f;
+                for (int i = 0; i < 8; ++i) s += k0 + G * i < K ? a[i] : 0.f;
               }
-              if (S > 0 && kq == 3) s += get1_shared(at + (size_t)(P + t) * D);
-              s += __shfl_xor(s, 16, 64);
-              s += __shfl_xor(s, 32, 64);
-              const size_t to = (size_t)t * D + n0 + r16;
-              if (kq == 0) {
+              if (G > 1) s += __shfl_xor(s, 16, 64);
+              if (G > 2) s += __shfl_xor(s, 32, 64);
+              if (part == 0 && t < T) {
+                const size_t to = (size_t)t * D + n0 + r16;
                 if (m.y_bf16) static_cast<uint16_t*>(m.y)[to] = f32_to_bf16(s);
                 else static_cast<float*>(m.y)[to] = s;
               }
@@ -760,9 +764,9 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const int P = m.T * m.r.K, E = m.r.E;
   // LDS: the tokens' rows and the waves' sums, in whose room the tokens are
   // routed before; then the lists
-  const bool here = m.T <= kRouteHere && E <= 512;
+  const bool few = m.T <= 4, here = E <= 128 || (E <= 512 && few);
   const int nj = !here ? 0 : (E <= 128 ? 2 : 8);
-  const int route = kRouteHere * (256 + nj * 512) + 8 * E + 4 * P;
+  const int route = kWaves * (256 + nj * 512) + 8 * E + 4 * P;
   const int turn = 16 / (m.y_bf16 ? 2 : 3);
   const int cols = (m.T < turn ? m.T : turn) * (m.y_bf16 ? 2 : 3);
   const int red = 2 * kThreads * 16, lists = 12 * P + 192;
@@ -770,7 +774,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   // itself), or two of them where the routing is done and there is more to read: T = 1
   // bf16 161 us against 163 (512 experts top-22, 2048 x 5120), MXFP4 76 against 90;
   // T = 6 FP8 378 against 349, T = 13 MXFP4 (128 experts top-8) 74 against 68.
-  const int room = (here ? 156 : 79) * 1024;
+  const int room = (few ? 156 : 79) * 1024;
   const int least = cols * (2048 + 16), left = room - red - lists - kWaves * 2048;
   const int xbytes = (left > least ? left : least) / 16 * 16;
   const int turned = kWaves * 2048, work = xbytes + red + turned;
@@ -804,7 +808,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
     e = route_logits(m.r, p.logits, false, m.bias, m.idx, m.weights, s);
     if (e != hipSuccess) return e;
   }
-  const int grid = here ? 256 : 512;
+  const int grid = few ? 256 : 512;
   with_format(m.format, [&](auto fmt) {
     constexpr int FMT = decltype(fmt)::value;
     if (nj == 0) moe_tokens_kernel<FMT, 0><<<grid, kThreads, lds, s>>>(p);
