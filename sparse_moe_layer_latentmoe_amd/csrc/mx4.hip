@@ -110,9 +110,9 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T* __restrict__
                                                            int cols, long stride, int nb,
                                                            uint32_t* __restrict__ codes,
                                                            uint8_t* __restrict__ scales) {
-  const long b = (long)blockIdx.x * 64 + threadIdx.x / 4;
-  if (b >= rows * nb) return;  // whole groups of four lanes
-  const long row = b / nb;
+  const uint32_t b = blockIdx.x * 64 + threadIdx.x / 4;  // (fewer than 2^30)
+  if (b >= (uint32_t)(rows * nb)) return;                // whole groups of four lanes
+  const uint32_t row = b / (uint32_t)nb;
   const int i = threadIdx.x & 3;
   float v[8];
   mx4_load8<VEC>(x + row * stride, (int)(b - row * nb) * 32 + i * 8, cols, v);
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T* __restrict__
   m = fmaxf(m, __shfl_xor(m, 1, 64));
   m = fmaxf(m, __shfl_xor(m, 2, 64));
   const int e = mx4_exponent(m);
-  codes[b * 4 + i] = mx4_pack8(v, e);
+  codes[(size_t)b * 4 + i] = mx4_pack8(v, e);
   if (i == 0) scales[b] = (uint8_t)(e + 127);
 }
 
@@ -132,13 +132,13 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint32_t* __r
                                                              const uint8_t* __restrict__ scales,
                                                              long rows, int cols, int nb,
                                                              T* __restrict__ y) {
-  const long b = (long)blockIdx.x * 64 + threadIdx.x / 4;
-  if (b >= rows * nb) return;
-  const long row = b / nb;
+  const uint32_t b = blockIdx.x * 64 + threadIdx.x / 4;
+  if (b >= (uint32_t)(rows * nb)) return;
+  const uint32_t row = b / (uint32_t)nb;
   const int i = threadIdx.x & 3;
   const int c = (int)(b - row * nb) * 32 + i * 8;
   if (c >= cols) return;
-  const uint32_t w = codes[b * 4 + i];
+  const uint32_t w = codes[(size_t)b * 4 + i];
   const float s = e8m0_value(scales[b]);
   float v[8];
 #pragma unroll
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint32_t* __r
                        : ((q & 1u) ? 0.5f : 0.f);
     v[j] = ((q & 8u) ? -a : a) * s;
   }
-  T* yp = y + row * cols + c;
+  T* yp = y + (size_t)row * cols + c;
   if constexpr (std::is_same<T, float>::value) {
     if (VEC && c + 8 <= cols) {
       *reinterpret_cast<f32x4*>(yp) = f32x4{v[0], v[1], v[2], v[3]};
