@@ -10,9 +10,17 @@
 // the weights' stream starts early and never pauses.  Two kernels: the first
 // computes the logits (64-bit sums, rounded once to fp32) and clears the second
 // one's counters and flags.  The second one's work-groups each route all tokens
-// by themselves (a wave a token; above kRouteHere tokens route_logits's kernel
-// does it before them), list the used experts, and then draw items: first blocks
-// of rows of the up projections, expert by expert, then of the down projections.
+// by themselves, a wave a token (for many experts and more than four tokens
+// route_logits's kernel does it before them), list the used experts, and then draw
+// items: first blocks of rows of the up projections, expert by expert, then of the
+// down projections.
+//
+// Measured, the second kernel: 22 experts of 2048 x 5120 for one token, bf16 155 us
+// (923 MB, 5.9 TB/s), MXFP4 76 (245 MB, 3.2 TB/s); 97 experts for six tokens, FP8 341
+// (2035 MB, 6.0 TB/s).  A card that only reads reaches 7.0.  What small layers add to
+// that is latency, one thing after the other: 5 to 9 us until the first weights are
+// asked for, about 4 for the first lines and rows, 3 to 6 for an expert's hidden rows
+// to be written, seen and read, 3 for the last output rows: 30 us for a layer of 35 MB.
 //
 // Items are drawn from kQueues counters a projection (one counter for all took
 // 25 ns an item, whatever its size), each work-group from its own until that is
@@ -764,16 +772,23 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const int P = m.T * m.r.K, E = m.r.E;
   // LDS: the tokens' rows and the waves' sums, in whose room the tokens are
   // routed before; then the lists
-  const bool few = m.T <= 4, here = E <= 128 || (E <= 512 && few);
+  // Routed here: a second pass of a wave, or eight tokens' logits of 512 experts in every
+  // work-group, cost more than a launch (T = 6 of 512 experts: 368 us against 341 + 5; T =
+  // 13 of 128: 68 against 64 + 5 and the gap between two kernels).
+  const bool here = E <= 128 || (E <= 512 && m.T <= 4);
   const int nj = !here ? 0 : (E <= 128 ? 2 : 8);
   const int route = kWaves * (256 + nj * 512) + 8 * E + 4 * P;
   const int turn = 16 / (m.y_bf16 ? 2 : 3);
   const int cols = (m.T < turn ? m.T : turn) * (m.y_bf16 ? 2 : 3);
   const int red = 2 * kThreads * 16, lists = 12 * P + 192;
-  // One work-group a CU (they route all tokens and stage the same rows, each for
-  // itself), or two of them where the routing is done and there is more to read: T = 1
-  // bf16 161 us against 163 (512 experts top-22, 2048 x 5120), MXFP4 76 against 90;
-  // T = 6 FP8 378 against 349, T = 13 MXFP4 (128 experts top-8) 74 against 68.
+  // One work-group a CU or two.  One starts sooner (each routes and stages for itself),
+  // two keep more on the way.  512 experts top-22 of 2048 x 5120, one against two: MXFP4 T = 1
+  // (245 MB) 76 us and 90, T = 2 (480 MB) 128 and 143, T = 4 (920 MB) 208 and 202; FP8 T = 2
+  // (900 MB) 176 and 166, T = 6 378 and 349; bf16 T = 1 (920 MB) 161 and 165, T = 2 291 and
+  // 276, T = 4 572 and 519.  Many tokens, 128 experts top-8 (T = 13, MXFP4, 168 MB): 74 and 68.
+  const double mb = 1e-6 * (P < E ? P : E) * m.D * m.F * (m.gated ? 3 : 2) *
+                    (m.format == 0 ? 2.0 : m.format == 1 ? 0.53 : 1.0);
+  const bool few = m.T <= 4 && mb < (m.T == 1 ? 1200 : 700);
   const int room = (few ? 156 : 79) * 1024;
   const int least = cols * (2048 + 16), left = room - red - lists - kWaves * 2048;
   const int xbytes = (left > least ? left : least) / 16 * 16;

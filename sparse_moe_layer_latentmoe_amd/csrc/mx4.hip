@@ -104,7 +104,8 @@ __device__ __forceinline__ uint32_t mx4_pack8(const float (&v)[8], int e) {
 }  // namespace
 
 // Rows [rows, cols], `stride` elements apart: four lanes to a block of 32, eight
-// values a lane; codes of nb blocks a row (those past cols are 0).
+// values a lane (16 or 32 bytes read, 4 written, in order); codes of nb blocks a row
+// (those past cols are 0).  HBM: 8192 x 8192 bf16 in 32 us, 5.3 TB/s.
 template <class T, bool VEC>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T* __restrict__ x, long rows,
                                                            int cols, long stride, int nb,
@@ -126,7 +127,8 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T* __restrict__
   if (i == 0) scales[b] = (uint8_t)(e + 127);
 }
 
-// The values, rounded once to T where they do not fit it: eight a lane.
+// The values, rounded once to T where they do not fit it: eight a lane.  HBM's writes:
+// 8192 x 8192 to bf16 in 42 us, 4.0 TB/s (2, 4 or 8 blocks in flight a lane: the same).
 template <class T, bool VEC>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint32_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ scales,
@@ -226,7 +228,10 @@ __device__ __forceinline__ i32x4 mx4_permute(const i32x4& a, const i32x4& b, int
 // fixed order.  Work-group: 16 RG weight rows x 16 token rows.  A step is a line
 // of 128 bytes of each row (256 k, eight blocks): lane (r, q) (r = lane % 16,
 // q = lane / 16) takes blocks q and 4 + q of row r, whose scales are byte q of
-// the line's two scale words.
+// the line's two scale words.  HBM and latency: 1 x 10240 x 8192 in 12.1 us (44 MB, 3.7
+// TB/s: all of it is asked for at once, then a launch's start and end); 1 x 16384 x 16384
+// in 30 us (4.7 TB/s).  Two or four row groups a work-group, 4 or 16 waves: 11.5 to 16.4
+// us, and slower where N or K is small.
 template <int NW, int RG, int U, class OUT>
 __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(Mx4Gemm p) {
   __shared__ f32x4 red[NW][RG][64];
@@ -345,7 +350,8 @@ __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(Mx4Gemm p) {
 // waves.  Scales come two lines at a time, 16 bytes of a row, into registers.  One
 // barrier a line.  LDS rows are XOR-swizzled: row r keeps its 16-byte chunk c at c ^
 // (r % 8), rows 8 to 15 of sixteen at c ^ (r % 8) ^ 1.  Work items (tile, row block) are
-// taken XCD-major.
+// taken XCD-major.  HBM: 704 rows over 512 groups of 5120 x 2048 in 308 us, 6.8 TB/s of
+// the weights of the groups that have rows (into registers, as above: 480 us).
 template <int NW, int RG, class OUT>
 __global__ __launch_bounds__(NW * 64) void mx4_lines_kernel(Mx4Gemm p, const Tile* tiles,
                                                             const int* ntiles) {
@@ -495,6 +501,14 @@ __global__ __launch_bounds__(NW * 64) void mx4_lines_kernel(Mx4Gemm p, const Til
 //
 // Scales come two lines at a time (16 bytes of a row), half of the tile's rows with
 // each step.
+//
+// Bound by the matrix instructions at the clock that the card's power limit leaves them:
+// 8192 x 10240 x 8192 in 313 us (4.4 PFLOP/s; they are busy in three quarters of a
+// step's cycles, at 1.4 to 1.5 GHz), and by what a tile costs beside its steps, about 11 us (start
+// and scales 3 to 4, first lines 3, the results' way out 4 to 6).  180224 rows over 512
+// groups of 2048 x 5120: 1.33 to 1.43 ms (2.7 PFLOP/s).  Four waves with half the LDS reads,
+// twice the registers: the same.  Tiles of half as many columns, two work-groups a CU: 2%
+// to 29% slower in groups of 8 to 128 rows.
 //
 // Split over k (dense, few tiles): work-group (x, y) computes tile x over the
 // y-th part of the lines and writes fp32 partial sums to part y of `y`.
@@ -866,7 +880,8 @@ struct DenseTile {
   int bm, bn;
 };
 constexpr DenseTile kDenseTiles[3] = {{256, 256}, {128, 256}, {64, 128}};
-// A line of n tiles (all at once, as far as there are CUs).
+// A line of 256 k of n tiles, us: of 256 tiles at a time 1.7 and 1.0; of the smallest 0.6,
+// two work-groups a CU, and no less than 0.8.
 double tile_us(const DenseTile& t, long n) {
   if (t.bm == 64) return n * (0.6 / 256) > 0.8 ? n * (0.6 / 256) : 0.8;
   return (double)((n + 255) / 256) * (t.bm == 256 ? 1.7 : 1.0);
