@@ -350,8 +350,8 @@ __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(Mx4Gemm p) {
 // waves.  Scales come two lines at a time, 16 bytes of a row, into registers.  One
 // barrier a line.  LDS rows are XOR-swizzled: row r keeps its 16-byte chunk c at c ^
 // (r % 8), rows 8 to 15 of sixteen at c ^ (r % 8) ^ 1.  Work items (tile, row block) are
-// taken XCD-major.  HBM: 704 rows over 512 groups of 5120 x 2048 in 308 us, 6.8 TB/s of
-// the weights of the groups that have rows (into registers, as above: 480 us).
+// taken XCD-major.  HBM: 704 rows over 512 groups of 5120 x 2048, 394 of which have any, in
+// 308 us, 7.1 TB/s (into registers, as above: 480 us).
 template <int NW, int RG, class OUT>
 __global__ __launch_bounds__(NW * 64) void mx4_lines_kernel(Mx4Gemm p, const Tile* tiles,
                                                             const int* ntiles) {

@@ -1,7 +1,7 @@
 """The operators around the layer: routing from given logits and the norms
-around a block, each with its gradient, and matrices in 8-bit floating point
-(e4m3) with a scale for each block of 128, with their dense and grouped
-products.
+around a block, each with its gradient; matrices in 8-bit floating point
+(e4m3) with a scale for each block of 128, and in 4-bit (MXFP4), with their
+dense and grouped products; and a whole sparse layer for a few tokens.
 
 Thin wrappers over the C ABI (``include/lmoe.h``), like the rest of the
 binding: they check tensors, allocate the outputs and marshal pointers; the

@@ -283,3 +283,12 @@ def test_a_bias_that_is_not_finite_stays_in_bounds():
     for T in (1, 4, 13):
         layer(x[:T])
     torch.cuda.synchronize()
+
+
+def test_two_work_groups_a_cu():
+    """Few tokens and much to read: 128 pairs of an expert of 5.5 MB."""
+    layer = Layer(132, 32, 1024, 1344, seed=11, scale=2.0)
+    layer.check(rand(4, 1024, seed=1), out=F)
+    layer.check(rand(4, 1024, seed=2, dtype=B))
+    layer = Layer(132, 32, 1024, 1408, "mxfp4", True, 128, seed=12)
+    layer.check(rand(3, 1024, seed=3, dtype=B))
