@@ -81,14 +81,14 @@ struct Fmt<2> {  // FP8
   static constexpr int LK = 128, NF = 2, WK = 2;
 };
 
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
 // c ? a : b of values.  (A conditional of variables chooses between their
 // addresses, which keeps all that a kernel's lambdas share in memory.)
 template <class V>
 __device__ __forceinline__ V pick(bool c, V a, V b) {
   return c ? a : b;
 }
-
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 struct MoeParams {
   MoeTokens m;
@@ -97,6 +97,7 @@ struct MoeParams {
   int turn;    // rows of an expert taken at a time
   int xbytes;  // LDS for the tokens' rows (then the waves' sums)
   int turn_at; // where in LDS lines change their layout
+  int early;   // LDS of one token's x, which is there before the first block; or 0
   int misc;    // where in LDS what is not of the loop begins
 };
 
@@ -128,6 +129,20 @@ __device__ __forceinline__ f32x4 get4_shared(const float* p) {
 }
 __device__ __forceinline__ float get1_shared(const float* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Four values as `parts` bf16 numbers each, `pitch` bytes apart.
+__device__ __forceinline__ void put_parts(f32x4 u, char* to, int pitch, int parts) {
+  // what is rounded to infinity, or is infinite, is the last part's
+#pragma unroll 1
+  for (int q = 1; q < parts; ++q, to += pitch) {
+    f32x4 c;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) c[n] = __builtin_amdgcn_fmed3f(u[n], -kBf16Max, kBf16Max);
+    const bf16x4 b = __builtin_convertvector(c, bf16x4);
+    *reinterpret_cast<bf16x4*>(to) = b;
+    u -= __builtin_convertvector(b, f32x4);
+  }
+  *reinterpret_cast<bf16x4*>(to) = __builtin_convertvector(u, bf16x4);
 }
 // This wave's stores are done (and none of its later accesses begins before).
 __device__ __forceinline__ void stores_done() {
@@ -231,15 +246,37 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   uint16_t* const sstart = sexp + P + 16;
   uint16_t* const srows = sstart + P + 16;
   constexpr int ROUTE = kWaves * (256 + NJ * 512);
-  uint32_t* const smask = reinterpret_cast<uint32_t*>(smem + ROUTE);  // [E] tokens
+  char* const scratch = smem + p.early;
+  uint32_t* const smask = reinterpret_cast<uint32_t*>(scratch + ROUTE);  // [E] tokens
   uint32_t* const sfirst = smask + E;                                 // [E]
   int32_t* const sidx = reinterpret_cast<int32_t*>(sfirst + E);       // [P]
   for (int i = tid; i < E; i += kThreads) smask[i] = 0;
+  // One token: its x is brought into LDS, as put_rows below does it, by the waves that
+  // do not route.
+  if (p.early && w > 0) {
+    const int parts = m.x_bf16 ? 1 : (m.y_bf16 ? 2 : 3), pitch = p.early / parts;
+    constexpr int N = 3, step = (kThreads - 64) * 4;
+#pragma unroll 1
+    for (int k = (tid - 64) * 4; k * 2 < pitch - 16; k += N * step) {
+      f32x4 v[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int at = min(k + j * step, D - 4);
+        v[j] = m.x_bf16 ? load4(static_cast<const uint16_t*>(m.x) + at)
+                        : load4(static_cast<const float*>(m.x) + at);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if ((k + j * step) * 2 < pitch - 16)
+          put_parts(k + j * step < D ? v[j] : f32x4{0.f, 0.f, 0.f, 0.f}, smem + (k + j * step) * 2,
+                    pitch, parts);
+    }
+  }
   if constexpr (NJ > 0) {
     for (int t = w; t < T; t += kWaves) {
       route_token<float, NJ>(p.logits + (size_t)t * E, m.bias, m.r, lane,
-                             reinterpret_cast<float*>(smem + w * 256),
-                             smem + kWaves * 256 + w * NJ * 512, sidx + t * K, sw + t * K);
+                             reinterpret_cast<float*>(scratch + w * 256),
+                             scratch + kWaves * 256 + w * NJ * 512, sidx + t * K, sw + t * K);
       if (NJ > 2) break;  // (up to four tokens)
       wave_lds_fence();
     }
@@ -521,18 +558,8 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
         const uint32_t c = c0 + j * kWaves, r = row_of(c);
         const int k = (int)(c - r * pieces) * 256 + lane * 4;
         if (c >= all || k >= kn) continue;
-        char* to = smem + r * parts * pitch + k * 2;
-        f32x4 u = k0 + k < it.K ? v[j] : f32x4{0.f, 0.f, 0.f, 0.f};
-        // what is rounded to infinity, or is infinite, is the last part's
-#pragma unroll 1
-        for (int q = 1; q < parts; ++q, to += pitch) {
-#pragma unroll
-          for (int n = 0; n < 4; ++n) v[j][n] = __builtin_amdgcn_fmed3f(u[n], -kBf16Max, kBf16Max);
-          const bf16x4 b = __builtin_convertvector(v[j], bf16x4);
-          *reinterpret_cast<bf16x4*>(to) = b;
-          u -= __builtin_convertvector(b, f32x4);
-        }
-        *reinterpret_cast<bf16x4*>(to) = __builtin_convertvector(u, bf16x4);
+        char* const to = smem + r * parts * pitch + k * 2;
+        put_parts(k0 + k < it.K ? v[j] : f32x4{0.f, 0.f, 0.f, 0.f}, to, pitch, parts);
       }
     }
   };
@@ -562,7 +589,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   }
   int run = cur;             // the first of the run's blocks
   int next = -1, nend = -1;  // the run after it; -1: not drawn, total: none
-  int staged = -1;           // whose rows are in LDS, all of them
+  int staged = p.early ? 0 : -1;  // whose rows are in LDS, all of them
   int waited = -1;           // whose hidden rows are known to be written
   int parity = 1;  // (the first run's place is still being read)
 #pragma unroll 1
@@ -793,6 +820,13 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const int least = cols * (2048 + 16), left = room - red - lists - kWaves * 2048;
   const int xbytes = (left > least ? left : least) / 16 * 16;
   const int turned = kWaves * 2048, work = xbytes + red + turned;
+  // One token's x comes before the first block if all of it fits (in turns of 2048
+  // bytes, as the kernel counts it) beside what routing takes.
+  const int line = m.format == 1 ? 512 : m.format == 2 ? 256 : 128;  // bytes of x
+  const int xparts = m.x_bf16 ? 1 : (m.y_bf16 ? 2 : 3), xrow = (m.D * 2 + line - 1) / line * line;
+  const bool fits = (xbytes / xparts - 16) / 2048 >= (xrow + 2047) / 2048 &&
+                    xparts * (xrow + 16) + route <= work;
+  const int early = m.T == 1 && fits ? xparts * (xrow + 16) : 0;
   MoeParams p{m,
               reinterpret_cast<float*>(ws + l.logits),
               reinterpret_cast<float*>(ws + l.h),
@@ -804,7 +838,8 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
               turn,
               xbytes,
               xbytes + red,
-              ((route > work ? route : work) + 15) / 16 * 16};
+              early,
+              ((early + route > work ? early + route : work) + 15) / 16 * 16};
   const int lds = p.misc + lists;
   auto logits = [&](auto g, auto x) {
     using GT = decltype(g);

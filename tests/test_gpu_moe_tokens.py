@@ -292,3 +292,13 @@ def test_two_work_groups_a_cu():
     layer.check(rand(4, 1024, seed=2, dtype=B))
     layer = Layer(132, 32, 1024, 1408, "mxfp4", True, 128, seed=12)
     layer.check(rand(3, 1024, seed=3, dtype=B))
+
+
+@pytest.mark.parametrize("D", [8192, 16384, 20480, 32768])
+def test_one_token_of_a_wide_layer(D):
+    """x in LDS before the first block, and where it does not fit."""
+    for E, fmt in ((130, "bf16"), (6, "mxfp4")):
+        layer = Layer(E, 3, D, 128, fmt, seed=D, S=128)
+        layer.check(rand(1, D, seed=1), out=F)
+        layer.check(rand(1, D, seed=2), out=B)
+        layer.check(rand(1, D, seed=3, dtype=B))
