@@ -15,12 +15,12 @@
 // items: first blocks of rows of the up projections, expert by expert, then of the
 // down projections.
 //
-// Measured, the second kernel: 22 experts of 2048 x 5120 for one token, bf16 155 us
-// (923 MB, 5.9 TB/s), MXFP4 76 (245 MB, 3.2 TB/s); 97 experts for six tokens, FP8 341
+// Measured, the second kernel: 22 experts of 2048 x 5120 for one token, bf16 157 us
+// (923 MB, 5.9 TB/s), MXFP4 75 (245 MB, 3.3 TB/s); 97 experts for six tokens, FP8 342
 // (2035 MB, 6.0 TB/s).  A card that only reads reaches 7.0.  What small layers add to
 // that is latency, one thing after the other: 5 to 9 us until the first weights are
-// asked for, about 4 for the first lines and rows, 3 to 6 for an expert's hidden rows
-// to be written, seen and read, 3 for the last output rows: 30 us for a layer of 35 MB.
+// asked for, 2 to 4 for the first lines and rows, 3 to 6 for an expert's hidden rows
+// to be written, seen and read, 3 for the last output rows: 29 us for a layer of 35 MB.
 //
 // Items are drawn from kQueues counters a projection (one counter for all took
 // 25 ns an item, whatever its size), each work-group from its own until that is
