@@ -302,3 +302,19 @@ def test_one_token_of_a_wide_layer(D):
         layer.check(rand(1, D, seed=1), out=F)
         layer.check(rand(1, D, seed=2), out=B)
         layer.check(rand(1, D, seed=3, dtype=B))
+
+
+def test_one_token_on_four_streams_at_once():
+    """More work-groups of a CU's whole LDS than there are CUs: none waits for one
+    that cannot start."""
+    layer = Layer(160, 12, 1024, 1024, "fp8", S=1024, seed=2)
+    xs = [rand(1, 1024, seed=s, dtype=B) for s in range(4)]
+    want = [layer(x) for x in xs]
+    sides = [torch.cuda.Stream() for _ in xs]
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        got = [layer(x, stream=s) for x, s in zip(xs, sides)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
