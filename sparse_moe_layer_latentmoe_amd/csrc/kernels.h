@@ -223,7 +223,7 @@ hipError_t mx4_matmul(Mx4Gemm p, const int32_t* offsets, bool out_bf16, void* ws
 
 // A whole sparse layer for 1 <= T <= 16 tokens (T K <= 1024): router, experts,
 // weighted sum, shared expert (S > 0).  D, F and S multiples of 64, or of 128
-// where the format is not bf16; a matrix is smaller than 2^32 bytes.
+// where the format is not bf16; a matrix is smaller than 2^31 - 16 bytes.
 struct MoeTokens {
   const void* x;                                 // [T, D], rows x_stride apart
   const void* gate;                              // [E, D]
