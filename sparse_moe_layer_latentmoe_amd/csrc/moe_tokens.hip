@@ -35,11 +35,12 @@
 // kAhead lines ahead (on into the next block), brought into its layout through LDS
 // and decoded exactly to bf16 (8-bit: the block's scale on its sum).  The tokens'
 // operand is bf16, too: a value that is no bf16 number (fp32 x, the hidden rows)
-// is the sum of two such parts (y in bf16: 16 bits, its error far below y's
-// rounding) or three (24 bits), each a column of its own of the operand, of which
-// one token leaves 15 free; their results are added at the end.  An expert with
-// more rows than the 16 columns hold is taken as several, whose weights come
-// again from a cache.
+// is the sum of three such parts (24 bits: an fp32 number's), each a column of its
+// own of the operand, of which one token leaves 15 free; their results are added at
+// the end.  (Two parts for results in bf16, 16 bits, were not enough: what cancels
+// between experts, or in a row of weights, leaves their error.)  The 16 columns hold
+// five tokens; an expert with more is taken as several entries, and its weights are
+// read again for each.
 //
 // The loop is kept small and rolled: unrolled over the forms of an item, its 40 KB
 // of code did not stay in the instruction cache and it ran three times as long.
@@ -59,6 +60,8 @@ namespace {
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kQueues = 16, kSpread = 64;  // counters, ints apart
 constexpr int kAhead = 3;                  // lines that a wave loads ahead
+constexpr int kParts = 3;                  // bf16 numbers of an fp32 operand
+constexpr int kTurn = 16 / kParts;         // rows of an expert taken at a time
 constexpr int kLogitTokens = 4;            // tokens of a work-group of the first kernel
 constexpr float kBf16Max = 0x1.FEp127f;
 
@@ -94,7 +97,6 @@ struct MoeParams {
   MoeTokens m;
   float *logits, *h, *hs, *o;
   int32_t *queues, *up_done, *down_done;
-  int turn;    // rows of an expert taken at a time
   int xbytes;  // LDS for the tokens' rows (then the waves' sums)
   int turn_at; // where in LDS lines change their layout
   int early;   // LDS of one token's x, which is there before the first block; or 0
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   // One token: its x is brought into LDS, as put_rows below does it, by the waves that
   // do not route.
   if (p.early && w > 0) {
-    const int parts = m.x_bf16 ? 1 : (m.y_bf16 ? 2 : 3), pitch = p.early / parts;
+    const int parts = m.x_bf16 ? 1 : kParts, pitch = p.early / parts;
     constexpr int N = 3, step = (kThreads - 64) * 4;
 #pragma unroll 1
     for (int k = (tid - 64) * 4; k * 2 < pitch - 16; k += N * step) {
@@ -299,12 +301,12 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   }
   __syncthreads();
   // Entries: the shared expert's first, then the used experts', each of up to
-  // `turn` of the tokens that take it.
-  const int nsh = S > 0 ? (T + p.turn - 1) / p.turn : 0;
+  // kTurn of the tokens that take it.
+  const int nsh = S > 0 ? (T + kTurn - 1) / kTurn : 0;
   if (tid < nsh) {
     sexp[tid] = kShared;
-    sstart[tid] = (uint16_t)(tid * p.turn);
-    srows[tid] = (uint16_t)min(p.turn, T - tid * p.turn);
+    sstart[tid] = (uint16_t)(tid * kTurn);
+    srows[tid] = (uint16_t)min(kTurn, T - tid * kTurn);
   }
   int nexp;
   {
@@ -313,7 +315,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = 4 * tid + j < E ? __popc(smask[4 * tid + j]) : 0;
-      v[j] = (n + p.turn - 1) / p.turn | n << 16;
+      v[j] = (n + kTurn - 1) / kTurn | n << 16;
       inc += v[j];
     }
     const int own = inc;
@@ -335,10 +337,10 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     for (int j = 0; j < 4; ++j) {
       const int n = v[j] >> 16, first = at >> 16;
       if (n) sfirst[4 * tid + j] = first;
-      for (int r = 0, u = nsh + (at & 0xFFFF); r < n; r += p.turn, ++u) {
+      for (int r = 0, u = nsh + (at & 0xFFFF); r < n; r += kTurn, ++u) {
         sexp[u] = (uint16_t)(4 * tid + j);
         sstart[u] = (uint16_t)(first + r);
-        srows[u] = (uint16_t)min(p.turn, n - r);
+        srows[u] = (uint16_t)min(kTurn, n - r);
       }
       at += v[j];
     }
@@ -606,7 +608,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     const bool known = coming >= 0 && coming < total;
     const bool sh = it.u < nsh;
     const int r0 = uniform(sstart[it.u]), rows = uniform(srows[it.u]);
-    const int parts = !it.down && m.x_bf16 ? 1 : (m.y_bf16 ? 2 : 3);
+    const int parts = !it.down && m.x_bf16 ? 1 : kParts;
     const int cols = rows * parts;
     // turns of NL lines a wave, and how many of them have their rows in LDS at a
     // time (at least one)
@@ -776,9 +778,9 @@ Layout layout(const MoeTokens& m) {
   const size_t used = pairs < (size_t)m.r.E ? pairs : m.r.E;
   l.down_done = 2 * kQueues * kSpread;
   l.up_done = l.down_done + m.D / 16 * kSpread;
-  // a flag for each 8 (gated) or 16 hidden columns of an entry (of five rows or
-  // more, and one more an expert)
-  const size_t entries = used + pairs / 5, shared = m.S ? 1 + m.T / 5 : 0;
+  // a flag for each 8 (gated) or 16 hidden columns of an entry (an expert has one for
+  // every kTurn rows, and one more)
+  const size_t entries = used + pairs / kTurn, shared = m.S ? 1 + m.T / kTurn : 0;
   l.nsync = l.up_done + (int)((entries * m.F + shared * m.S) / (m.gated ? 8 : 16));
   l.sync = take((size_t)l.nsync * 4);
   l.logits = take((size_t)m.T * m.r.E * 4);
@@ -805,8 +807,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const bool here = E <= 128 || (E <= 512 && m.T <= 4);
   const int nj = !here ? 0 : (E <= 128 ? 2 : 8);
   const int route = kWaves * (256 + nj * 512) + 8 * E + 4 * P;
-  const int turn = 16 / (m.y_bf16 ? 2 : 3);
-  const int cols = (m.T < turn ? m.T : turn) * (m.y_bf16 ? 2 : 3);
+  const int cols = (m.T < kTurn ? m.T : kTurn) * kParts;
   const int red = 2 * kThreads * 16, lists = 12 * P + 192;
   // One work-group a CU or two.  One starts sooner (each routes and stages for itself),
   // two keep more on the way.  512 experts top-22 of 2048 x 5120, one against two: MXFP4 T = 1
@@ -823,7 +824,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   // One token's x comes before the first block if all of it fits (in turns of 2048
   // bytes, as the kernel counts it) beside what routing takes.
   const int line = m.format == 1 ? 512 : m.format == 2 ? 256 : 128;  // bytes of x
-  const int xparts = m.x_bf16 ? 1 : (m.y_bf16 ? 2 : 3), xrow = (m.D * 2 + line - 1) / line * line;
+  const int xparts = m.x_bf16 ? 1 : kParts, xrow = (m.D * 2 + line - 1) / line * line;
   const bool fits = (xbytes / xparts - 16) / 2048 >= (xrow + 2047) / 2048 &&
                     xparts * (xrow + 16) + route <= work;
   const int early = m.T == 1 && fits ? xparts * (xrow + 16) : 0;
@@ -835,7 +836,6 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
               sync,
               sync + l.up_done,
               sync + l.down_done,
-              turn,
               xbytes,
               xbytes + red,
               early,
