@@ -486,7 +486,9 @@ lmoe_status lmoe_mxfp4_matmul(const lmoe_mxfp4_matmul_args *a, void *workspace,
  * expert's fp32 output, and y rounds once.  Each used expert's weights are
  * read from memory once, whatever the number of its tokens.  The same call gives
  * the same bits.  Inputs should be finite: what is not stays in its token's row
- * of y (an infinite value may become NaN there). */
+ * of y (an infinite value may become NaN there).  Work-groups wait for each
+ * other's hidden rows; should one ever wait about ten seconds in vain, the rows of
+ * y that it works on are NaN. */
 typedef enum { LMOE_ACT_RELU2 = 0, LMOE_ACT_SWIGLU = 1 } lmoe_activation;
 typedef struct {
   lmoe_router router;

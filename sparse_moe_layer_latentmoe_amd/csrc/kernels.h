@@ -240,6 +240,8 @@ struct MoeTokens {
 };
 size_t moe_tokens_workspace(const MoeTokens& m);
 hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s);
+// How often a work-group looks for an entry's hidden rows before it gives up.
+extern int moe_tokens_looks;
 
 // r = sum_k w[t][k] O[inv[t][k]] -> r16 (bf16) and, if r32 != NULL, fp32.
 hipError_t combine(const uint16_t* o, const int32_t* inv, const float* w, int T, int K, int R,

@@ -97,6 +97,7 @@ struct MoeParams {
   MoeTokens m;
   float *logits, *h, *hs, *o;
   int32_t *queues, *up_done, *down_done;
+  int looks;   // for an entry's hidden rows, before a work-group gives up
   int xbytes;  // LDS for the tokens' rows (then the waves' sums)
   int turn_at; // where in LDS lines change their layout
   int early;   // LDS of one token's x, which is there before the first block; or 0
@@ -565,21 +566,25 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
       }
     }
   };
-  // Until the flags of an entry's hidden rows are all set (bounded, about ten
-  // seconds: should one ever be lost, the result is wrong, but the kernel ends).
+  // Until the flags of an entry's hidden rows are all set.  Bounded (about ten
+  // seconds; once it has run out, one look an entry): should one ever be lost, the
+  // kernel ends, and what it adds to y for that entry is NaN.
   auto flags_of = [&](int u) __attribute__((always_inline)) {
     return pick(u < nsh, u * ns, nsup + (u - nsh) * nf) * WR;
   };
+  int looks = p.looks;
   auto wait_hidden = [&](int u) __attribute__((always_inline)) {
     const int n = pick(u < nsh, ns, nf) * WR;
     const int32_t* const flags = p.up_done + flags_of(u);
 #pragma unroll 1
-    for (int tries = 0; tries < (1 << 22); ++tries) {
+    for (int look = 0; look < looks; ++look) {
       int ok = 1;
       for (int i = tid; i < n; i += kThreads)
         ok &= __hip_atomic_load(flags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (__syncthreads_and(ok)) break;
+      if (__syncthreads_and(ok)) return 1.f;
     }
+    looks = min(looks, 1);
+    return __uint_as_float(0x7FC00000u);
   };
 
   Line buf[NL];
@@ -592,7 +597,8 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   int run = cur;             // the first of the run's blocks
   int next = -1, nend = -1;  // the run after it; -1: not drawn, total: none
   int staged = p.early ? 0 : -1;  // whose rows are in LDS, all of them
-  int waited = -1;           // whose hidden rows are known to be written
+  int waited = -1;           // whose hidden rows are known to be written,
+  float there = 1.f;         // and 1, or NaN where they were waited for in vain
   int parity = 1;  // (the first run's place is still being read)
 #pragma unroll 1
   while (cur < total) {
@@ -628,7 +634,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
 #pragma unroll 1
     for (int j = 0; j < turns; ++j) {
       if (in == 0 && !keep) {
-        if (it.down && it.u != waited) wait_hidden(it.u);
+        if (it.down && it.u != waited) there = wait_hidden(it.u);
         else if (j > 0) __syncthreads();  // what is there has been read
         waited = pick(it.down != 0, it.u, waited);
         l0 = j * NL * WK;
@@ -686,7 +692,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
         }
       } else if (live) {
         put4_shared(p.o + (size_t)(sh ? P + pair : pair) * D + group * 16 + 4 * q,
-                    v * (sh ? 1.f : sw[pair]));
+                    v * ((sh ? 1.f : sw[pair]) * there));
       }
       if (last) {
         // the run is written: a lane tells of each of its blocks
@@ -792,6 +798,8 @@ Layout layout(const MoeTokens& m) {
 
 }  // namespace
 
+int moe_tokens_looks = 1 << 22;
+
 size_t moe_tokens_workspace(const MoeTokens& m) { return layout(m).total; }
 
 hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
@@ -836,6 +844,7 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
               sync,
               sync + l.up_done,
               sync + l.down_done,
+              moe_tokens_looks,
               xbytes,
               xbytes + red,
               early,
