@@ -483,9 +483,10 @@ lmoe_status lmoe_mxfp4_matmul(const lmoe_mxfp4_matmul_args *a, void *workspace,
  * (bf16; e4m3 with a scale for each 128 x 128 block; MXFP4); activations are
  * not quantised.  Logits are 64-bit sums rounded once to fp32; products and
  * sums are fp32 (the hidden rows are kept in fp32), w_k is applied to an
- * expert's fp32 output, and y rounds once.  Each used expert's weights are
- * read from memory once, whatever the number of its tokens.  The same call gives
- * the same bits.  Inputs should be finite: what is not stays in its token's row
+ * expert's fp32 output, and y rounds once.  Only used experts' weights are read:
+ * once where up to five tokens take an expert, else once for each five of them
+ * (its up projection once where x is bf16); so with a shared expert.  The same
+ * call gives the same bits.  Inputs should be finite: what is not stays in its token's row
  * of y (an infinite value may become NaN there).  Work-groups wait for each
  * other's hidden rows; should one ever wait about ten seconds in vain, the rows of
  * y that it works on are NaN. */

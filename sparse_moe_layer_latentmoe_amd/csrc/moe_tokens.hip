@@ -5,9 +5,9 @@
 //   y_t = sum_k w_tk h_p Wdown[e]^T  (+ the shared expert's, weight 1)
 //   act: relu(u)^2, or silu(u_gate) u_up of two halves of the up rows
 //
-// Bound by HBM: each used expert's weights are read once, whatever the number
-// of tokens that use it, and everything else is small; so what counts is that
-// the weights' stream starts early and never pauses.  Two kernels: the first
+// Bound by HBM: each used expert's weights are read once (where more than five
+// tokens use it, once for each five), and everything else is small; so what counts
+// is that the weights' stream starts early and never pauses.  Two kernels: the first
 // computes the logits (64-bit sums, rounded once to fp32) and clears the second
 // one's counters and flags.  The second one's work-groups each route all tokens
 // by themselves, a wave a token (for many experts and more than four tokens
@@ -39,8 +39,9 @@
 // own of the operand, of which one token leaves 15 free; their results are added at
 // the end.  (Two parts for results in bf16, 16 bits, were not enough: what cancels
 // between experts, or in a row of weights, leaves their error.)  The 16 columns hold
-// five tokens; an expert with more is taken as several entries, and its weights are
-// read again for each.
+// five tokens, or all of them where x is bf16 and the projection up; an expert with
+// more is taken as several entries, and its weights are read again for each (blocks
+// of such entries next to each other, for a cache to hold them: 3% to 13% slower).
 //
 // The loop is kept small and rolled: unrolled over the forms of an item, its 40 KB
 // of code did not stay in the instruction cache and it ran three times as long.
@@ -61,7 +62,7 @@ constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kQueues = 16, kSpread = 64;  // counters, ints apart
 constexpr int kAhead = 3;                  // lines that a wave loads ahead
 constexpr int kParts = 3;                  // bf16 numbers of an fp32 operand
-constexpr int kTurn = 16 / kParts;         // rows of an expert taken at a time
+constexpr int kTurn = 16 / kParts;         // rows of an entry
 constexpr int kLogitTokens = 4;            // tokens of a work-group of the first kernel
 constexpr float kBf16Max = 0x1.FEp127f;
 
@@ -194,8 +195,8 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const XT* __restrict__ 
 
 namespace {
 
-// What a work-group works on: block `blk` of rows of entry u in one of the two
-// projections, K long.
+// What a work-group works on: block `blk` of rows of the projection's entry u, K
+// long.
 struct Item {
   int down, u, blk, K;
 };
@@ -244,10 +245,14 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   int* const scount = stick + 4;                                // [kWaves]
   float* const sw = reinterpret_cast<float*>(scount + kWaves);  // [P] pairs' weights
   uint16_t* const slist = reinterpret_cast<uint16_t*>(sw + P);  // [P] pairs by expert
-  // entries: expert, first of its pairs in the list, their number
+  // entries: expert, first of its pairs in the list, their number and, from bit 5 on,
+  // its entry in the projection up.  The down projection's, then (from upto on; the
+  // same ones where x is fp32) the up projection's.
+  const bool own_up = m.x_bf16 && T > kTurn;
+  const int upto = own_up ? P + 16 : 0;
   uint16_t* const sexp = slist + P;
-  uint16_t* const sstart = sexp + P + 16;
-  uint16_t* const srows = sstart + P + 16;
+  uint16_t* const sstart = sexp + P + 16 + upto;
+  uint16_t* const srows = sstart + P + 16 + upto;
   constexpr int ROUTE = kWaves * (256 + NJ * 512);
   char* const scratch = smem + p.early;
   uint32_t* const smask = reinterpret_cast<uint32_t*>(scratch + ROUTE);  // [E] tokens
@@ -301,48 +306,55 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     }
   }
   __syncthreads();
-  // Entries: the shared expert's first, then the used experts', each of up to
-  // kTurn of the tokens that take it.
+  // Entries: the shared expert's first, then the used experts', each of up to kTurn of
+  // the tokens that take it, or (up, x in bf16) of all of them.
   const int nsh = S > 0 ? (T + kTurn - 1) / kTurn : 0;
-  if (tid < nsh) {
-    sexp[tid] = kShared;
-    sstart[tid] = (uint16_t)(tid * kTurn);
-    srows[tid] = (uint16_t)min(kTurn, T - tid * kTurn);
-  }
-  int nexp;
+  const int nshu = S > 0 && own_up ? 1 : nsh;
+  auto put_entry = [&](int u, int e, int first, int n, int ue) __attribute__((always_inline)) {
+    sexp[u] = (uint16_t)e;
+    sstart[u] = (uint16_t)first;
+    srows[u] = (uint16_t)(n | ue << 5);
+  };
+  if (tid < nsh)
+    put_entry(tid, kShared, tid * kTurn, min(kTurn, T - tid * kTurn), own_up ? 0 : tid);
+  if (tid < nshu && own_up) put_entry(upto, kShared, 0, T, 0);
+  int nexp, nexpu;
   {
-    // thread i: experts 4 i to 4 i + 3; low half: entries, high half: pairs
-    int v[4], inc = 0;
+    // thread i: experts 4 i to 4 i + 3.  Sums of three numbers each: experts used (11
+    // bits), their further entries (10), their pairs.
+    uint32_t v[4], inc = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = 4 * tid + j < E ? __popc(smask[4 * tid + j]) : 0;
-      v[j] = (n + kTurn - 1) / kTurn | n << 16;
+      const uint32_t n = 4 * tid + j < E ? __popc(smask[4 * tid + j]) : 0;
+      v[j] = n ? 1u | ((n - 1) / kTurn) << 11 | n << 21 : 0u;
       inc += v[j];
     }
-    const int own = inc;
+    const uint32_t own = inc;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(inc, off, 64);
+      const uint32_t o = __shfl_up(inc, off, 64);
       if (lane >= off) inc += o;
     }
-    if (lane == 63) scount[w] = inc;
+    if (lane == 63) scount[w] = (int)inc;
     __syncthreads();
-    int at = inc - own, all = 0;
+    uint32_t at = inc - own, all = 0;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
-      if (i < w) at += scount[i];
-      all += scount[i];
+      if (i < w) at += (uint32_t)scount[i];
+      all += (uint32_t)scount[i];
     }
-    nexp = nsh + uniform(all & 0xFFFF);
+    const int used = uniform((int)(all & 0x7FF)), more = uniform((int)(all >> 11 & 0x3FF));
+    nexp = nsh + used + more;
+    nexpu = nshu + used + (own_up ? 0 : more);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = v[j] >> 16, first = at >> 16;
-      if (n) sfirst[4 * tid + j] = first;
-      for (int r = 0, u = nsh + (at & 0xFFFF); r < n; r += kTurn, ++u) {
-        sexp[u] = (uint16_t)(4 * tid + j);
-        sstart[u] = (uint16_t)(first + r);
-        srows[u] = (uint16_t)min(kTurn, n - r);
+      const int n = (int)(v[j] >> 21), first = (int)(at >> 21), x = (int)(at & 0x7FF);
+      if (n) {
+        sfirst[4 * tid + j] = first;
+        if (own_up) put_entry(upto + nshu + x, 4 * tid + j, first, n, 0);
       }
+      for (int r = 0, u = nsh + x + (int)(at >> 11 & 0x3FF); r < n; r += kTurn, ++u)
+        put_entry(u, 4 * tid + j, first + r, min(kTurn, n - r), own_up ? nshu + x : u);
       at += v[j];
     }
   }
@@ -352,8 +364,8 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     slist[sfirst[e] + __popc(smask[e] & ((1u << t) - 1u))] = (uint16_t)i;
   }
   const int fr = 16 * WR >> gated;  // hidden columns of an up item
-  const int nf = F / fr, ns = S / fr, nd = D / (16 * WR), nsup = nsh * ns;
-  const int nup = nsup + (nexp - nsh) * nf, ndown = nexp * nd, total = nup + ndown;
+  const int nf = F / fr, ns = S / fr, nd = D / (16 * WR), nsup = nshu * ns;
+  const int nup = nsup + (nexpu - nshu) * nf, ndown = nexp * nd, total = nup + ndown;
 
   // Runs of blocks: the first gridDim.x of a projection are long and cover three
   // quarters of it, the others are short.
@@ -412,16 +424,19 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
     const int n = pick(it.down != 0, nd, pick(sh, ns, nf));
     const int u = j / n;
     it.blk = j - u * n;
-    it.u = u + pick(it.down || sh, 0, nsh);
+    it.u = u + pick(it.down != 0, 0, upto + pick(sh, 0, nshu));
     it.K = pick(it.down != 0, pick(it.u < nsh, S, F), D);
     return it;
+  };
+  auto of_shared = [&](const Item& it) __attribute__((always_inline)) {
+    return it.u < pick(it.down != 0, nsh, upto + nshu);
   };
   auto lines_of = [&](int k) __attribute__((always_inline)) { return (k + LK - 1) / LK; };
   const int r16 = lane & 15, kq = lane >> 4;
 
   Source src;
   auto enter = [&](const Item& it) __attribute__((always_inline)) {
-    const bool sh = it.u < nsh, down = it.down, two = gated && !down;
+    const bool sh = of_shared(it), down = it.down, two = gated && !down;
     const int rows = pick(down, D, pick(sh, S, F));  // of one half where gated
     const int ex = uniform(sexp[it.u]);
     const size_t e = sh ? 0 : (size_t)ex * ((size_t)rows << two);
@@ -524,7 +539,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   // after the other would wait for memory once a row).
   auto put_rows = [&](const Item& it, int r0, int rows, int k0, int kn, int pitch, int parts)
                       __attribute__((always_inline)) {
-    const bool sh = it.u < nsh, down = it.down;
+    const bool sh = of_shared(it), down = it.down;
     constexpr int N = 5;
     const uint32_t pieces = (kn + 255) >> 8, all = rows * pieces;  // at most 2^11
     const uint32_t per_row = 0xFFFFFFFFu / pieces + 1;             // (0 of one piece)
@@ -566,15 +581,15 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
       }
     }
   };
-  // Until the flags of an entry's hidden rows are all set.  Bounded (about ten
+  // Until the flags of an up entry's hidden rows are all set.  Bounded (about ten
   // seconds; once it has run out, one look an entry): should one ever be lost, the
   // kernel ends, and what it adds to y for that entry is NaN.
   auto flags_of = [&](int u) __attribute__((always_inline)) {
-    return pick(u < nsh, u * ns, nsup + (u - nsh) * nf) * WR;
+    return pick(u < nshu, u * ns, nsup + (u - nshu) * nf) * WR;
   };
   int looks = p.looks;
   auto wait_hidden = [&](int u) __attribute__((always_inline)) {
-    const int n = pick(u < nsh, ns, nf) * WR;
+    const int n = pick(u < nshu, ns, nf) * WR;
     const int32_t* const flags = p.up_done + flags_of(u);
 #pragma unroll 1
     for (int look = 0; look < looks; ++look) {
@@ -597,7 +612,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
   int run = cur;             // the first of the run's blocks
   int next = -1, nend = -1;  // the run after it; -1: not drawn, total: none
   int staged = p.early ? 0 : -1;  // whose rows are in LDS, all of them
-  int waited = -1;           // whose hidden rows are known to be written,
+  int waited = -1;           // the up entry whose hidden rows are known to be written,
   float there = 1.f;         // and 1, or NaN where they were waited for in vain
   int parity = 1;  // (the first run's place is still being read)
 #pragma unroll 1
@@ -612,8 +627,9 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const int coming = last ? next : cur + 1;  // the block after this one
     const bool known = coming >= 0 && coming < total;
-    const bool sh = it.u < nsh;
-    const int r0 = uniform(sstart[it.u]), rows = uniform(srows[it.u]);
+    const bool sh = of_shared(it);
+    const int r0 = uniform(sstart[it.u]), info = uniform(srows[it.u]);
+    const int rows = info & 31, above = info >> 5;
     const int parts = !it.down && m.x_bf16 ? 1 : kParts;
     const int cols = rows * parts;
     // turns of NL lines a wave, and how many of them have their rows in LDS at a
@@ -634,9 +650,9 @@ __global__ __launch_bounds__(kThreads, 4) void moe_tokens_kernel(MoeParams p) {
 #pragma unroll 1
     for (int j = 0; j < turns; ++j) {
       if (in == 0 && !keep) {
-        if (it.down && it.u != waited) there = wait_hidden(it.u);
+        if (it.down && above != waited) there = wait_hidden(above);
         else if (j > 0) __syncthreads();  // what is there has been read
-        waited = pick(it.down != 0, it.u, waited);
+        waited = pick(it.down != 0, above, waited);
         l0 = j * NL * WK;
         put_rows(it, r0, rows, l0 * LK, min(chunk * (per / 2), (lines - l0) * LK), pitch, parts);
         __syncthreads();
@@ -815,13 +831,16 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const bool here = E <= 128 || (E <= 512 && m.T <= 4);
   const int nj = !here ? 0 : (E <= 128 ? 2 : 8);
   const int route = kWaves * (256 + nj * 512) + 8 * E + 4 * P;
-  const int cols = (m.T < kTurn ? m.T : kTurn) * kParts;
-  const int red = 2 * kThreads * 16, lists = 12 * P + 192;
+  const int down_cols = (m.T < kTurn ? m.T : kTurn) * kParts;
+  const int cols = m.x_bf16 && m.T > down_cols ? m.T : down_cols;
+  const int red = 2 * kThreads * 16, lists = m.x_bf16 && m.T > kTurn ? 18 * P + 288 : 12 * P + 192;
   // One work-group a CU or two.  One starts sooner (each routes and stages for itself),
   // two keep more on the way.  512 experts top-22 of 2048 x 5120, one against two: MXFP4 T = 1
   // (245 MB) 76 us and 90, T = 2 (480 MB) 128 and 143, T = 4 (920 MB) 208 and 202; FP8 T = 2
   // (900 MB) 176 and 166, T = 6 378 and 349; bf16 T = 1 (920 MB) 161 and 165, T = 2 291 and
   // 276, T = 4 572 and 519.  Many tokens, 128 experts top-8 (T = 13, MXFP4, 168 MB): 74 and 68.
+  // The shared expert is not counted: of one of 1.07 GB (bf16, 8192 x 32768) T = 2 takes
+  // 291 us and 283, T = 4 323 and 340.
   const double mb = 1e-6 * (P < E ? P : E) * m.D * m.F * (m.gated ? 3 : 2) *
                     (m.format == 0 ? 2.0 : m.format == 1 ? 0.53 : 1.0);
   const bool few = m.T <= 4 && mb < (m.T == 1 ? 1200 : 700);
