@@ -496,6 +496,7 @@ def mxfp4_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=to
     ``offsets`` (int32 [G + 1], ascending) with w [G, N, K / 2]: rows
     offsets[g] .. offsets[g + 1] - 1 take matrix g; rows of no group are not
     written (pass ``out`` to keep what they hold).  out_dtype: bf16 or fp32."""
+    _no_gradient("mxfp4_matmul", out)
     u8, i32 = (torch.uint8,), (torch.int32,)
     _check(x, "x", u8, ndim=2)
     dev, gpu = x.device, x.get_device()
@@ -567,7 +568,8 @@ def moe_tokens(router: LmoeRouter, x, gate, up, down, bias=None, up_scales=None,
     all in one format.  shared_up [S or 2 S, D], shared_down [D, S]: an expert
     that every token takes with weight 1.  Widths are multiples of 64 (bf16) or
     128.  out_dtype: bf16 or fp32."""
-    _no_gradient("moe_tokens", x, gate, bias, up, down, shared_up, shared_down)
+    _no_gradient("moe_tokens", x, gate, bias, up, down, up_scales, down_scales, shared_up,
+                 shared_down, shared_up_scales, shared_down_scales)
     _check(x, "x", _TYPE, ndim=2, dense=False)
     T, D = x.shape
     gpu = x.get_device()
