@@ -122,16 +122,17 @@ def _check(t, what: str, dtypes, ndim=None, shape=None, device=None, dense: bool
             raise ValueError(f"{what}: on {t.device}, expected cuda:{device}")
 
 
-def _no_graph(where: str, *tensors) -> None:
+def _no_graph(where: str, *tensors, backward: bool = True) -> None:
     """Raise where autograd would expect ``where`` to record a gradient
-    (``_check`` speaks up for what is no tensor)."""
+    (``_check`` speaks up for what is no tensor); backward: whether there is a
+    call that computes it."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and getattr(t, "requires_grad", False):
+                use = f"from a torch.autograd.Function whose backward is {where}_backward, or "
                 raise ValueError(
                     f"{where}: an input requires a gradient, which this call does not record; "
-                    f"call it from a torch.autograd.Function whose backward is {where}_backward, "
-                    "or under torch.no_grad()")
+                    f"call it {use if backward else ''}under torch.no_grad()")
 
 
 def _type(t) -> int:
@@ -430,22 +431,13 @@ def fp8_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=torc
 # ---- microscaled 4-bit floating point ------------------------------------------
 
 
-def _no_gradient(where: str, *tensors) -> None:
-    """Raise where autograd would expect a gradient of ``where``, which has none."""
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and getattr(t, "requires_grad", False):
-                raise ValueError(f"{where}: an input requires a gradient, and this call has none; "
-                                 "call it under torch.no_grad()")
-
-
 def quantize_mxfp4_rows(x, stream=None):
     """(codes uint8 [T, 16 ceil(K / 32)], scales uint8 [T, ceil(K / 32)]) of
     activations x [T, K] (fp32 or bf16, rows may be strided) in MXFP4: E2M1
     elements, two to a byte, the first in the low half, and a scale
     2^(byte - 127) for each 32 of a row.  K is padded with zeros to a multiple
     of 32.  The rounding is quantize_mxfp4's."""
-    _no_gradient("quantize_mxfp4_rows", x)
+    _no_graph("quantize_mxfp4_rows", x, backward=False)
     _check(x, "x", _TYPE, ndim=2, dense=False)
     T, K = x.shape
     nb = (K + 31) // 32
@@ -496,7 +488,7 @@ def mxfp4_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=to
     ``offsets`` (int32 [G + 1], ascending) with w [G, N, K / 2]: rows
     offsets[g] .. offsets[g + 1] - 1 take matrix g; rows of no group are not
     written (pass ``out`` to keep what they hold).  out_dtype: bf16 or fp32."""
-    _no_gradient("mxfp4_matmul", out)
+    _no_graph("mxfp4_matmul", out, backward=False)
     u8, i32 = (torch.uint8,), (torch.int32,)
     _check(x, "x", u8, ndim=2)
     dev, gpu = x.device, x.get_device()
@@ -568,8 +560,8 @@ def moe_tokens(router: LmoeRouter, x, gate, up, down, bias=None, up_scales=None,
     all in one format.  shared_up [S or 2 S, D], shared_down [D, S]: an expert
     that every token takes with weight 1.  Widths are multiples of 64 (bf16) or
     128.  out_dtype: bf16 or fp32."""
-    _no_gradient("moe_tokens", x, gate, bias, up, down, up_scales, down_scales, shared_up,
-                 shared_down, shared_up_scales, shared_down_scales)
+    _no_graph("moe_tokens", x, gate, bias, up, down, up_scales, down_scales, shared_up, shared_down,
+              shared_up_scales, shared_down_scales, backward=False)
     _check(x, "x", _TYPE, ndim=2, dense=False)
     T, D = x.shape
     gpu = x.get_device()
