@@ -20,8 +20,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (EXPERTS_BF16, EXPERTS_FP8, EXPERTS_MXFP4, LMOE_OK, LmoeError, _ptr,
-               load_library)
+from . import (EXPERTS_BF16, EXPERTS_FP8, EXPERTS_MXFP4, LMOE_ERR_UNSUPPORTED, LMOE_OK, LmoeError,
+               _ptr, load_library)
 
 F32, BF16 = 0, 1                                    # lmoe_dtype
 SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1                 # lmoe_score
@@ -431,6 +431,12 @@ def fp8_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=torc
 # ---- microscaled 4-bit floating point ------------------------------------------
 
 
+def _int32(where: str, *sizes) -> None:
+    """Refuse sizes that the C ABI's 32-bit arguments would cut."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise LmoeError(LMOE_ERR_UNSUPPORTED, where)
+
+
 def quantize_mxfp4_rows(x, stream=None):
     """(codes uint8 [T, 16 ceil(K / 32)], scales uint8 [T, ceil(K / 32)]) of
     activations x [T, K] (fp32 or bf16, rows may be strided) in MXFP4: E2M1
@@ -440,6 +446,7 @@ def quantize_mxfp4_rows(x, stream=None):
     _no_graph("quantize_mxfp4_rows", x, backward=False)
     _check(x, "x", _TYPE, ndim=2, dense=False)
     T, K = x.shape
+    _int32("lmoe_quantize_mxfp4_rows", K)
     nb = (K + 31) // 32
     with _launch(x.get_device(), stream) as s:
         codes = torch.empty((T, 16 * nb), dtype=torch.uint8, device=x.device)
@@ -464,6 +471,7 @@ def dequantize_mxfp4(codes, scales, cols=None, out_dtype=torch.bfloat16, stream=
     cols = 32 * n if cols is None else int(cols)
     if not 32 * (n - 1) < cols <= 32 * n:
         raise ValueError(f"cols: {cols}, the codes hold {n} blocks of 32")
+    _int32("lmoe_dequantize_mxfp4", cols)
     if out_dtype not in _TYPE:
         raise TypeError(f"out_dtype: {out_dtype}, expected torch.bfloat16 or torch.float32")
     rows = 1
@@ -513,6 +521,7 @@ def mxfp4_matmul(x, x_scales, w, w_scales, offsets=None, rows=None, out_dtype=to
         _check(out, "out", _TYPE, shape=(M, N), device=gpu)
     elif out_dtype not in _TYPE:
         raise TypeError(f"out_dtype: {out_dtype}, expected torch.bfloat16 or torch.float32")
+    _int32("lmoe_mxfp4_matmul", M, X, N, K)
     lib = load_library()
     with _launch(gpu, stream) as s:
         y = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
@@ -593,6 +602,7 @@ def moe_tokens(router: LmoeRouter, x, gate, up, down, bias=None, up_scales=None,
         raise ValueError("shared scales without a shared expert")
     if out_dtype not in _TYPE:
         raise TypeError(f"out_dtype: {out_dtype}, expected torch.bfloat16 or torch.float32")
+    _int32("lmoe_moe_tokens", T, D, F, S)
     lib = load_library()
     with _launch(gpu, stream) as s:
         y = torch.empty((T, D), dtype=out_dtype, device=x.device)
