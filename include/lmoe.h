@@ -489,7 +489,8 @@ lmoe_status lmoe_mxfp4_matmul(const lmoe_mxfp4_matmul_args *a, void *workspace,
  * call gives the same bits.  Inputs should be finite: what is not stays in its token's row
  * of y (an infinite value may become NaN there).  Work-groups wait for each
  * other's hidden rows; should one ever wait about ten seconds in vain, the rows of
- * y that it works on are NaN. */
+ * y that it works on are NaN.  An MXFP4 scale byte of 255 makes what it takes
+ * part in NaN, an MXFP4 weight from 2^128 on infinite or NaN. */
 typedef enum { LMOE_ACT_RELU2 = 0, LMOE_ACT_SWIGLU = 1 } lmoe_activation;
 typedef struct {
   lmoe_router router;
