@@ -6,8 +6,8 @@ through the binding: the cases of ``perf/more_operators.py`` and further forms
 
 prints, for each case, the time of a pass among others (events around rounds of
 ``N`` passes on one stream, the shortest of the rounds) and what it has to move
-over that time.  Under a profiler ``--passes 10 --rounds 1`` gives ten launches a
-kernel and round.
+over that time (a sparse layer: with the experts that its tokens used).  Under a
+profiler ``--passes 10 --rounds 1`` gives ten launches a kernel and round.
 """
 
 import argparse
@@ -30,9 +30,38 @@ def further():
         out.append(P._grouped(f"experts_up_{t}", t, 22, 512, 5120, 2048, True))
         out.append(P._grouped(f"experts_down_{t}", t, 22, 512, 2048, 5120, False))
     for fmt in ("bf16", "fp8", "mxfp4"):
-        for t in (2, 4, 8, 16):
+        for t in (1, 2, 4, 8, 16):
             out.append(P._tokens(f"tokens_{t}_{fmt}", t, 512, 22, 2048, 5120, fmt=fmt, dtype="f32"))
+        # gated experts of the same width
+        out.append(P._tokens(f"gated_1_{fmt}", 1, 512, 22, 2048, 5120, fmt=fmt, act="swiglu"))
+        # a wide shared expert, and experts that all tokens take
+        for t, x in ((8, "bf16"), (8, "f32"), (16, "bf16"), (16, "f32")):
+            out.append(P._tokens(f"shared_{t}_{fmt}_{x}", t, 8, 2, 8192, 1024, fmt=fmt,
+                                 shared=10240, dtype=x))
+        for t in (8, 16):
+            out.append(P._tokens(f"crowded_{t}_{fmt}", t, 8, 8, 2048, 2048, fmt=fmt, act="swiglu",
+                                 score="softmax", scale=1.0))
+    # one expert takes every row
+    out.append(dict(P._grouped("experts_one_of_64", 80, 8, 64, 5120, 2048, True), crowd=True))
     return out
+
+
+def prepare(case):
+    st = P.prepare(case, 1)
+    if case.get("crowd"):
+        st["offsets"][1:] = st["offsets"][-1]
+    return st
+
+
+def moved(case, out):
+    """Bytes of a pass: a sparse layer's with the experts its tokens used."""
+    if case["op"] != "tokens":
+        return P.work(case)["bytes"]
+    alone = P.work(dict(case, tokens=1, top_k=1))["bytes"]
+    two = P.work(dict(case, tokens=1, top_k=2))["bytes"]
+    rest = P.work(dict(case, top_k=0))["bytes"]
+    used = len(set(out["experts"].flatten().tolist()))
+    return rest + used * (two - alone)
 
 
 def main():
@@ -46,8 +75,8 @@ def main():
     for case in P.listed() + further():
         if only and case["name"] not in only:
             continue
-        st = P.prepare(case, 1)
-        P.run(st)
+        st = prepare(case)
+        bytes_ = moved(case, P.run(st))
         torch.cuda.synchronize()
         best = float("inf")
         for _ in range(a.rounds):
@@ -58,9 +87,8 @@ def main():
             end.record()
             torch.cuda.synchronize()
             best = min(best, beg.elapsed_time(end) * 1e3 / a.passes)
-        w = P.work(case)
-        print(f"{case['name']:24s} {best:10.2f} us  {w['bytes'] / best / 1e3:8.0f} GB/s"
-              f"  {w['flops'] / best / 1e6:8.1f} TFLOP/s", flush=True)
+        print(f"{case['name']:24s} {best:10.2f} us  {bytes_ / best / 1e3:8.0f} GB/s"
+              f"  {P.work(case)['flops'] / best / 1e6:8.1f} TFLOP/s", flush=True)
         del st
         torch.cuda.empty_cache()
 

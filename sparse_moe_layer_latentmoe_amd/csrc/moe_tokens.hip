@@ -15,8 +15,8 @@
 // items: first blocks of rows of the up projections, expert by expert, then of the
 // down projections.
 //
-// Measured, the second kernel: 22 experts of 2048 x 5120 for one token, bf16 157 us
-// (923 MB, 5.9 TB/s), MXFP4 75 (245 MB, 3.3 TB/s); 97 experts for six tokens, FP8 342
+// Measured, the second kernel: 22 experts of 2048 x 5120 for one token, bf16 162 us
+// (923 MB, 5.7 TB/s), MXFP4 74 (245 MB, 3.3 TB/s); 97 experts for six tokens, FP8 340
 // (2035 MB, 6.0 TB/s).  A card that only reads reaches 7.0.  What small layers add to
 // that is latency, one thing after the other: 5 to 9 us until the first weights are
 // asked for, 2 to 4 for the first lines and rows, 3 to 6 for an expert's hidden rows
@@ -836,9 +836,10 @@ hipError_t moe_tokens(const MoeTokens& m, void* workspace, hipStream_t s) {
   const int red = 2 * kThreads * 16, lists = m.x_bf16 && m.T > kTurn ? 18 * P + 288 : 12 * P + 192;
   // One work-group a CU or two.  One starts sooner (each routes and stages for itself),
   // two keep more on the way.  512 experts top-22 of 2048 x 5120, one against two: MXFP4 T = 1
-  // (245 MB) 76 us and 90, T = 2 (480 MB) 128 and 143, T = 4 (920 MB) 208 and 202; FP8 T = 2
-  // (900 MB) 176 and 166, T = 6 378 and 349; bf16 T = 1 (920 MB) 161 and 165, T = 2 291 and
-  // 276, T = 4 572 and 519.  Many tokens, 128 experts top-8 (T = 13, MXFP4, 168 MB): 74 and 68.
+  // (245 MB) 78 us and 91, T = 2 (460 MB) 130 and 146, T = 4 (840 MB) 210 and 208; FP8 T = 1 105
+  // and 112, T = 2 (860 MB) 184 and 180, T = 6 405 and 364; bf16 T = 1 (920 MB) 162 and 167, T =
+  // 2 308 and 294, T = 4 625 and 583.  Many tokens, 128 experts top-8 (T = 13, MXFP4, 168 MB): 79
+  // and 71.
   // The shared expert is not counted: of one of 1.07 GB (bf16, 8192 x 32768) T = 2 takes
   // 291 us and 283, T = 4 323 and 340.
   const double mb = 1e-6 * (P < E ? P : E) * m.D * m.F * (m.gated ? 3 : 2) *

@@ -9,7 +9,7 @@
 // and add into fp32.  Products of codes are multiples of 1/4 up to 36, so a
 // block's sum is exact; blocks of different scales and the running sum are
 // added to about 2^-23 of the sum of the magnitudes (measured: exact where all
-// scales are equal, at worst 2^-22.3 with scales spread over 2^24), which is
+// scales are equal, at worst 2^-22.3 with scales from 2^-20 to 2^20), which is
 // an fp32 sum.  So results of either type take the same instructions.
 // Weights are the A operand and tokens the B operand: a lane's results are
 // consecutive columns of one token.
@@ -502,9 +502,9 @@ __global__ __launch_bounds__(NW * 64) void mx4_lines_kernel(Mx4Gemm p, const Til
 // Scales come two lines at a time (16 bytes of a row), half of the tile's rows with
 // each step.
 //
-// Bound by the matrix instructions at the clock that the card's power limit leaves them:
-// 8192 x 10240 x 8192 in 313 us (4.4 PFLOP/s; they are busy in three quarters of a
-// step's cycles, at 1.4 to 1.5 GHz), and by what a tile costs beside its steps, about 11 us (start
+// Bound by the matrix instructions at the clock that the card runs them at:
+// 8192 x 10240 x 8192 in 309 to 317 us (4.4 PFLOP/s; they are busy in 65% of the
+// cycles, at 1.6 GHz), and by what a tile costs beside its steps, about 11 us (start
 // and scales 3 to 4, first lines 3, the results' way out 4 to 6).  180224 rows over 512
 // groups of 2048 x 5120: 1.33 to 1.43 ms (2.7 PFLOP/s).  Four waves with half the LDS reads,
 // twice the registers: the same.  Tiles of half as many columns, two work-groups a CU: 2%
